@@ -18,8 +18,6 @@ import numpy as np
 import torch
 
 own = False
-if own:
-    import invariant_lm_head_gb300 as lmh
 
 BLOCK = 128
 E4M3_MAX = 448.0
@@ -202,6 +200,8 @@ def _plain_sample(logits, u, temperature, top_k, top_p, min_p):
 
 def run(state):
     op = state["op"]
+    if own:
+        import invariant_lm_head_gb300 as lmh
     if op == "quantize":
         if own:
             return lmh.lmhead_quantize_fp8(state["x"], state["block_rows"])
