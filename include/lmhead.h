@@ -421,6 +421,88 @@ int lmhead_logprob_fwd_noalloc(const uint16_t* hidden, const uint16_t* weight,
                                float inv_temperature, float* out_logprob, float* out_entropy,
                                float* out_lse, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------ fp8 head
+ *
+ * What a server needs beside the log-probs: a head whose weight is held in 8
+ * bits, and a sampler. lmhead_quantize_fp8 makes the operands,
+ * lmhead_logits_fp8 the bf16 logits, lmhead_sample the tokens and their
+ * log-probs. e4m3 values are passed as uint8_t bit patterns. As everywhere in
+ * this library a row's results do not depend, bit for bit, on the batch it
+ * arrives in. These are serving operators: they have no backward.
+ */
+
+/*
+ * Block quantisation of a bf16 matrix to e4m3. For each block of block_rows x
+ * 128 elements (the last ones are shorter), with a = max(max |x|, 2^-60):
+ *   scale = a / 448, rounded to fp32 once
+ *   q     = x * 448 / a, rounded to e4m3 once (nearest, ties to even)
+ * so q * scale is the block's best e4m3 approximation. A block that holds a
+ * NaN or an infinity gets that as its scale and NaN in every q.
+ *   x       bf16 [rows, cols], 16-byte aligned, rows ld elements apart (ld >=
+ *           cols, ld % 8 == 0); cols % 16 == 0
+ *   block_rows  1 (activations: one scale per row and 128 columns) or 128 (a
+ *           weight: one scale per 128 x 128 tile)
+ *   q       e4m3 [rows, cols], contiguous, 16-byte aligned
+ *   scale   f32 [ceil(rows / block_rows), ceil(cols / 128)]
+ * rows == 0 is a no-op.
+ */
+int lmhead_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int block_rows,
+                        uint8_t* q, float* scale, struct CUstream_st* stream);
+
+/*
+ * bf16 logits of an fp8 head: with K blocks b of 128 hidden columns,
+ *   logits[t, v] = sum_b (hidden_scale[t, b] * weight_scale[v / 128, b])
+ *                        * sum_{k in b} hidden_q[t, k] * weight_q[v, k]
+ * fp32 throughout (products in tensor cores, blocks added in ascending order),
+ * rounded to bf16 once.
+ *   hidden_q      e4m3 [T, H], 16-byte aligned, H % 16 == 0
+ *   hidden_scale  f32 [T, ceil(H / 128)]
+ *   weight_q      e4m3 [V, H], 16-byte aligned
+ *   weight_scale  f32 [ceil(V / 128), ceil(H / 128)]
+ *   logits        bf16 [T, V], rows ld_logits elements apart (ld_logits >= V),
+ *                 2-byte aligned; 16-byte aligned rows are written faster
+ * T == 0 is a no-op.
+ */
+int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_scale, const uint8_t* weight_q,
+                      const float* weight_scale, int64_t T, int64_t H, int64_t V,
+                      uint16_t* logits, int64_t ld_logits, struct CUstream_st* stream);
+
+/*
+ * One token per row of bf16 logits x, from a given uniform number. With z = x /
+ * temperature (fp32 division) and weights w = exp(z - max z), the tokens in
+ * descending order of x, equal ones by index, are cut to
+ *   the first top_k                                            (0: off)
+ *   then the shortest prefix whose mass is >= top_p of theirs  (>= 1: off)
+ *   then those with w >= min_p, min_p of the likeliest         (0: off)
+ * and the token is the first whose running mass exceeds uniform times the kept
+ * mass. temperature 0 returns the likeliest token (the lowest index of equal
+ * ones) and ignores the rest. out_logprob is the token's log-prob in the whole
+ * distribution at that temperature (at 1 for temperature 0), before any cut:
+ * the sampler formula's value, as logprob_from_logits_div gives it.
+ *   logits   bf16 [T, V], rows ld_logits elements apart, 2-byte aligned
+ *   temperature, top_k, top_p, min_p  for every row, in [0, inf), [0, ..),
+ *            (0, 1], [0, 1]; each can be replaced by a device array with one
+ *            value per row (f32, int32, f32, f32; NULL: none). The host
+ *            cannot check device values: a row whose temperature is negative
+ *            or not finite, top_k < 0, top_p <= 0, min_p > 1, any of them NaN,
+ *            or uniform outside [0, 1] gets token -1 and log-prob NaN
+ *            (top_p >= 1 and min_p <= 0 turn those cuts off)
+ *   uniform  f32 [T] in [0, 1]; 1 takes the last kept token
+ *   out_token    int32 [T]
+ *   out_logprob  f32 [T] or NULL
+ * NaN and -inf logits are never drawn; a row of nothing else gets token -1 and
+ * log-prob 0 (what the log-prob entry points give for a label outside the
+ * vocabulary). Logits equal to the largest weigh 1 even where z overflows.
+ * Weights are held in units of 2^-44 of the largest (V <= 2^19; 2^-(63 -
+ * ceil(log2 V)) above) and summed as integers, so neither the order of sums
+ * nor the batch can change a token. T == 0 is a no-op.
+ */
+int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logits,
+                  float temperature, const float* row_temperature, int32_t top_k,
+                  const int32_t* row_top_k, float top_p, const float* row_top_p, float min_p,
+                  const float* row_min_p, const float* uniform, int32_t* out_token,
+                  float* out_logprob, struct CUstream_st* stream);
+
 /* ---------------------------------------------------------------- diagnostics */
 
 /* Message of the calling thread's last error ("" if none). */

@@ -79,6 +79,10 @@ SIGNATURES = {
     "lmhead_logprob_bwd_shard": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _I64, _F, _P, _P,
                                   _P, ctypes.c_size_t, _P], ctypes.c_int),
     "lmhead_sum_ranks_bf16": ([_P, _I64, _I64, _P, _P], ctypes.c_int),
+    "lmhead_quantize_fp8": ([_P, _I64, _I64, _I64, ctypes.c_int, _P, _P, _P], ctypes.c_int),
+    "lmhead_logits_fp8": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
+    "lmhead_sample": ([_P, _I64, _I64, _I64, _F, _P, ctypes.c_int32, _P, _F, _P, _F, _P, _P, _P, _P,
+                       _P], ctypes.c_int),
 }
 
 _lib_handle: Optional[ctypes.CDLL] = None
@@ -508,6 +512,137 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
         _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _stream_ptr(stream))
     _check("lmhead_logprob_merge", rc)
     return out_logprob, out_entropy, out_lse
+
+
+def _need_rows(t, name: str, dtype, device) -> int:
+    """A matrix whose rows are contiguous, at any row stride; returns the stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
+    if t.shape[0] <= 1:
+        return max(t.shape[1], t.stride(0))
+    if t.stride(0) < t.shape[1]:
+        raise ValueError(f"{name} must have rows that do not overlap")
+    return t.stride(0)
+
+
+def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, stream=None):
+    """Block quantisation of a bf16 matrix to e4m3 (see include/lmhead.h).
+
+    x bf16 [rows, cols] (rows may be strided), blocks of block_rows (1 or 128)
+    x 128. Returns (q float8_e4m3fn [rows, cols], scale f32 [ceil(rows /
+    block_rows), ceil(cols / 128)]).
+    """
+    torch = _torch()
+    dev = x.device
+    ld = _need_rows(x, "x", torch.bfloat16, dev)
+    rows, cols = x.shape
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    if rows <= 1:  # one row has no stride to respect
+        ld = -(-cols // 8) * 8
+    shape = (-(-rows // block_rows), -(-cols // 128))
+    if out is None:
+        out = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=dev)
+    if out_scale is None:
+        out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float8_e4m3fn, dev, 2)
+    _need(out_scale, "out_scale", torch.float32, dev, 2)
+    if tuple(out.shape) != (rows, cols) or tuple(out_scale.shape) != shape:
+        raise ValueError("shape mismatch between x, out and out_scale")
+    rc = library().lmhead_quantize_fp8(_ptr(x), rows, cols, ld, int(block_rows), _ptr(out),
+                                       _ptr(out_scale), _stream_ptr(stream))
+    _check("lmhead_quantize_fp8", rc)
+    return out, out_scale
+
+
+def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_logits=None,
+                      stream=None):
+    """bf16 logits [T, V] of block-scaled e4m3 operands (see include/lmhead.h).
+
+    hidden_q [T, H] with hidden_scale [T, ceil(H / 128)], weight_q [V, H] with
+    weight_scale [ceil(V / 128), ceil(H / 128)], as lmhead_quantize_fp8 returns
+    them with block_rows 1 and 128. out_logits may have strided rows.
+    """
+    torch = _torch()
+    dev = hidden_q.device
+    _need(hidden_q, "hidden_q", torch.float8_e4m3fn, dev, 2)
+    _need(weight_q, "weight_q", torch.float8_e4m3fn, dev, 2)
+    _need(hidden_scale, "hidden_scale", torch.float32, dev, 2)
+    _need(weight_scale, "weight_scale", torch.float32, dev, 2)
+    T, H = hidden_q.shape
+    V = weight_q.shape[0]
+    kb = -(-H // 128)
+    if weight_q.shape[1] != H:
+        raise ValueError("shape mismatch between hidden_q and weight_q")
+    if tuple(hidden_scale.shape) != (T, kb) or tuple(weight_scale.shape) != (-(-V // 128), kb):
+        raise ValueError("hidden_scale must be [T, ceil(H / 128)] and weight_scale "
+                         "[ceil(V / 128), ceil(H / 128)]")
+    if out_logits is None:
+        out_logits = torch.empty(T, V, dtype=torch.bfloat16, device=dev)
+    ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev)
+    if tuple(out_logits.shape) != (T, V):
+        raise ValueError(f"out_logits must be [{T}, {V}]")
+    rc = library().lmhead_logits_fp8(_ptr(hidden_q), _ptr(hidden_scale), _ptr(weight_q),
+                                     _ptr(weight_scale), T, H, V, _ptr(out_logits), ld,
+                                     _stream_ptr(stream))
+    _check("lmhead_logits_fp8", rc)
+    return out_logits
+
+
+def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0,
+                  out_token=None, out_logprob=None, want_logprob: bool = True, stream=None):
+    """One token per row of bf16 logits from a given uniform number (see include/lmhead.h).
+
+    logits bf16 [T, V] (rows may be strided), uniform f32 [T] in [0, 1].
+    temperature (0: greedy), top_k (0: off), top_p (1: off) and min_p (0: off)
+    are numbers, or tensors [T] (f32; top_k int32) with one value per row.
+    Returns (token int32 [T], logprob f32 [T] or None).
+    """
+    torch = _torch()
+    dev = logits.device
+    ld = _need_rows(logits, "logits", torch.bfloat16, dev)
+    T, V = logits.shape
+    _need(uniform, "uniform", torch.float32, dev, 1)
+    if uniform.shape[0] != T:
+        raise ValueError("uniform must have one value per row")
+
+    def setting(v, name, dtype):
+        if not isinstance(v, torch.Tensor):
+            return v, None
+        _need(v, name, dtype, dev, 1)
+        if v.shape[0] != T:
+            raise ValueError(f"{name} must have one value per row")
+        return 1, v
+
+    t, row_t = setting(temperature, "temperature", torch.float32)
+    k, row_k = setting(top_k, "top_k", torch.int32)
+    p, row_p = setting(top_p, "top_p", torch.float32)
+    m, row_m = setting(min_p, "min_p", torch.float32)
+    k = int(k)
+    if not 0 <= k <= 0x7fffffff:
+        raise ValueError("top_k must be in [0, 2^31)")
+    if out_token is None:
+        out_token = torch.empty(T, dtype=torch.int32, device=dev)
+    if out_logprob is None and want_logprob:
+        out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+    for o, name, dtype in ((out_token, "out_token", torch.int32),
+                           (out_logprob, "out_logprob", torch.float32)):
+        if o is not None:
+            _need(o, name, dtype, dev, 1)
+            if o.shape[0] != T:
+                raise ValueError(f"{name} must have one value per row")
+    rc = library().lmhead_sample(_ptr(logits), T, V, ld, float(t), _ptr(row_t), k, _ptr(row_k),
+                                 float(p), _ptr(row_p), float(m), _ptr(row_m), _ptr(uniform),
+                                 _ptr(out_token), _ptr(out_logprob), _stream_ptr(stream))
+    _check("lmhead_sample", rc)
+    return out_token, out_logprob
 
 
 _LOGPROB_FN = None

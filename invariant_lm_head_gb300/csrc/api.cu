@@ -125,16 +125,17 @@ int device_info(DeviceInfo** out) {
   return LMH_OK;
 }
 
-// 2-D bf16 tensor map: `inner` contiguous elements per row, `outer` rows,
-// rows `row_bytes` apart; box `box_inner` x `box_outer` with 128-byte swizzle.
-// Out-of-range elements of a box read as zero.
+// 2-D tensor map (bf16 unless `type` says otherwise): `inner` contiguous
+// elements per row, `outer` rows, rows `row_bytes` apart; box `box_inner` x
+// `box_outer` with 128-byte swizzle. Out-of-range elements of a box read as zero.
 int make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
-              uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+              uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer,
+              CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   cuuint64_t dims[2] = {inner, outer};
   cuuint64_t strides[1] = {row_bytes};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+  CUresult r = g_encode(map, type, 2, const_cast<void*>(base), dims,
                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -289,7 +290,8 @@ int launch_status(cudaError_t e, const char* what) {
 const char* const kKindNames[lmh::K_COUNT] = {
     "fused_fwd_gemm", "fwd_merge",   "dlogits_gemm",  "grad_hidden_gemm",  "grad_weight_gemm",
     "logits_rowwise", "engine_gemm", "selftest_wait", "logits_rowwise_div",
-    "hidden_transpose", "sum_parts_bf16", "grad_hidden_sum"};
+    "hidden_transpose", "sum_parts_bf16", "grad_hidden_sum",   "quantize_fp8",
+    "logits_fp8_gemm", "sample"};
 
 struct TimingRec {
   int kind;
@@ -787,6 +789,12 @@ int api_noalloc_scratch(void** scratch) {
 int api_make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
   return make_tmap(map, base, inner, outer, row_bytes, box_inner, box_outer);
+}
+
+int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return make_tmap(map, base, inner, outer, row_bytes, box_inner, box_outer,
+                   CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 }  // namespace lmh
 

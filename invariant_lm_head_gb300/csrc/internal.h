@@ -129,6 +129,9 @@ enum KernelKind : int {
   K_HIDDEN_TRANSPOSE,
   K_SUM_PARTS,
   K_DHIDDEN_SUM,
+  K_QUANTIZE_FP8,
+  K_LOGITS_FP8,
+  K_SAMPLE,
   K_COUNT
 };
 
@@ -161,6 +164,9 @@ int api_noalloc_scratch(void** scratch);
 int noalloc_scratch_lookup(void** scratch);
 int api_make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// The same for 8-bit elements (fp8 operands), 128-byte swizzle.
+int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                     uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
 
 size_t gemm_smem_bytes();
 // Which contractions run on CTA pairs (launches with two or more 128-row m
