@@ -796,6 +796,11 @@ int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_
   return make_tmap(map, base, inner, outer, row_bytes, box_inner, box_outer,
                    CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
+
+int api_make_out_tmap_bf16(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows,
+                           uint64_t row_bytes) {
+  return make_out_tmap(map, base, cols, rows, row_bytes, false);
+}
 }  // namespace lmh
 
 extern "C" {

@@ -21,6 +21,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -169,31 +170,38 @@ __global__ void __launch_bounds__(kQuantThreads)
 }
 
 // ------------------------------------------------------------ fp8 logits
-constexpr int kFM = 128;               // token rows of a tile
-constexpr int kFN = 128;               // vocabulary columns of a tile
+constexpr int kFM = 128;               // token rows of one CTA's tile
+constexpr int kFMaxN = 256;            // most vocabulary columns of a tile
 constexpr int kFK = kQBlock;           // one K block per ring stage: 128 bytes per row
-constexpr int kFAccs = 512 / kFN;      // accumulators in TMEM
+constexpr int kFChunk = 16;            // columns read from TMEM at once
+constexpr int kFBox = 32;              // columns of an output box; tile widths are multiples
+constexpr int kFGroups = 2;            // promote groups of four warps; a warp reads its lane quarter
+constexpr int kFMaxAccs = 4;
 constexpr int kFMaxStages = 12;
-constexpr int kFRingBytes = 208 * 1024;
-constexpr int kFBBytes = kFN * kFK;
-constexpr int kFPromoteWarps = 8;      // two groups of four: a warp reads its quarter of the lanes
-constexpr int kFThreads = 64 + 32 * kFPromoteWarps;
-constexpr int kFCols = kFN / 2;        // columns of one promote group
-constexpr int kFStageRow = 17;         // 32-bit words per staged row of 32 bf16 (odd: no conflicts)
-constexpr int kFStagingBytes = kFPromoteWarps * 32 * kFStageRow * 4;
-constexpr int kFBarBytes = 1024;
-constexpr int kFSmemBytes = kFRingBytes + kFStagingBytes + kFBarBytes + 1024;
-static_assert(kFSmemBytes <= 232448, "exceeds the 227 KB shared-memory limit per CTA");
+constexpr int kFPromoteWarps = 4 * kFGroups;
+constexpr int kFThreads = 128 + 32 * kFPromoteWarps;  // warps 0-3: load, issue, two idle
+// Registers: 384 threads start with 168 each. The first warpgroup gives most
+// of its own back and the promote groups take 232 for their 128 sums and two
+// chunks in flight: 128 * 40 + 256 * 232 = 384 * 168.
+constexpr int kFRegsFew = 40, kFRegsMany = 232;
+static_assert(128 * kFRegsFew + 32 * kFPromoteWarps * kFRegsMany <= kFThreads * 168, "registers");
+constexpr int kFStagingWarp = 4096;    // output staging of a warp: two 32 x 32 bf16 boxes
+constexpr int kFStagingBytes = kFPromoteWarps * kFStagingWarp;
+constexpr int kFBarBytes = 512;
+constexpr int kFSmemBytes = 232448;    // all that a CTA can have
+constexpr int kFRingBytes = (kFSmemBytes - 1024 - kFBarBytes - kFStagingBytes) / 1024 * 1024;
 
 struct Fp8Params {
   int T, V, KB;          // rows, vocabulary, K blocks
+  int tile_n;            // columns of a tile
   int n_m, n_n, n_units; // tiles
+  int group_m;           // m tiles that share a vocabulary tile in the raster
   int a_rows;            // rows of an A box (T <= 128: T rounded up to 8)
   const float* hs;       // [T][KB]
   const float* ws;       // [ceil(V / 128)][KB]
   uint16_t* out;
   int64_t ld;
-  int vec;               // 16-byte stores are aligned
+  int tma_out;           // rows on 16-byte boundaries: the output leaves by TMA
   unsigned* status;
 };
 
@@ -210,7 +218,7 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
 
 // Instruction descriptor for kind::f8f6f4: D f32 (bit 4), A and B e4m3 (format
 // 0 in bits 7 and 10), both K-major, [17,23) N >> 3, [24,29) M >> 4.
-constexpr uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
+__device__ __forceinline__ uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
@@ -219,41 +227,108 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Warp 0 loads, warp 1 issues the MMAs, warps 2-9 scale and add each K block's
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Predicated stores: divergent branches around single stores cost more than they.
+__device__ __forceinline__ void st_global_u32_if(uint16_t* at, uint32_t v, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at),
+               "r"(v), "r"(static_cast<int>(on))
+               : "memory");
+}
+__device__ __forceinline__ void st_global_u16_if(uint16_t* at, uint32_t v, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(at),
+               "h"(static_cast<uint16_t>(v)), "r"(static_cast<int>(on))
+               : "memory");
+}
+// One row's 32 columns as bf16 into a 32 x 32 box with 64-byte swizzle (16-byte
+// chunk j of row r at j ^ ((r / 2) % 4)), as the TMA store reads it.
+__device__ __forceinline__ void stage_box_row(uint32_t buf, int r, const float* v) {
+  const uint32_t row = buf + static_cast<uint32_t>(r) * 64u;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                     row + ((static_cast<uint32_t>(j) ^ ((r >> 1) & 3)) << 4)),
+                 "r"(bf16x2_of(v[8 * j], v[8 * j + 1])), "r"(bf16x2_of(v[8 * j + 2], v[8 * j + 3])),
+                 "r"(bf16x2_of(v[8 * j + 4], v[8 * j + 5])),
+                 "r"(bf16x2_of(v[8 * j + 6], v[8 * j + 7]))
+                 : "memory");
+}
+
+// Unit u -> (m tile, n tile): groups of group_m m tiles, vocabulary tiles
+// inside, so that the CTAs at work share a vocabulary tile in L2.
+__device__ __forceinline__ void fp8_unit(const Fp8Params& p, int u, int& m, int& n) {
+  const int per_group = p.group_m * p.n_n;
+  const int g = u / per_group;
+  const int first = g * p.group_m;
+  const int gm = min(p.group_m, p.n_m - first);
+  const int r = u - g * per_group;
+  n = r / gm;
+  m = first + (r - n * gm);
+}
+
+// Warp 0 loads, warp 1 issues the MMAs, the others scale and add each K block's
 // accumulator into registers and store the finished tile. Tokens are the MMA's
 // rows (one TMEM lane each, so a thread's hidden scale is one number), the
-// vocabulary its columns (128 of them share one weight scale). A short batch
-// loads only its own rows: the rest of the 128-row A operand reads whatever the
-// stage holds next (its own B rows), which only feeds lanes that no one reads.
+// vocabulary its columns (128 of them share one weight scale).
+//
+// A short batch loads only its own rows: the rest of the 128-row A operand reads
+// whatever the stage holds next (its own vocabulary rows), which only feeds
+// lanes that no one reads.
+//
+// What bounds it. A short batch reads the weight once and is bound by that: 82.6
+// us at T=1 H=3584 V=152064, 6.6 TB/s; 26.0 us at T=64 H=4096 V=32000, 5.2 TB/s
+// (one wave: its start and end show). A long one is bound by the promote groups:
+// a K block's 128 x 256 accumulator is read out of TMEM beside the MMAs, which
+// use TMEM as well (about 500 cycles, against 190 with no MMA running), scaled,
+// added and handed back, about 1100 cycles in all for 512 of MMAs. 999 us at
+// T=2048 H=3584 V=152064, 2.24 PFLOP/s (the same loop with one hand-over a tile
+// runs at 3.15, but sums unscaled blocks).
+// Tried and slower at T=2048 H=3584 V=38912 (253 us): CTA pairs sharing 256 x 256
+// tiles (276 us: half the weight traffic, but the hand-over crosses two CTAs);
+// four promote groups of 64 columns (293 us); halves of 128 columns with their
+// own MMAs and buffers (336 us: the MMAs read the A tile twice).
 __global__ void __launch_bounds__(kFThreads, 1)
     logits_fp8_kernel(const __grid_constant__ CUtensorMap tmA,
-                      const __grid_constant__ CUtensorMap tmB, const Fp8Params p) {
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t base = smem_u32(smem);
-  uint32_t* staging = reinterpret_cast<uint32_t*>(smem + kFRingBytes);
+  const uint32_t staging = base + kFRingBytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kFRingBytes + kFStagingBytes);
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kFMaxStages + s); };
   auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kFMaxStages + a); };
-  auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kFMaxStages + kFAccs + a); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kFMaxStages + 2 * kFAccs);
+  auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kFMaxStages + kFMaxAccs + a); };
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kFMaxStages + 2 * kFMaxAccs);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * (2 * kFMaxStages + 2 * kFMaxAccs) + 16 <= kFBarBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * kFK;
-  const uint32_t stage_bytes = a_bytes + kFBBytes;
-  const uint32_t n_st = min(static_cast<uint32_t>(kFMaxStages), kFRingBytes / stage_bytes);
+  const uint32_t stage_bytes = a_bytes + static_cast<uint32_t>(p.tile_n) * kFK;
+  // the last stage's A operand may reach 128 rows on, past a short stage
+  const uint32_t n_st = min(static_cast<uint32_t>(kFMaxStages),
+                            (kFRingBytes - (kFM * kFK - min(stage_bytes, kFM * kFK))) / stage_bytes);
+  // accumulators side by side in the 512 columns
+  const uint32_t acc_cols = p.tile_n > 128 ? 256u : 128u;
+  const uint32_t n_acc = 512u / acc_cols;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kFMaxStages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
     }
-    for (int a = 0; a < kFAccs; ++a) {
+    for (int a = 0; a < kFMaxAccs; ++a) {
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), kFPromoteWarps);
     }
@@ -261,6 +336,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    if (p.tma_out) tma_prefetch_desc(&tmC);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -271,13 +347,15 @@ __global__ void __launch_bounds__(kFThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFRegsFew));
+    if (warp == 0 && lane == 0) {
       uint32_t stage = 0, phase = 0;
       long long issued = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        const int n_tile = u / p.n_m, m_tile = u - n_tile * p.n_m;
+        int m, n;
+        fp8_unit(p, u, m, n);
         for (int kb = 0; kb < p.KB; ++kb) {
           if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
             ok = false;
@@ -285,8 +363,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
           const uint32_t sA = base + stage * stage_bytes;
           mbar_arrive_expect_tx(full_bar(stage), stage_bytes);
-          tma_load_2d(sA + a_bytes, &tmB, full_bar(stage), kb * kFK, n_tile * kFN);
-          tma_load_2d(sA, &tmA, full_bar(stage), kb * kFK, m_tile * kFM);
+          tma_load_2d(sA + a_bytes, &tmB, full_bar(stage), kb * kFK, n * p.tile_n);
+          tma_load_2d(sA, &tmA, full_bar(stage), kb * kFK, m * kFM);
           ++issued;
           if (++stage == n_st) {
             stage = 0;
@@ -302,9 +380,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
                     static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
       }
     }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_e4m3_f32(kFM, kFN);
+    if (warp == 1 && lane == 0) {
+      const uint32_t idesc = idesc_e4m3_f32(kFM, static_cast<uint32_t>(p.tile_n));
       uint32_t stage = 0, phase = 0, acc = 0, aphase = 0;
       bool ok = true;
       for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
@@ -319,14 +396,14 @@ __global__ void __launch_bounds__(kFThreads, 1)
           const uint64_t ad = sw128_kmajor_desc(sA), bd = sw128_kmajor_desc(sA + a_bytes);
 #pragma unroll
           for (int k = 0; k < kFK / 32; ++k)  // 32 bytes on in each 128-byte row
-            tc_mma_e4m3(tmem + acc * kFN, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+            tc_mma_e4m3(tmem + acc * acc_cols, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
           tc_commit(empty_bar(stage));
           tc_commit(tfull_bar(acc));
           if (++stage == n_st) {
             stage = 0;
             phase ^= 1u;
           }
-          if (++acc == kFAccs) {
+          if (++acc == n_acc) {
             acc = 0;
             aphase ^= 1u;
           }
@@ -334,88 +411,156 @@ __global__ void __launch_bounds__(kFThreads, 1)
       }
     }
   } else {
-    const int pw = warp - 2;
-    const int grp = pw >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
+    const int pw = warp - 4;
     const int lanes0 = 32 * (warp & 3);  // the TMEM lanes this warp may read
-    uint32_t* stg = staging + pw * 32 * kFStageRow;
-    uint32_t acc = 0, aphase = 0;
-    bool ok = true;
-    for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-      const int n_tile = u / p.n_m, m_tile = u - n_tile * p.n_m;
-      const int row0 = m_tile * kFM + lanes0;
+    const uint32_t lane_addr = static_cast<uint32_t>(lanes0) << 16;
+    const uint32_t stg = staging + pw * kFStagingWarp;
+    // this group's part of a tile's columns: whole output boxes, in chunks
+    const int boxes = p.tile_n / kFBox;
+    const int per = (boxes + kFGroups - 1) / kFGroups;
+    const int box0 = (pw >> 2) * per;
+    const int chunk0 = box0 * (kFBox / kFChunk);
+    const int my = max(0, min(per, boxes - box0)) * (kFBox / kFChunk);
+    const int last_vb = (p.V - 1) / kQBlock;
+    uint32_t acc = 0, aphase = 0, obuf = 0;
+    // One tile, kCh chunks of it this group's: branch-free inside a K block (with
+    // a test at each chunk the reads and sums of a block took 870 cycles).
+    auto tile = [&](auto chunk_count, int u) -> bool {
+      constexpr int kCh = decltype(chunk_count)::value;
+      int m, n;
+      fp8_unit(p, u, m, n);
+      const int row0 = m * kFM + lanes0;
       const int row = row0 + lane;
       const bool warp_on = row0 < p.T;
+      const int64_t col0 = static_cast<int64_t>(n) * p.tile_n + chunk0 * kFChunk;
+      // the group's columns (at most 128) meet at most two weight scales:
+      // chunks below `cut` take the first
+      const int vb0 = static_cast<int>(col0 / kQBlock);
+      const int cut = static_cast<int>((static_cast<int64_t>(vb0 + 1) * kQBlock - col0) / kFChunk);
       const float* hs = p.hs + static_cast<int64_t>(min(row, p.T - 1)) * p.KB;
-      const float* ws = p.ws + static_cast<int64_t>(n_tile) * p.KB;
-      float sum[kFCols];
+      const float* ws0 = p.ws + static_cast<int64_t>(min(vb0, last_vb)) * p.KB;
+      const float* ws1 = p.ws + static_cast<int64_t>(min(vb0 + 1, last_vb)) * p.KB;
+      float sum[kCh > 0 ? kCh * kFChunk : 1];
 #pragma unroll
-      for (int i = 0; i < kFCols; ++i) sum[i] = 0.f;
+      for (int i = 0; i < kCh * kFChunk; ++i) sum[i] = 0.f;
+      float h = hs[0], w0 = ws0[0], w1 = ws1[0];
       for (int kb = 0; kb < p.KB; ++kb) {
-        const float s = __fmul_rn(hs[kb], ws[kb]);
-        ok = mbar_wait(tfull_bar(acc), aphase, abort_flag, p.status);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        const float s0 = __fmul_rn(h, w0), s1 = __fmul_rn(h, w1);
+        if (kb + 1 < p.KB) {  // the next block's scales arrive during this one
+          ++hs;
+          ++ws0;
+          ++ws1;
+        }
+        h = *hs;
+        w0 = *ws0;
+        w1 = *ws1;
+        const bool ready = mbar_wait(tfull_bar(acc), aphase, abort_flag, p.status);
+        if (!__all_sync(0xffffffffu, ready)) return false;
         tc_fence_after();
         if (warp_on) {
+          // the next chunk's load is under way while one chunk is added
+          const uint32_t src = tmem + lane_addr + acc * acc_cols + chunk0 * kFChunk;
+          uint32_t d[2][kFChunk];
+          if (kCh > 0) tmem_ld16_issue(src, d[0]);
 #pragma unroll
-          for (int c = 0; c < kFCols / 32; ++c) {
-            uint32_t d[32];
-            tmem_ld32_issue(tmem + (static_cast<uint32_t>(lanes0) << 16) + acc * kFN + grp * kFCols +
-                                c * 32,
-                            d);
-            tmem_ld_wait(d);
+          for (int c = 0; c < kCh; ++c) {
+            tmem_ld_wait(d[c & 1]);
+            if (c + 1 < kCh) tmem_ld16_issue(src + (c + 1) * kFChunk, d[(c + 1) & 1]);
+            const float s = c < cut ? s0 : s1;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              sum[c * 32 + i] = __fmaf_rn(__uint_as_float(d[i]), s, sum[c * 32 + i]);
+            for (int i = 0; i < kFChunk; i += 2) {
+              float* o = sum + c * kFChunk + i;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(d[c & 1][i]), __uint_as_float(d[c & 1][i + 1])),
+                               f2_pack(s, s), f2_pack(o[0], o[1])),
+                        o[0], o[1]);
+            }
           }
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(tempty_bar(acc));
-        if (++acc == kFAccs) {
+        if (++acc == n_acc) {
           acc = 0;
           aphase ^= 1u;
         }
       }
-      if (!ok || !warp_on) continue;
-      const int64_t col0 = static_cast<int64_t>(n_tile) * kFN + grp * kFCols;
-      if (p.vec) {
-        uint16_t* o = p.out + static_cast<int64_t>(row) * p.ld + col0;
+      if (!warp_on) return true;
 #pragma unroll
-        for (int j = 0; j < kFCols / 8; ++j) {
-          if (row < p.T && col0 + 8 * j + 8 <= p.V) {
-            *reinterpret_cast<uint4*>(o + 8 * j) =
-                make_uint4(bf16x2_of(sum[8 * j], sum[8 * j + 1]),
-                           bf16x2_of(sum[8 * j + 2], sum[8 * j + 3]),
-                           bf16x2_of(sum[8 * j + 4], sum[8 * j + 5]),
-                           bf16x2_of(sum[8 * j + 6], sum[8 * j + 7]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (row < p.T && col0 + 8 * j + i < p.V)
-                o[8 * j + i] = static_cast<uint16_t>(bf16x2_of(sum[8 * j + i], 0.f));
-          }
-        }
-      } else {
-        // rows at odd addresses: turn 32 columns at a time through shared
-        // memory, so that a warp writes consecutive elements of one row
-#pragma unroll
-        for (int c = 0; c < kFCols / 32; ++c) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            stg[lane * kFStageRow + i] = bf16x2_of(sum[c * 32 + 2 * i], sum[c * 32 + 2 * i + 1]);
+      for (int b = 0; b < kCh * kFChunk / kFBox; ++b) {
+        const int64_t colb = col0 + b * kFBox;
+        if (colb >= p.V) break;
+        if (p.tma_out) {
+          // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
+          const uint32_t obox = stg + obuf;
+          obuf ^= kFStagingWarp / 2;
+          if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
           __syncwarp();
-          const int64_t col = col0 + c * 32 + lane;
-          if (col < p.V) {
-            const int n = min(32, p.T - row0);
-            for (int r = 0; r < n; ++r)
-              p.out[static_cast<int64_t>(row0 + r) * p.ld + col] =
-                  reinterpret_cast<const uint16_t*>(stg + r * kFStageRow)[lane];
+          stage_box_row(obox, lane, sum + b * kFBox);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
+            bulk_commit_group();
+          }
+        } else {
+          // Rows at odd addresses: turned through shared memory (word w of row r
+          // at w ^ r), so that half a warp writes one row's 64 bytes as the
+          // 4-byte words they straddle.
+#pragma unroll
+          for (int w = 0; w < 16; ++w)
+            st_shared_u32(stg + lane * 64 + ((w ^ (lane & 15)) << 2),
+                          bf16x2_of(sum[b * kFBox + 2 * w], sum[b * kFBox + 2 * w + 1]));
+          __syncwarp();
+          const int n = static_cast<int>(min(static_cast<int64_t>(kFBox), p.V - colb));
+          const int j = lane & 15, half = lane >> 4;
+          const int rows = min(32, p.T - row0);
+          uint16_t* o = p.out + static_cast<int64_t>(row0 + half) * p.ld + colb;
+#pragma unroll 1
+          for (int r0 = 0; r0 < rows; r0 += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int r = r0 + 2 * i + half;
+              w[i] = ld_shared_u32(stg + r * 64 + ((j ^ (r & 15)) << 2));
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const bool on = r0 + 2 * i + half < rows;
+              // an odd start: word j holds elements 2j - 1 and 2j, the first and
+              // the last element are left over
+              const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(o) >> 1) & 1);
+              const uint32_t before = __shfl_up_sync(0xffffffffu, w[i], 1, 16);
+              const uint32_t v = odd ? (before >> 16) | (w[i] << 16) : w[i];
+              st_global_u32_if(o + 2 * j - odd, v, on && 2 * j >= odd && 2 * j + 1 - odd < n);
+              if (n == kFBox) {
+                st_global_u16_if(o + (j == 0 ? 0 : kFBox - 1), j == 0 ? w[i] : w[i] >> 16,
+                                 on && odd && (j == 0 || j == 15));
+              } else {  // the vocabulary's end: the elements that made no whole word
+                st_global_u16_if(o, w[i], on && odd && j == 0);
+                st_global_u16_if(o + n - 1, v, on && 2 * j - odd == n - 1 && n > odd);
+              }
+              o += 2 * p.ld;
+            }
           }
           __syncwarp();
         }
       }
+      return true;
+    };
+    // this group's boxes: the same number in every tile, possibly none
+    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x) {
+      bool more = true;
+      switch (my / (kFBox / kFChunk)) {
+        case 4: more = tile(std::integral_constant<int, 8>{}, u); break;
+        case 3: more = tile(std::integral_constant<int, 6>{}, u); break;
+        case 2: more = tile(std::integral_constant<int, 4>{}, u); break;
+        case 1: more = tile(std::integral_constant<int, 2>{}, u); break;
+        default: more = tile(std::integral_constant<int, 0>{}, u); break;
+      }
+      if (!more) break;
     }
+    if (lane == 0) bulk_wait_group<0>();  // every output box of this warp has been written
   }
 
   tc_fence_before();
@@ -425,6 +570,33 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+}
+
+// The kernel's shared-memory attribute belongs to the device: set by its first call.
+cudaError_t fp8_setup() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(logits_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kFSmemBytes);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// Columns of a tile when `sms` CTAs share the vocabulary m_tiles times over: as
+// few waves as 256-column tiles need, each tile just wide enough to fill them (one
+// 64-row tile of H=4096 V=32000, one wave of 152: 224 columns on 143 CTAs 26.6 us,
+// 128 columns in two waves 32.1 us).
+int fp8_tile_n(int64_t V, int64_t m_tiles, int sms) {
+  const int64_t units = m_tiles * ((V + kFMaxN - 1) / kFMaxN);
+  const int64_t waves = (units + sms - 1) / sms;
+  const int64_t per_m = waves * sms / m_tiles;  // vocabulary tiles in that many waves
+  if (per_m < 1) return kFMaxN;
+  const int64_t n = ((V + per_m - 1) / per_m + kFBox - 1) / kFBox * kFBox;
+  return static_cast<int>(n < kFMaxN ? n : kFMaxN);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -492,6 +664,8 @@ extern "C" int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_sc
   if (H % 16 != 0) return api_set_error(LMH_ERR_ALIGNMENT, "H must be a multiple of 16");
   if (ld_logits < V)
     return api_set_error(LMH_ERR_INVALID_ARG, "ld_logits must be at least V");
+  if (ceil_div(T, kFM) * ceil_div(V, kFBox) > (1LL << 30))
+    return api_set_error(LMH_ERR_INVALID_ARG, "T x V has too many tiles");
   if (T == 0) return api_set_error(LMH_OK, "");
   if (!hidden_q || !hidden_scale || !weight_q || !weight_scale || !logits)
     return api_set_error(LMH_ERR_INVALID_ARG, "every pointer is required");
@@ -500,41 +674,43 @@ extern "C" int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_sc
     return api_set_error(LMH_ERR_ALIGNMENT,
                          "hidden_q and weight_q need 16-byte, the scales 4-byte, logits 2-byte "
                          "alignment");
-  const int64_t n_m = ceil_div(T, kFM), n_n = ceil_div(V, kFN);
-  if (n_m * n_n > (1LL << 30))
-    return api_set_error(LMH_ERR_INVALID_ARG, "T x V has too many tiles");
   int sms = 0;
   unsigned* status = nullptr;
   int rc = api_device(&sms, &status);
   if (rc != LMH_OK) return rc;
+  cudaError_t e = fp8_setup();
+  if (e != cudaSuccess) return launch_error(e, "fp8 logits");
+  const int64_t n_m = ceil_div(T, kFM);
   Fp8Params p{};
+  p.tile_n = fp8_tile_n(V, n_m, sms);
+  const int64_t n_n = ceil_div(V, p.tile_n);
   p.T = static_cast<int>(T);
   p.V = static_cast<int>(V);
   p.KB = static_cast<int>(ceil_div(H, kFK));
   p.n_m = static_cast<int>(n_m);
   p.n_n = static_cast<int>(n_n);
   p.n_units = static_cast<int>(n_m * n_n);
+  p.group_m = 16;
   p.a_rows = T < kFM ? static_cast<int>((T + 7) / 8 * 8) : kFM;
   p.hs = hidden_scale;
   p.ws = weight_scale;
   p.out = logits;
   p.ld = ld_logits;
-  p.vec = (ld_logits % 8 == 0 && !misaligned(logits, 16)) ? 1 : 0;
+  p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16)) ? 1 : 0;
   p.status = status;
-  CUtensorMap ta, tb;
+  CUtensorMap ta, tb, tc{};
+  if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, V, T, ld_logits * 2)) != LMH_OK)
+    return rc;
   if ((rc = api_make_tmap_u8(&ta, hidden_q, H, T, H, kFK, p.a_rows)) != LMH_OK) return rc;
-  if ((rc = api_make_tmap_u8(&tb, weight_q, H, V, H, kFK, kFN)) != LMH_OK) return rc;
+  if ((rc = api_make_tmap_u8(&tb, weight_q, H, V, H, kFK, p.tile_n)) !=
+      LMH_OK)
+    return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  cudaError_t e;
   {
     KernelTimer timer(K_LOGITS_FP8, st);
-    e = cudaFuncSetAttribute(logits_fp8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kFSmemBytes);
-    if (e == cudaSuccess) {
-      const int grid = p.n_units < sms ? p.n_units : sms;
-      logits_fp8_kernel<<<grid, kFThreads, kFSmemBytes, st>>>(ta, tb, p);
-      e = cudaGetLastError();
-    }
+    const int grid = p.n_units < sms ? p.n_units : sms;
+    logits_fp8_kernel<<<grid, kFThreads, kFSmemBytes, st>>>(ta, tb, tc, p);
+    e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) return launch_error(e, "fp8 logits");

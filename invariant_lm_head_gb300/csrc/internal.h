@@ -167,6 +167,9 @@ int api_make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t o
 // The same for 8-bit elements (fp8 operands), 128-byte swizzle.
 int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// A bf16 output in 32 x 32 boxes with 64-byte swizzle (one epilogue warp's).
+int api_make_out_tmap_bf16(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows,
+                           uint64_t row_bytes);
 
 size_t gemm_smem_bytes();
 // Which contractions run on CTA pairs (launches with two or more 128-row m
