@@ -36,20 +36,25 @@ namespace {
 
 constexpr int kSThreads = 512;
 constexpr int kSWarps = kSThreads / 32;
-// Magnitude bits (sign dropped) of the histogram's range.
+constexpr int kBatch = 5;  // 16-byte loads in flight per thread
+constexpr int kMaxC = 8;   // most CTAs of a row (a portable cluster)
+// Magnitude bits (sign dropped) of the direct range.
 constexpr int kMagLo = (127 - 32) << 7;         // 2^-32
 constexpr int kMagHi = ((127 + 8) << 7) - 1;    // largest below 2^8
 constexpr int kHalf = kMagHi - kMagLo + 1;      // values of one sign: 5120
 constexpr int kBins = 2 * kHalf + 1;            // 10241
-constexpr int kPer = 21;                        // bins per thread (odd: no bank conflicts)
-constexpr int kBinsPad = kPer * kSThreads;      // 10752
-static_assert(kBinsPad >= kBins, "every bin needs an owner");
+constexpr int kBinsPad = 10752;                 // whole 16-byte vectors for 1, 2, 4 or 8 CTAs
+static_assert(kBinsPad >= kBins && kBinsPad % (4 * kMaxC) == 0, "bins");
 // Every bf16 value in descending order: positive 0 .. 32766, zero 32767,
 // negative 32768 .. 65534 (inf and NaN magnitudes included).
 constexpr int kFullKeys = 65535;
 constexpr int kWindows = (kFullKeys + kBinsPad - 1) / kBinsPad;
+constexpr int kDirect = -1;  // the direct range, beside windows 0 .. kWindows - 1
+constexpr int kNoBin = 0x7fffffff;
 // A weight below 2^-45 is zero: d < -45 ln 2.
 constexpr float kTail = -31.2f;
+
+typedef unsigned long long u64;
 
 // Position of a bf16 bit pattern in the full descending order (both zeros at 32767).
 __device__ __forceinline__ int full_key(uint32_t b) {
@@ -66,8 +71,6 @@ __device__ __forceinline__ bool is_masked(uint32_t b) {
   return (b & 0x7fffu) > 0x7f80u || b == 0xff80u;
 }
 
-typedef unsigned long long u64;
-
 struct SampleParams {
   const uint16_t* logits;
   int64_t T, V, ld;
@@ -81,35 +84,218 @@ struct SampleParams {
   int fix;  // weights are in units of 2^-fix
 };
 
-struct RowShared {
-  int flags;       // 1: above the range, 2: tiny, 4: below the range
-  int top;         // smallest occupied bin of a window
-  uint32_t cnt;    // results of a crossing search
-  u64 mass;
-  int bin;
-  u64 sc[kSWarps], sm[kSWarps], sq[kSWarps];
+// What a row asks for; load() is false when a setting is out of range.
+struct Settings {
+  float t, top_p, min_p, u;
+  int top_k;
+  __device__ __forceinline__ bool load(const SampleParams& p, int64_t row) {
+    t = p.row_t ? p.row_t[row] : p.temperature;
+    top_p = p.row_p ? p.row_p[row] : p.top_p;
+    min_p = p.row_m ? p.row_m[row] : p.min_p;
+    top_k = p.row_k ? p.row_k[row] : p.top_k;
+    u = p.uniform[row];
+    return t >= 0.f && t <= 3.402823466e38f && top_p > 0.f && min_p <= 1.f && u >= 0.f &&
+           u <= 1.f && top_k >= 0;
+  }
 };
 
-// One row's running state in a CTA.
+// Where the running count or mass passes a point: the value's key, the token's
+// rank among its equals, the mass up to and with it.
+struct Crossing {
+  u64 upto;
+  int key;
+  uint32_t rank;
+};
+
+struct Totals {
+  u64 count, mass, kept;  // kept: the mass that min-p keeps
+};
+
+struct RowShared {
+  Totals part[kMaxC];       // every CTA's share of the built window
+  Crossing found[2];
+  u64 warp_c[kSWarps], warp_m[kSWarps], warp_q[kSWarps];
+  int64_t index;
+  uint32_t hits[kBatch + 1][kSWarps];
+  int flags;                // 1: above the direct range, 2: tiny, 4: below the range
+  int top;                  // smallest occupied bin of the CTA's own counts
+  int cmd_key;              // the token to look for: its key (-1: not in this CTA)
+  uint32_t cmd_rank;        // and its rank among the CTA's own tokens of that key
+};
+
+// ------------------------------------------------------------ the cluster
+template <int kC>
+__device__ __forceinline__ void row_sync() {
+  if constexpr (kC > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+}
+// The address of the same shared variable in CTA c.
+template <int kC>
+__device__ __forceinline__ uint32_t peer(const void* here, int c) {
+  return kC > 1 ? mapa_shared(smem_u32(here), static_cast<uint32_t>(c)) : smem_u32(here);
+}
+__device__ __forceinline__ uint4 ld_peer_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_peer_u64(uint32_t addr, u64 v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+
+// ------------------------------------------------------------ reading a row
+// A CTA's part of a row in index order: 2-byte steps up to the row's first
+// 16-byte boundary (the first CTA), a run of 16-byte vectors, and the row's last
+// elements (the last CTA).
+struct Slice {
+  const uint16_t* x;   // the row
+  int64_t head;        // elements before the row's first vector
+  int64_t v0, v1;      // this CTA's vectors
+  int n_head, n_tail;  // this CTA's elements before and after them (at most 7)
+  __device__ __forceinline__ Slice(const uint16_t* row, int64_t V, int rank, int n_ranks) : x(row) {
+    const int64_t to16 = ((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) >> 1;
+    head = to16 < V ? to16 : V;
+    const int64_t nv = (V - head) >> 3;
+    const int64_t per = (nv + n_ranks - 1) / n_ranks;
+    v0 = min(nv, per * rank);
+    v1 = min(nv, v0 + per);
+    n_head = rank == 0 ? static_cast<int>(head) : 0;
+    n_tail = rank == n_ranks - 1 ? static_cast<int>(V - head - 8 * nv) : 0;
+  }
+  __device__ __forceinline__ const uint4* vec() const {
+    return reinterpret_cast<const uint4*>(x + head);
+  }
+  __device__ __forceinline__ const uint16_t* tail() const { return x + head + 8 * v1; }
+};
+
+// What a CTA has seen besides its counts.
+struct Seen {
+  int flags = 0;
+  int top = kNoBin;
+};
+
+// Counts one value in the direct range.
+__device__ __forceinline__ bool count_in_range(uint32_t b, uint32_t* hist, Seen& seen) {
+  const int t = static_cast<int>(b & 0x7fffu) - (kMagLo - 1);
+  const bool in = static_cast<unsigned>(t - 1) < static_cast<unsigned>(kHalf);
+  const int bin = (b & 0x8000u) ? kHalf + t : kHalf - t;
+  if (in) {
+    atomicAdd(&hist[bin], 1u);
+    seen.top = min(seen.top, bin);
+  }
+  return in;
+}
+// The others: zero, masked, or outside the range.
+__device__ __forceinline__ void count_rest(uint32_t b, uint32_t* hist, Seen& seen) {
+  const uint32_t mag = b & 0x7fffu;
+  if (mag == 0u) {
+    atomicAdd(&hist[kHalf], 1u);
+    seen.top = min(seen.top, kHalf);
+  } else if (!is_masked(b)) {
+    seen.flags |= mag < kMagLo ? 2 : ((b & 0x8000u) ? 4 : 1);
+  }
+}
+__device__ __forceinline__ void count_in_window(uint32_t b, int lo, uint32_t* hist, Seen& seen) {
+  const int k = full_key(b) - lo;
+  if (k >= 0 && k < kBinsPad && !is_masked(b)) {
+    atomicAdd(&hist[k], 1u);
+    seen.top = min(seen.top, k);
+  }
+}
+
+// Zeroes the histogram and counts the slice's values of window `win` in it.
+__device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* hist) {
+  Seen seen;
+  const uint4* v = sl.vec();
+  bool zeroed = false;
+  for (int64_t i0 = sl.v0 + threadIdx.x; !zeroed || i0 < sl.v1; i0 += kBatch * kSThreads) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k * kSThreads < sl.v1) w[k] = v[i0 + k * kSThreads];
+    if (!zeroed) {  // while the first loads are under way
+      uint4* h = reinterpret_cast<uint4*>(hist);
+      for (int i = threadIdx.x; i < kBinsPad / 4; i += kSThreads) h[i] = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+      zeroed = true;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (i0 + k * kSThreads >= sl.v1) continue;
+      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      if (win == kDirect) {
+        bool all = true;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          all &= count_in_range(ws[q] & 0xffffu, hist, seen);
+          all &= count_in_range(ws[q] >> 16, hist, seen);
+        }
+        if (!all) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t b = q & 1 ? ws[q / 2] >> 16 : ws[q / 2] & 0xffffu;
+            const uint32_t mag = b & 0x7fffu;
+            if (mag < kMagLo || mag > kMagHi) count_rest(b, hist, seen);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int q = 0; q < 8; ++q) {
+          const uint32_t b = (ws[q / 2] >> (16 * (q & 1))) & 0xffffu;
+          count_in_window(b, win * kBinsPad, hist, seen);
+        }
+      }
+    }
+  }
+  if (threadIdx.x < sl.n_head + sl.n_tail) {
+    const int i = threadIdx.x;
+    const uint32_t b = i < sl.n_head ? sl.x[i] : sl.tail()[i - sl.n_head];
+    if (win != kDirect)
+      count_in_window(b, win * kBinsPad, hist, seen);
+    else if (!count_in_range(b, hist, seen))
+      count_rest(b, hist, seen);
+  }
+  return seen;
+}
+
+// ------------------------------------------------------------ one row
+template <int kC>
 struct Row {
-  const uint16_t* x;
-  int64_t V;
+  static constexpr int kShare = kBinsPad / kC;  // bins that a CTA sums over the cluster
+  static constexpr int kVec = (kShare / 4 + kSThreads - 1) / kSThreads;  // 16-byte vectors a thread
+  static constexpr int kOwn = 4 * kVec;         // bins of one thread
+  static_assert(kOwn <= 32, "one lane per bin in a crossing");
+
   uint32_t* hist;
   RowShared* sh;
+  int cta;
   float t, z_max, x_max, min_p;
   int fix;
-  int window;       // window held by the histogram: -1 the direct range
-  // this thread's exclusive prefix of the built window
-  uint32_t c0, cn;
-  u64 m0, mn;
+  int window;       // what the histogram holds
+  int top;          // the window's smallest occupied bin, kNoBin if none
+  int flags;        // what the row holds outside the direct range
+  int turn;         // which of the two result slots is next
+  // this thread's bins in the built window: what comes before them, and their totals
+  u64 c0, cn, m0, mn;
 
   __device__ __forceinline__ int bin_key(int bin) const {
-    if (window >= 0) return window * kBinsPad + bin;
+    if (window != kDirect) return window * kBinsPad + bin;
     if (bin < kHalf) return 32767 - (kMagHi - bin);
     return bin == kHalf ? 32767 : 32767 + (bin - kHalf - 1 + kMagLo);
   }
-  __device__ __forceinline__ int n_bins() const {
-    return window < 0 ? kBins : min(kBinsPad, kFullKeys - window * kBinsPad);
+  __device__ __forceinline__ void set_max(int key) {
+    x_max = key_value(key);
+    z_max = __fdiv_rn(x_max, t);
   }
   // exp(z - m) of one value in fp32, and as an integer
   __device__ __forceinline__ float weight(float v) const {
@@ -126,363 +312,457 @@ struct Row {
   __device__ __forceinline__ u64 fixed(float w) const {
     return __float2ull_rn(w * __uint_as_float(static_cast<uint32_t>(127 + fix) << 23));
   }
+
+  // Counts window `win` of the row over the cluster: afterwards top and flags
+  // are the whole row's. Two barriers follow (finish): between them the CTAs read
+  // each other's counts.
+  __device__ __forceinline__ void count(const Slice& sl, int win) {
+    window = win;
+    if (threadIdx.x == 0) {
+      sh->flags = 0;
+      sh->top = kNoBin;
+    }
+    const Seen seen = count_slice(sl, win, hist);  // its barrier also covers the two above
+    const int f = __reduce_or_sync(0xffffffffu, seen.flags);
+    const int b = __reduce_min_sync(0xffffffffu, seen.top);
+    if ((threadIdx.x & 31) == 0) {
+      if (f) atomicOr(&sh->flags, f);
+      if (b != kNoBin) atomicMin(&sh->top, b);
+    }
+    row_sync<kC>();
+    flags = 0;
+    top = kNoBin;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      flags |= static_cast<int>(ld_peer_u32(peer<kC>(&sh->flags, c)));
+      top = min(top, static_cast<int>(ld_peer_u32(peer<kC>(&sh->top, c))));
+    }
+  }
+
+  // Sums this CTA's share of the bins over the cluster (in place: no one else
+  // reads that share here), weighs them, and returns the window's totals. x_max
+  // must be set.
+  __device__ __forceinline__ Totals finish() {
+    uint4* h = reinterpret_cast<uint4*>(hist + cta * kShare) + threadIdx.x * kVec;
+    uint4 n[kVec];
+    u64 q = 0;
+    cn = mn = 0;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      n[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (static_cast<int>(threadIdx.x) * kVec + k < kShare / 4) {
+        if constexpr (kC > 1) {
+          uint4 v[kC];
+#pragma unroll
+          for (int c = 0; c < kC; ++c) v[c] = ld_peer_v4(peer<kC>(h + k, c));
+#pragma unroll
+          for (int c = 0; c < kC; ++c) {
+            n[k].x += v[c].x;
+            n[k].y += v[c].y;
+            n[k].z += v[c].z;
+            n[k].w += v[c].w;
+          }
+          h[k] = n[k];
+        } else {
+          n[k] = h[k];
+        }
+      }
+    }
+    const int bin0 = cta * kShare + threadIdx.x * kOwn;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const uint32_t ns[4] = {n[k].x, n[k].y, n[k].z, n[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (ns[j]) {
+          const float w = weight(key_value(bin_key(bin0 + 4 * k + j)));
+          const u64 mass = ns[j] * fixed(w);
+          cn += ns[j];
+          mn += mass;
+          if (w >= min_p) q += mass;
+        }
+      }
+    }
+    // exclusive prefixes over the CTA's threads
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 ic = cn, im = mn;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const u64 oc = __shfl_up_sync(0xffffffffu, ic, off), om = __shfl_up_sync(0xffffffffu, im, off);
+      if (lane >= off) {
+        ic += oc;
+        im += om;
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+    if (lane == 31) {
+      sh->warp_c[warp] = ic;
+      sh->warp_m[warp] = im;
+      sh->warp_q[warp] = q;
+    }
+    __syncthreads();
+    c0 = ic - cn;
+    m0 = im - mn;
+    Totals mine{0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kSWarps; ++w) {
+      if (w < warp) {
+        c0 += sh->warp_c[w];
+        m0 += sh->warp_m[w];
+      }
+      mine.count += sh->warp_c[w];
+      mine.mass += sh->warp_m[w];
+      mine.kept += sh->warp_q[w];
+    }
+    if (threadIdx.x < kC) {
+      const uint32_t to = peer<kC>(&sh->part[cta], threadIdx.x);
+      st_peer_u64(to, mine.count);
+      st_peer_u64(to + 8, mine.mass);
+      st_peer_u64(to + 16, mine.kept);
+    }
+    row_sync<kC>();
+    Totals all{0, 0, 0};
+#pragma unroll
+    for (int c = 0; c < kC; ++c) {
+      if (c < cta) {
+        c0 += sh->part[c].count;
+        m0 += sh->part[c].mass;
+      }
+      all.count += sh->part[c].count;
+      all.mass += sh->part[c].mass;
+      all.kept += sh->part[c].kept;
+    }
+    return all;
+  }
+
+  // The token of rank `at` in the built window (kMass false), or where its
+  // running mass passes `at`. The thread that owns the crossing's bins has its
+  // warp look at them, one lane each, and tells every CTA. With kLast the CTA that
+  // holds the token is told to look for it.
+  template <bool kMass, bool kLast>
+  __device__ __forceinline__ Crossing cross(u64 at) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = kMass ? m0 <= at && at - m0 < mn : c0 <= at && at - c0 < cn;
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    if (who) {
+      const int src = __ffs(who) - 1;
+      const u64 bm = __shfl_sync(0xffffffffu, m0, src), bc = __shfl_sync(0xffffffffu, c0, src);
+      const int bin = cta * kShare + ((threadIdx.x & ~31) + src) * kOwn + lane;
+      // a thread's last vectors may lie beyond the share: it counted none of them
+      const u64 n = lane < kOwn && bin < (cta + 1) * kShare ? hist[bin] : 0u;
+      const u64 w = n ? fixed(weight(key_value(bin_key(bin)))) : 0u;
+      u64 c = n, m = n * w;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const u64 oc = __shfl_up_sync(0xffffffffu, c, off);
+        const u64 om = __shfl_up_sync(0xffffffffu, m, off);
+        if (lane >= off) {
+          c += oc;
+          m += om;
+        }
+      }
+      c += bc - n;  // before this bin
+      m += bm - n * w;
+      const bool here = kMass ? m <= at && at - m < n * w : c <= at && at - c < n;
+      const int at_lane = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+      // the rank among the bin's tokens; the quotient is below 2^32
+      u64 j = at - c;
+      if (kMass && here) {
+        const u64 rest = at - m;
+        j = static_cast<u64>(__fdividef(static_cast<float>(rest), static_cast<float>(w)));
+        while (j * w > rest) --j;
+        while ((j + 1) * w <= rest) ++j;
+      }
+      const u64 upto = __shfl_sync(0xffffffffu, m + (j + 1) * w, at_lane);
+      uint32_t rank = __shfl_sync(0xffffffffu, static_cast<uint32_t>(j), at_lane);
+      const int hit = __shfl_sync(0xffffffffu, bin, at_lane);
+      const int key = bin_key(hit);
+      if (lane < kC) {
+        const uint32_t to = peer<kC>(&sh->found[turn], lane);
+        st_peer_u64(to, upto);
+        st_peer_u64(to + 8, static_cast<u64>(static_cast<uint32_t>(key)) |
+                                (static_cast<u64>(rank) << 32));
+      }
+      if constexpr (kLast) {
+        // each CTA's own count: this CTA's was replaced by the sum
+        uint32_t own = lane < kC && lane != cta ? ld_peer_u32(peer<kC>(hist + hit, min(lane, kC - 1))) : 0u;
+        const uint32_t others = __reduce_add_sync(0xffffffffu, own);
+        if (lane == cta) own = hist[hit] - others;
+        uint32_t upto_c = own;
+#pragma unroll
+        for (int off = 1; off < kC; off <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, upto_c, off);
+          if (lane >= off) upto_c += o;
+        }
+        if (lane < kC && rank >= upto_c - own && rank < upto_c) {
+          st_shared_cluster_u32(peer<kC>(&sh->cmd_rank, lane), rank - (upto_c - own));
+          st_shared_cluster_u32(peer<kC>(&sh->cmd_key, lane), static_cast<uint32_t>(key));
+        }
+      }
+    }
+    row_sync<kC>();
+    const Crossing r = sh->found[turn];
+    turn ^= 1;
+    return r;
+  }
 };
 
-// f(value bits) for every element of the row, whatever its address: 2-byte
-// steps up to the first 16-byte boundary, 16-byte loads, 2-byte steps.
-template <class F>
-__device__ __forceinline__ void for_row(const uint16_t* x, int64_t n, F&& f) {
-  const int64_t head =
-      min(n, static_cast<int64_t>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) >> 1));
-  const int64_t nv = (n - head) >> 3;
-  for (int64_t i = threadIdx.x; i < head; i += kSThreads) f(static_cast<uint32_t>(x[i]));
-  const uint4* v = reinterpret_cast<const uint4*>(x + head);
-  for (int64_t i = threadIdx.x; i < nv; i += kSThreads) {
-    const uint4 w = v[i];
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      f(ws[q] & 0xffffu);
-      f(ws[q] >> 16);
-    }
+// floor(f * m) for an fp32 f in [0, 1], and whether that is f * m itself.
+__device__ __forceinline__ u64 scaled_floor(float f, u64 m, bool& exact) {
+  const uint32_t b = __float_as_uint(f) & 0x7fffffffu;  // -0 is 0
+  const int e = static_cast<int>(b >> 23);
+  const u64 mant = e ? (b & 0x7fffffu) | 0x800000u : b & 0x7fffffu;
+  const int s = 150 - max(e, 1);  // f = mant * 2^-s, s >= 23
+  const u64 hi = __umul64hi(mant, m), lo = mant * m;
+  if (s >= 128) {
+    exact = (hi | lo) == 0;
+    return 0;
   }
-  for (int64_t i = head + nv * 8 + threadIdx.x; i < n; i += kSThreads)
-    f(static_cast<uint32_t>(x[i]));
-}
-
-// Counts the row's values in the direct range; r.sh->flags tells what else it holds.
-__device__ void build_direct(Row& r) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBinsPad; i += kSThreads) r.hist[i] = 0u;
-  if (threadIdx.x == 0) r.sh->flags = 0;
-  __syncthreads();
-  int flags = 0;
-  uint32_t* hist = r.hist;
-  for_row(r.x, r.V, [&](uint32_t b) {
-    const int mag = static_cast<int>(b & 0x7fffu);
-    const bool neg = b & 0x8000u;
-    if (mag >= kMagLo && mag <= kMagHi) {
-      atomicAdd(&hist[neg ? kHalf + 1 + (mag - kMagLo) : kMagHi - mag], 1u);
-    } else if (mag == 0) {
-      atomicAdd(&hist[kHalf], 1u);
-    } else if (!is_masked(b)) {
-      flags |= mag < kMagLo ? 2 : (neg ? 4 : 1);
-    }
-  });
-  if (flags) atomicOr(&r.sh->flags, flags);
-  r.window = -1;
-  __syncthreads();
-}
-
-__device__ void build_window(Row& r, int w) {
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBinsPad; i += kSThreads) r.hist[i] = 0u;
-  __syncthreads();
-  uint32_t* hist = r.hist;
-  const int lo = w * kBinsPad;
-  for_row(r.x, r.V, [&](uint32_t b) {
-    if (is_masked(b)) return;
-    const int k = full_key(b) - lo;
-    if (k >= 0 && k < kBinsPad) atomicAdd(&hist[k], 1u);
-  });
-  r.window = w;
-  __syncthreads();
-}
-
-// The first occupied bin of the built window, or -1.
-__device__ int top_bin(Row& r) {
-  if (threadIdx.x == 0) r.sh->top = 0x7fffffff;
-  __syncthreads();
-  for (int i = 0; i < kPer; ++i) {
-    const int bin = threadIdx.x * kPer + i;
-    if (r.hist[bin]) {
-      atomicMin(&r.sh->top, bin);
-      break;
-    }
+  if (s >= 64) {
+    const u64 q = s == 64 ? hi : hi >> (s - 64);
+    exact = lo == 0 && (s == 64 || (q << (s - 64)) == hi);
+    return q;
   }
-  __syncthreads();
-  const int top = r.sh->top;
-  __syncthreads();
-  return top == 0x7fffffff ? -1 : top;
+  exact = (lo << (64 - s)) == 0;
+  return (hi << (64 - s)) | (lo >> s);
 }
 
-// Exclusive prefixes of count and mass over the built window, kept per thread;
-// returns the window's totals, and the mass of the bins that min-p keeps.
-__device__ void scan_window(Row& r, u64& total_c, u64& total_m, u64& total_q) {
-  u64 c = 0, m = 0, q = 0;
-  const int nb = r.n_bins();
-  for (int i = 0; i < kPer; ++i) {
-    const int bin = threadIdx.x * kPer + i;
-    const uint32_t n = bin < nb ? r.hist[bin] : 0u;
-    if (n) {
-      const float w = r.weight(key_value(r.bin_key(bin)));
-      const u64 mass = n * r.fixed(w);
-      c += n;
-      m += mass;
-      if (w >= r.min_p) q += mass;
-    }
-  }
+// Index in the row of the slice's rank-th element (from 0) with this key.
+// A batch's matches are counted per vector row and warp, in index order.
+__device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int key,
+                                            uint32_t rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 ic = c, im = m;
+  auto match = [&](uint32_t b) { return full_key(b) == key ? 1u : 0u; };
+  // the elements before and after the vectors: every warp counts the former
+  const uint32_t h = __ballot_sync(0xffffffffu, lane < sl.n_head && match(sl.x[lane]));
+  if (rank < __popc(h)) {
+    uint32_t m = h;
+    for (uint32_t s = rank; s > 0; --s) m &= m - 1;
+    return __ffs(m) - 1;
+  }
+  uint32_t left = rank - __popc(h);
+  for (int64_t i0 = sl.v0; i0 < sl.v1; i0 += kBatch * kSThreads) {
+    uint4 w[kBatch];
+    uint32_t bits[kBatch];
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const u64 oc = __shfl_up_sync(0xffffffffu, ic, off), om = __shfl_up_sync(0xffffffffu, im, off);
-    if (lane >= off) {
-      ic += oc;
-      im += om;
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t i = i0 + k * kSThreads + threadIdx.x;
+      if (i < sl.v1) w[k] = sl.vec()[i];
     }
-  }
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-  if (lane == 31) {
-    r.sh->sc[warp] = ic;
-    r.sh->sm[warp] = im;
-    r.sh->sq[warp] = q;
-  }
-  __syncthreads();
-  u64 bc = 0, bm = 0;
-  total_c = total_m = total_q = 0;
-  for (int w = 0; w < kSWarps; ++w) {
-    if (w == warp) {
-      bc = total_c;
-      bm = total_m;
-    }
-    total_c += r.sh->sc[w];
-    total_m += r.sh->sm[w];
-    total_q += r.sh->sq[w];
-  }
-  r.c0 = static_cast<uint32_t>(bc + ic - c);
-  r.cn = static_cast<uint32_t>(c);
-  r.m0 = bm + im - m;
-  r.mn = m;
-  __syncthreads();
-}
-
-// Mass of the first `count` tokens of the built window (0 < count <= its total).
-__device__ u64 mass_of_count(Row& r, uint32_t count) {
-  const uint32_t at = count - 1;
-  if (r.c0 <= at && at - r.c0 < r.cn) {
-    uint32_t c = r.c0;
-    u64 m = r.m0;
-    for (int i = 0; i < kPer; ++i) {
-      const int bin = threadIdx.x * kPer + i;
-      const uint32_t n = r.hist[bin];
-      if (!n) continue;
-      const u64 w = r.fixed(r.weight(key_value(r.bin_key(bin))));
-      if (at - c < n) {
-        r.sh->mass = m + (at - c + 1) * w;
-        break;
-      }
-      c += n;
-      m += n * w;
-    }
-  }
-  __syncthreads();
-  const u64 v = r.sh->mass;
-  __syncthreads();
-  return v;
-}
-
-// The token at running mass `at` of the built window (0 <= at < its total): its
-// bin, its rank among the bin's tokens, and the mass up to and with it.
-__device__ void at_mass(Row& r, u64 at, int& bin_out, uint32_t& rank, u64& upto) {
-  if (r.m0 <= at && at - r.m0 < r.mn) {
-    u64 m = r.m0;
-    for (int i = 0; i < kPer; ++i) {
-      const int bin = threadIdx.x * kPer + i;
-      const uint32_t n = r.hist[bin];
-      if (!n) continue;
-      const u64 w = r.fixed(r.weight(key_value(r.bin_key(bin))));
-      if (at - m < n * w) {
-        const u64 j = (at - m) / w;
-        r.sh->bin = bin;
-        r.sh->cnt = static_cast<uint32_t>(j);
-        r.sh->mass = m + (j + 1) * w;
-        break;
-      }
-      m += n * w;
-    }
-  }
-  __syncthreads();
-  bin_out = r.sh->bin;
-  rank = r.sh->cnt;
-  upto = r.sh->mass;
-  __syncthreads();
-}
-
-// Index of the rank-th element (from 0) of the row whose value has this key. Each
-// warp owns a contiguous part of the row, in index order.
-__device__ int64_t index_of(Row& r, int key, uint32_t rank) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t per = (r.V + kSWarps - 1) / kSWarps;
-  const int64_t b = min(r.V, per * warp), e = min(r.V, per * (warp + 1));
-  uint32_t n = 0;
-  for (int64_t i = b + lane; i < e; i += 32)
-    n += full_key(r.x[i]) == key;
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t i = i0 + k * kSThreads + threadIdx.x;
+      bits[k] = 0;
+      if (i < sl.v1) {
+        const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) n += __shfl_xor_sync(0xffffffffu, n, off);
-  if (lane == 0) r.sh->sc[warp] = n;
-  __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < warp; ++w) before += static_cast<uint32_t>(r.sh->sc[w]);
-  if (rank >= before && rank - before < n) {
-    uint32_t left = rank - before;
-    for (int64_t i = b; i < e; i += 32) {
-      const int64_t j = i + lane;
-      const bool hit = j < e && full_key(r.x[j]) == key;
-      const uint32_t mask = __ballot_sync(0xffffffffu, hit);
-      const uint32_t k = __popc(mask);
-      if (left < k) {
-        if (hit && __popc(mask & ((1u << lane) - 1u)) == left) r.sh->mass = static_cast<u64>(j);
-        break;
+        for (int q = 0; q < 4; ++q)
+          bits[k] |= (match(ws[q] & 0xffffu) << (2 * q)) | (match(ws[q] >> 16) << (2 * q + 1));
       }
-      left -= k;
+      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(bits[k]));
+      if (lane == 0) sh->hits[k][warp] = n;
     }
-  }
-  __syncthreads();
-  const int64_t v = static_cast<int64_t>(r.sh->mass);
-  __syncthreads();
-  return v;
-}
-
-__global__ void __launch_bounds__(kSThreads) sample_kernel(const SampleParams p) {
-  __shared__ uint32_t hist[kBinsPad];
-  __shared__ RowShared sh;
-  for (int64_t row = blockIdx.x; row < p.T; row += gridDim.x) {
-    const float t_in = p.row_t ? p.row_t[row] : p.temperature;
-    const float top_p = p.row_p ? p.row_p[row] : p.top_p;
-    const float min_p = p.row_m ? p.row_m[row] : p.min_p;
-    const int top_k = p.row_k ? p.row_k[row] : p.top_k;
-    const float u = p.uniform[row];
-    if (!(t_in >= 0.f && t_in <= 3.402823466e38f && top_p > 0.f && min_p <= 1.f && u >= 0.f &&
-          u <= 1.f && top_k >= 0)) {
-      if (threadIdx.x == 0) {
-        p.token[row] = -1;
-        if (p.logprob) p.logprob[row] = __int_as_float(0x7fffffff);
+    __syncthreads();
+    uint32_t before = 0, at_k = kBatch, at_w = 0, at_before = 0;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+#pragma unroll
+      for (int x = 0; x < kSWarps; ++x) {
+        const uint32_t n = sh->hits[k][x];
+        if (at_k == kBatch && left < before + n) {
+          at_k = k;
+          at_w = x;
+          at_before = before;
+        }
+        before += n;
       }
-      continue;
     }
-    const bool greedy = t_in == 0.f;
-    Row r;
-    r.x = p.logits + row * p.ld;
-    r.V = p.V;
-    r.hist = hist;
-    r.sh = &sh;
-    r.t = greedy ? 1.f : t_in;
-    r.min_p = min_p;
-    r.fix = p.fix;
-
-    // the maximum, and whether the direct range holds all that matters
-    build_direct(r);
-    const int flags = sh.flags;
-    int n_win = 1, top_key = -1;
-    int top = top_bin(r);
-    if (top >= 0) {
-      top_key = r.bin_key(top);
-      r.x_max = key_value(top_key);
-      r.z_max = __fdiv_rn(r.x_max, r.t);
-    }
-    const bool high = flags & 1;
-    const bool tiny = (flags & 2) && (top < 0 || !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail));
-    const bool low = (flags & 4) && (top < 0 || !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail));
-    if (high || tiny || low) {
-      n_win = kWindows;
-      top_key = -1;
-    }
-    // totals, window by window
-    u64 wc[kWindows], wm[kWindows], wq[kWindows];
-    u64 n_all = 0, m_all = 0, q_all = 0;
-#pragma unroll 1
-    for (int w = 0; w < n_win; ++w) {
-      if (n_win > 1) {
-        build_window(r, w);
-        if (top_key < 0) {
-          top = top_bin(r);
-          if (top >= 0) {
-            top_key = r.bin_key(top);
-            r.x_max = key_value(top_key);
-            r.z_max = __fdiv_rn(r.x_max, r.t);
-          }
+    if (at_k < kBatch) {
+      if (warp == static_cast<int>(at_w)) {
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (k == static_cast<int>(at_k)) mine = bits[k];
+        uint32_t inc = __popc(mine);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+          if (lane >= off) inc += o;
+        }
+        const uint32_t want = left - at_before, low = inc - __popc(mine);
+        if (low <= want && want < inc) {
+          for (uint32_t s = want - low; s > 0; --s) mine &= mine - 1;
+          sh->index = sl.head + 8 * (i0 + at_k * kSThreads + threadIdx.x) + __ffs(mine) - 1;
         }
       }
-      if (top_key < 0) {
-        wc[w] = wm[w] = wq[w] = 0;
+      __syncthreads();
+      return sh->index;
+    }
+    left -= before;
+    __syncthreads();  // the counts have been read
+  }
+  const uint32_t m0 = __ballot_sync(0xffffffffu, lane < sl.n_tail && match(sl.tail()[lane]));
+  uint32_t m = m0;
+  for (uint32_t s = left; s > 0; --s) m &= m - 1;
+  return sl.tail() - sl.x + __ffs(m) - 1;
+}
+
+// One row per cluster of kC CTAs, each counting a contiguous part of it, each
+// weighing a share of the bins; every step that needs the whole row ends with a
+// cluster barrier, after which all CTAs hold the same numbers and go the same way.
+template <int kC>
+__global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleParams p) {
+  __shared__ __align__(16) uint32_t hist[kBinsPad];
+  __shared__ RowShared sh;
+  const int cta = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int64_t row = blockIdx.x / kC;
+  Settings s;
+  if (!s.load(p, row)) {
+    if (cta == 0 && threadIdx.x == 0) {
+      p.token[row] = -1;
+      if (p.logprob) p.logprob[row] = __int_as_float(0x7fffffff);
+    }
+    return;  // the whole cluster leaves
+  }
+  const bool greedy = s.t == 0.f;
+  const Slice sl(p.logits + row * p.ld, p.V, cta, kC);
+  Row<kC> r;
+  r.hist = hist;
+  r.sh = &sh;
+  r.cta = cta;
+  r.t = greedy ? 1.f : s.t;
+  r.min_p = s.min_p;
+  r.fix = p.fix;
+  r.turn = 0;
+  if (threadIdx.x == 0) sh.cmd_key = -1;
+
+  r.count(sl, kDirect);
+  if (r.top != kNoBin) r.set_max(r.bin_key(r.top));
+  // does a value outside the direct range matter?
+  const bool none = r.top == kNoBin;
+  const bool windows =
+      (r.flags & 1) ||
+      ((r.flags & 2) && (none || !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail))) ||
+      ((r.flags & 4) && (none || !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail)));
+  if (none && !windows) {  // nothing to draw
+    if (cta == 0 && threadIdx.x == 0) {
+      p.token[row] = -1;
+      if (p.logprob) p.logprob[row] = 0.f;
+    }
+    row_sync<kC>();  // the others have read this CTA's flags
+    return;
+  }
+
+  Totals all{0, 0, 0};
+  u64 wc[kWindows], wm[kWindows];
+  const int n_win = windows ? kWindows : 1;
+  if (!windows) {
+    all = r.finish();
+    wc[0] = all.count;
+    wm[0] = all.mass;
+  } else {
+    row_sync<kC>();
+    bool any = false;
+#pragma unroll 1
+    for (int w = 0; w < kWindows; ++w) {
+      r.count(sl, w);
+      if (!any && r.top != kNoBin) {
+        r.set_max(r.bin_key(r.top));
+        any = true;
+      }
+      if (!any) {
+        wc[w] = wm[w] = 0;
+        row_sync<kC>();
         continue;
       }
-      scan_window(r, wc[w], wm[w], wq[w]);
-      n_all += wc[w];
-      m_all += wm[w];
-      q_all += wq[w];
-    }
-    if (top_key < 0) {  // nothing to draw
-      if (threadIdx.x == 0) {
-        p.token[row] = -1;
-        if (p.logprob) p.logprob[row] = 0.f;
-      }
-      continue;
-    }
-    auto enter = [&](int w) {  // make window w the built one
-      if (n_win == 1 || r.window == w) return;
-      build_window(r, w);
-      u64 a, b, c;
-      scan_window(r, a, b, c);
-    };
-    // the window where the running mass passes `at`, and the mass before it
-    auto find_mass = [&](u64 at, u64& before) {
-      int w = 0;
-      before = 0;
-      while (w + 1 < n_win && at - before >= wm[w]) before += wm[w++];
-      return w;
-    };
-
-    int key = top_key;
-    uint32_t rank = 0;
-    if (!greedy) {
-      u64 kept = m_all;
-      if (top_k > 0 && static_cast<u64>(top_k) < n_all) {
-        u64 c = 0, m = 0;
-        int w = 0;
-        while (static_cast<u64>(top_k) - c > wc[w]) {
-          c += wc[w];
-          m += wm[w++];
-        }
-        enter(w);
-        kept = m + mass_of_count(r, static_cast<uint32_t>(top_k - c));
-      }
-      if (top_p < 1.f) {
-        u64 reach = static_cast<u64>(ceil(static_cast<double>(top_p) * static_cast<double>(kept)));
-        reach = reach < 1 ? 1 : (reach > kept ? kept : reach);
-        u64 before, upto;
-        const int w = find_mass(reach - 1, before);
-        enter(w);
-        int bin;
-        uint32_t j;
-        at_mass(r, reach - 1 - before, bin, j, upto);
-        kept = before + upto;
-      }
-      if (q_all < kept) kept = q_all;
-      u64 at = static_cast<u64>(static_cast<double>(u) * static_cast<double>(kept));
-      if (at >= kept) at = kept - 1;
-      u64 before, upto;
-      const int w = find_mass(at, before);
-      enter(w);
-      int bin;
-      at_mass(r, at - before, bin, rank, upto);
-      key = r.bin_key(bin);
-    }
-    const int64_t index = index_of(r, key, rank);
-    if (threadIdx.x == 0) {
-      p.token[row] = static_cast<int32_t>(index);
-      if (p.logprob) {
-        const float v = key_value(key);
-        const double d = v == r.x_max ? 0.0
-                                      : static_cast<double>(__fdiv_rn(v, r.t)) -
-                                            static_cast<double>(r.z_max);
-        p.logprob[row] =
-            static_cast<float>(d - log(ldexp(static_cast<double>(m_all), -p.fix)));
-      }
+      const Totals a = r.finish();
+      wc[w] = a.count;
+      wm[w] = a.mass;
+      all.count += a.count;
+      all.mass += a.mass;
+      all.kept += a.kept;
     }
   }
+  auto enter = [&](int w) {  // make window w the built one
+    if (!windows || r.window == w) return;
+    r.count(sl, w);
+    r.finish();
+  };
+  // the window where the running mass passes `at`, and the mass before it
+  auto find_mass = [&](u64 at, u64& before) {
+    int w = 0;
+    before = 0;
+    while (w + 1 < n_win && at - before >= wm[w]) before += wm[w++];
+    return w;
+  };
+
+  u64 at = 0;  // the draw: the first token whose running mass exceeds it
+  if (!greedy) {
+    u64 kept = all.mass, before;
+    bool exact;
+    if (s.top_k > 0 && static_cast<u64>(s.top_k) < all.count) {
+      u64 c = 0, m = 0;
+      int w = 0;
+      while (static_cast<u64>(s.top_k) - c > wc[w]) {
+        c += wc[w];
+        m += wm[w++];
+      }
+      enter(w);
+      kept = m + r.template cross<false, false>(s.top_k - c - 1).upto;
+    }
+    if (s.top_p < 1.f) {
+      u64 reach = scaled_floor(s.top_p, kept, exact);
+      if (!exact) ++reach;
+      reach = reach < 1 ? 1 : reach;
+      const int w = find_mass(reach - 1, before);
+      enter(w);
+      kept = before + r.template cross<true, false>(reach - 1 - before).upto;
+    }
+    if (all.kept < kept) kept = all.kept;
+    at = scaled_floor(s.u, kept, exact);
+    if (at >= kept) at = kept - 1;
+  }
+  u64 before;
+  const int w_at = find_mass(at, before);
+  enter(w_at);
+  const Crossing c = r.template cross<true, true>(at - before);
+  // no CTA reads another's memory from here on
+  if (sh.cmd_key >= 0) {
+    const int64_t index = index_of(sl, &sh, sh.cmd_key, sh.cmd_rank);
+    if (threadIdx.x == 0) p.token[row] = static_cast<int32_t>(index);
+  }
+  if (p.logprob && cta == kC - 1 && threadIdx.x == kSThreads - 1) {
+    // d - ln(mass * 2^-fix), the logarithm as that of a number in [1, 2) and a
+    // multiple of ln 2 whose first part is exact
+    const float v = key_value(c.key);
+    const float z = __fdiv_rn(v, r.t);
+    const float d = v == r.x_max ? 0.f : __fsub_rn(z, r.z_max);
+    const float lost =  // what the difference rounded off; 0 where z overflows
+        v == r.x_max ? 0.f
+                     : __fsub_rn(__fsub_rn(z, __fsub_rn(d, __fsub_rn(d, z))),
+                                 __fadd_rn(r.z_max, __fsub_rn(d, z)));
+    const int e = 63 - __clzll(static_cast<long long>(all.mass));
+    const float f = __ull2float_rn(all.mass) * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    const float k = static_cast<float>(e - p.fix);
+    p.logprob[row] = (d - k * 0x1.62ep-1f) + (lost - fmaf(k, 0x1.0bfbe8p-15f, logf(f)));
+  }
+}
+
+template <int kC>
+cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kC;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<kC>, p);
 }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -498,7 +778,7 @@ extern "C" int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64
                              int32_t* out_token, float* out_logprob,
                              struct CUstream_st* stream) {
   using namespace lmh;
-  if (T < 0 || T > LMH_MAX_DIM || V < 1 || V > LMH_MAX_DIM)
+  if (T < 0 || T > LMH_MAX_DIM / 8 || V < 1 || V > LMH_MAX_DIM)
     return api_set_error(LMH_ERR_INVALID_ARG, "T or V out of range");
   if (ld_logits < V)
     return api_set_error(LMH_ERR_INVALID_ARG, "ld_logits must be at least V");
@@ -545,9 +825,15 @@ extern "C" int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64
   cudaError_t e;
   {
     KernelTimer timer(K_SAMPLE, st);
-    const int64_t grid = T < 4 * sms ? T : 4 * sms;
-    sample_kernel<<<static_cast<unsigned>(grid), kSThreads, 0, st>>>(p);
-    e = cudaGetLastError();
+    const int64_t slots = 2 * static_cast<int64_t>(sms);  // CTAs at work at once
+    if (T * 8 <= slots)
+      e = launch_sample<8>(p, st);
+    else if (T * 4 <= slots)
+      e = launch_sample<4>(p, st);
+    else if (T * 2 <= slots)
+      e = launch_sample<2>(p, st);
+    else
+      e = launch_sample<1>(p, st);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) {
