@@ -26,16 +26,19 @@
 #include <cstdio>
 #include <cmath>
 
+#include <cuda_bf16.h>
+
 #include "internal.h"
 #include "lmhead.h"
+#include "online_softmax.cuh"
 #include "ptx.cuh"
 
 namespace lmh {
 
 namespace {
 
-constexpr int kSThreads = 512;
-constexpr int kSWarps = kSThreads / 32;
+constexpr int kMaxThreads = 512;
+constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kBatch = 5;  // 16-byte loads in flight per thread
 constexpr int kMaxC = 8;   // most CTAs of a row (a portable cluster)
 // Magnitude bits (sign dropped) of the direct range.
@@ -50,7 +53,7 @@ static_assert(kBinsPad >= kBins && kBinsPad % (4 * kMaxC) == 0, "bins");
 constexpr int kFullKeys = 65535;
 constexpr int kWindows = (kFullKeys + kBinsPad - 1) / kBinsPad;
 constexpr int kDirect = -1;  // the direct range, beside windows 0 .. kWindows - 1
-constexpr int kNoBin = 0x7fffffff;
+constexpr int kNone = 0x7fffffff;
 // A weight below 2^-45 is zero: d < -45 ln 2.
 constexpr float kTail = -31.2f;
 
@@ -108,17 +111,18 @@ struct Crossing {
 };
 
 struct Totals {
-  u64 count, mass, kept;  // kept: the mass that min-p keeps
+  u64 mass, kept;  // kept: the mass that min-p keeps
+  uint32_t count;
 };
 
 struct RowShared {
   Totals part[kMaxC];       // every CTA's share of the built window
   Crossing found[2];
-  u64 warp_c[kSWarps], warp_m[kSWarps], warp_q[kSWarps];
+  Totals warp[kMaxWarps];
+  uint32_t hits[kMaxWarps];
   int64_t index;
-  uint32_t hits[kBatch + 1][kSWarps];
   int flags;                // 1: above the direct range, 2: tiny, 4: below the range
-  int top;                  // smallest occupied bin of the CTA's own counts
+  int top;                  // smallest position of the CTA's own values
   int cmd_key;              // the token to look for: its key (-1: not in this CTA)
   uint32_t cmd_rank;        // and its rank among the CTA's own tokens of that key
 };
@@ -178,115 +182,144 @@ struct Slice {
   __device__ __forceinline__ const uint16_t* tail() const { return x + head + 8 * v1; }
 };
 
-// What a CTA has seen besides its counts.
+// What a thread has seen besides its counts: flags, and the smallest position
+// (that of the largest value).
 struct Seen {
   int flags = 0;
-  int top = kNoBin;
+  int top = kNone;
 };
 
-// Counts one value in the direct range.
-__device__ __forceinline__ bool count_in_range(uint32_t b, uint32_t* hist, Seen& seen) {
-  const int t = static_cast<int>(b & 0x7fffu) - (kMagLo - 1);
-  const bool in = static_cast<unsigned>(t - 1) < static_cast<unsigned>(kHalf);
-  const int bin = (b & 0x8000u) ? kHalf + t : kHalf - t;
-  if (in) {
-    atomicAdd(&hist[bin], 1u);
-    seen.top = min(seen.top, bin);
-  }
-  return in;
-}
-// The others: zero, masked, or outside the range.
-__device__ __forceinline__ void count_rest(uint32_t b, uint32_t* hist, Seen& seen) {
-  const uint32_t mag = b & 0x7fffu;
-  if (mag == 0u) {
-    atomicAdd(&hist[kHalf], 1u);
-    seen.top = min(seen.top, kHalf);
-  } else if (!is_masked(b)) {
-    seen.flags |= mag < kMagLo ? 2 : ((b & 0x8000u) ? 4 : 1);
+// Counts eight values, all in the direct range, two to a word: with a = |x|'s
+// bits the bins are kHalf - (a - kMagLo + 1) for a positive value and kHalf +
+// (a - kMagLo + 1) for a negative one, both halves at once (no half carries).
+__device__ __forceinline__ void count_pairs(const uint4& w, uint32_t* hist) {
+  constexpr uint32_t kPlus = (kHalf + kMagLo - 1) * 0x10001u, kMinus = (kMagLo - 1 - kHalf) * 0x10001u;
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t a = ws[q] & 0x7fff7fffu;
+    uint32_t neg;  // each half's sign bit in all of its bits
+    asm("prmt.b32 %0, %1, %1, 0xbb99;" : "=r"(neg) : "r"(ws[q]));
+    const uint32_t bin = ((kPlus - a) & ~neg) | ((a - kMinus) & neg);
+    atomicAdd(&hist[bin & 0xffffu], 1u);
+    atomicAdd(&hist[bin >> 16], 1u);
   }
 }
-__device__ __forceinline__ void count_in_window(uint32_t b, int lo, uint32_t* hist, Seen& seen) {
-  const int k = full_key(b) - lo;
-  if (k >= 0 && k < kBinsPad && !is_masked(b)) {
-    atomicAdd(&hist[k], 1u);
-    seen.top = min(seen.top, k);
+// n values of which some may be zero, masked, or outside the direct range.
+__device__ __noinline__ Seen count_any(uint4 w, int n, uint32_t* hist, Seen seen) {
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) {
+    const uint32_t b = w.x & 0xffffu;
+    w.x = __funnelshift_r(w.x, w.y, 16);
+    w.y = __funnelshift_r(w.y, w.z, 16);
+    w.z = __funnelshift_r(w.z, w.w, 16);
+    w.w >>= 16;
+    if (is_masked(b)) continue;
+    const int t = static_cast<int>(b & 0x7fffu) - (kMagLo - 1);
+    const bool neg = b & 0x8000u;
+    if ((b & 0x7fffu) == 0u)
+      atomicAdd(&hist[kHalf], 1u);
+    else if (t < 1 || t > kHalf)
+      seen.flags |= t < 1 ? 2 : (neg ? 4 : 1);
+    else
+      atomicAdd(&hist[neg ? kHalf + t : kHalf - t], 1u);
+    seen.top = min(seen.top, full_key(b));
   }
+  return seen;
+}
+// n values in a window over all bf16 values that starts at position lo.
+__device__ __noinline__ Seen count_in_window(uint4 w, int n, int lo, uint32_t* hist, Seen seen) {
+#pragma unroll 1
+  for (int q = 0; q < n; ++q) {
+    const uint32_t b = w.x & 0xffffu;
+    w.x = __funnelshift_r(w.x, w.y, 16);
+    w.y = __funnelshift_r(w.y, w.z, 16);
+    w.z = __funnelshift_r(w.z, w.w, 16);
+    w.w >>= 16;
+    const int k = full_key(b) - lo;
+    if (k >= 0 && k < kBinsPad && !is_masked(b)) {
+      atomicAdd(&hist[k], 1u);
+      seen.top = min(seen.top, full_key(b));
+    }
+  }
+  return seen;
 }
 
 // Zeroes the histogram and counts the slice's values of window `win` in it.
+template <int kThr>
 __device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* hist) {
   Seen seen;
+  __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(0xff80u), __ushort_as_bfloat16(0xff80u));
   const uint4* v = sl.vec();
   bool zeroed = false;
-  for (int64_t i0 = sl.v0 + threadIdx.x; !zeroed || i0 < sl.v1; i0 += kBatch * kSThreads) {
+  for (int64_t i0 = sl.v0 + threadIdx.x; !zeroed || i0 < sl.v1; i0 += kBatch * kThr) {
     uint4 w[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (i0 + k * kSThreads < sl.v1) w[k] = v[i0 + k * kSThreads];
+      if (i0 + k * kThr < sl.v1) w[k] = v[i0 + k * kThr];
     if (!zeroed) {  // while the first loads are under way
       uint4* h = reinterpret_cast<uint4*>(hist);
-      for (int i = threadIdx.x; i < kBinsPad / 4; i += kSThreads) h[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < kBinsPad / 4; i += kThr) h[i] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       zeroed = true;
     }
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (i0 + k * kSThreads >= sl.v1) continue;
-      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+      if (i0 + k * kThr >= sl.v1) continue;
       if (win == kDirect) {
-        bool all = true;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          all &= count_in_range(ws[q] & 0xffffu, hist, seen);
-          all &= count_in_range(ws[q] >> 16, hist, seen);
-        }
-        if (!all) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t b = q & 1 ? ws[q / 2] >> 16 : ws[q / 2] & 0xffffu;
-            const uint32_t mag = b & 0x7fffu;
-            if (mag < kMagLo || mag > kMagHi) count_rest(b, hist, seen);
-          }
+        const uint32_t a0 = w[k].x & 0x7fff7fffu, a1 = w[k].y & 0x7fff7fffu;
+        const uint32_t a2 = w[k].z & 0x7fff7fffu, a3 = w[k].w & 0x7fff7fffu;
+        const uint32_t lo = __vminu2(__vminu2(a0, a1), __vminu2(a2, a3));
+        const uint32_t hi = __vmaxu2(__vmaxu2(a0, a1), __vmaxu2(a2, a3));
+        if (__vminu2(lo, kMagLo * 0x10001u) == kMagLo * 0x10001u &&
+            __vmaxu2(hi, kMagHi * 0x10001u) == kMagHi * 0x10001u) {
+          const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(&w[k]);
+          most = __hmax2(most, __hmax2(__hmax2(f[0], f[1]), __hmax2(f[2], f[3])));
+          count_pairs(w[k], hist);
+        } else {
+          seen = count_any(w[k], 8, hist, seen);
         }
       } else {
-#pragma unroll 1
-        for (int q = 0; q < 8; ++q) {
-          const uint32_t b = (ws[q / 2] >> (16 * (q & 1))) & 0xffffu;
-          count_in_window(b, win * kBinsPad, hist, seen);
-        }
+        seen = count_in_window(w[k], 8, win * kBinsPad, hist, seen);
       }
     }
   }
   if (threadIdx.x < sl.n_head + sl.n_tail) {
     const int i = threadIdx.x;
     const uint32_t b = i < sl.n_head ? sl.x[i] : sl.tail()[i - sl.n_head];
-    if (win != kDirect)
-      count_in_window(b, win * kBinsPad, hist, seen);
-    else if (!count_in_range(b, hist, seen))
-      count_rest(b, hist, seen);
+    const uint4 one = make_uint4(b, 0u, 0u, 0u);
+    seen = win == kDirect ? count_any(one, 1, hist, seen)
+                          : count_in_window(one, 1, win * kBinsPad, hist, seen);
   }
+  const __nv_bfloat16 m = __hmax(__low2bfloat16(most), __high2bfloat16(most));
+  if (win == kDirect && __bfloat16_as_ushort(m) != 0xff80u)
+    seen.top = min(seen.top, full_key(__bfloat16_as_ushort(m)));
   return seen;
 }
 
 // ------------------------------------------------------------ one row
-template <int kC>
+template <int kC, int kThr>
 struct Row {
+  static constexpr int kWarps = kThr / 32;
   static constexpr int kShare = kBinsPad / kC;  // bins that a CTA sums over the cluster
-  static constexpr int kVec = (kShare / 4 + kSThreads - 1) / kSThreads;  // 16-byte vectors a thread
+  static constexpr int kVec = (kShare / 4 + kThr - 1) / kThr;  // 16-byte vectors of a thread
   static constexpr int kOwn = 4 * kVec;         // bins of one thread
-  static_assert(kOwn <= 32, "one lane per bin in a crossing");
+  static constexpr int kLaneBins = (kOwn + 31) / 32;  // of them, a lane's in a crossing
 
   uint32_t* hist;
   RowShared* sh;
   int cta;
   float t, z_max, x_max, min_p;
+  ScaleDiv div;     // z = x / t
   int fix;
   int window;       // what the histogram holds
-  int top;          // the window's smallest occupied bin, kNoBin if none
+  int top;          // the window's smallest position, kNone if it is empty
   int flags;        // what the row holds outside the direct range
   int turn;         // which of the two result slots is next
   // this thread's bins in the built window: what comes before them, and their totals
-  u64 c0, cn, m0, mn;
+  u64 m0, mn;
+  uint32_t c0, cn;
 
   __device__ __forceinline__ int bin_key(int bin) const {
     if (window != kDirect) return window * kBinsPad + bin;
@@ -297,10 +330,18 @@ struct Row {
     x_max = key_value(key);
     z_max = __fdiv_rn(x_max, t);
   }
+  // x / t rounded to nearest; in the direct range ScaleDiv's short form holds
+  // for every usual temperature (zero divides exactly)
+  __device__ __forceinline__ float divide(float v) const {
+    if (window != kDirect || div.r == 0.f) return __fdiv_rn(v, t);
+    float lo, hi;
+    f2_unpack(div.fast_quotient2(f2_pack(v, v)), lo, hi);
+    return lo;
+  }
   // exp(z - m) of one value in fp32, and as an integer
   __device__ __forceinline__ float weight(float v) const {
     if (v == x_max) return 1.f;
-    const float z = __fdiv_rn(v, t);
+    const float z = divide(v);
     const float d = __fsub_rn(z, z_max);
     if (!(d > -45.f)) return 0.f;
     // what the subtraction rounded off (Knuth's two-sum)
@@ -320,18 +361,18 @@ struct Row {
     window = win;
     if (threadIdx.x == 0) {
       sh->flags = 0;
-      sh->top = kNoBin;
+      sh->top = kNone;
     }
-    const Seen seen = count_slice(sl, win, hist);  // its barrier also covers the two above
+    const Seen seen = count_slice<kThr>(sl, win, hist);  // its barrier also covers the two above
     const int f = __reduce_or_sync(0xffffffffu, seen.flags);
     const int b = __reduce_min_sync(0xffffffffu, seen.top);
     if ((threadIdx.x & 31) == 0) {
       if (f) atomicOr(&sh->flags, f);
-      if (b != kNoBin) atomicMin(&sh->top, b);
+      if (b != kNone) atomicMin(&sh->top, b);
     }
     row_sync<kC>();
     flags = 0;
-    top = kNoBin;
+    top = kNone;
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
       flags |= static_cast<int>(ld_peer_u32(peer<kC>(&sh->flags, c)));
@@ -343,52 +384,50 @@ struct Row {
   // reads that share here), weighs them, and returns the window's totals. x_max
   // must be set.
   __device__ __forceinline__ Totals finish() {
-    uint4* h = reinterpret_cast<uint4*>(hist + cta * kShare) + threadIdx.x * kVec;
-    uint4 n[kVec];
-    u64 q = 0;
-    cn = mn = 0;
+    const int first = static_cast<int>(threadIdx.x) * kVec;  // this thread's vectors
+    const int n_vec = max(0, min(kVec, kShare / 4 - first));
+    uint4* h = reinterpret_cast<uint4*>(hist + cta * kShare) + first;
+    if constexpr (kC > 1) {
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      n[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (static_cast<int>(threadIdx.x) * kVec + k < kShare / 4) {
-        if constexpr (kC > 1) {
+      for (int k = 0; k < kVec; ++k) {
+        if (k < n_vec) {
           uint4 v[kC];
 #pragma unroll
           for (int c = 0; c < kC; ++c) v[c] = ld_peer_v4(peer<kC>(h + k, c));
 #pragma unroll
-          for (int c = 0; c < kC; ++c) {
-            n[k].x += v[c].x;
-            n[k].y += v[c].y;
-            n[k].z += v[c].z;
-            n[k].w += v[c].w;
+          for (int c = 1; c < kC; ++c) {
+            v[0].x += v[c].x;
+            v[0].y += v[c].y;
+            v[0].z += v[c].z;
+            v[0].w += v[c].w;
           }
-          h[k] = n[k];
-        } else {
-          n[k] = h[k];
+          h[k] = v[0];
         }
       }
     }
-    const int bin0 = cta * kShare + threadIdx.x * kOwn;
-#pragma unroll
-    for (int k = 0; k < kVec; ++k) {
-      const uint32_t ns[4] = {n[k].x, n[k].y, n[k].z, n[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (ns[j]) {
-          const float w = weight(key_value(bin_key(bin0 + 4 * k + j)));
-          const u64 mass = ns[j] * fixed(w);
-          cn += ns[j];
-          mn += mass;
-          if (w >= min_p) q += mass;
-        }
+    u64 q = 0;
+    cn = 0;
+    mn = 0;
+    const int bin0 = cta * kShare + 4 * first;
+#pragma unroll 1
+    for (int i = 0; i < 4 * n_vec; ++i) {
+      const uint32_t n = hist[bin0 + i];
+      if (n) {
+        const float w = weight(key_value(bin_key(bin0 + i)));
+        const u64 mass = n * fixed(w);
+        cn += n;
+        mn += mass;
+        if (w >= min_p) q += mass;
       }
     }
     // exclusive prefixes over the CTA's threads
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    u64 ic = cn, im = mn;
+    uint32_t ic = cn;
+    u64 im = mn;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const u64 oc = __shfl_up_sync(0xffffffffu, ic, off), om = __shfl_up_sync(0xffffffffu, im, off);
+      const uint32_t oc = __shfl_up_sync(0xffffffffu, ic, off);
+      const u64 om = __shfl_up_sync(0xffffffffu, im, off);
       if (lane >= off) {
         ic += oc;
         im += om;
@@ -396,87 +435,101 @@ struct Row {
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-    if (lane == 31) {
-      sh->warp_c[warp] = ic;
-      sh->warp_m[warp] = im;
-      sh->warp_q[warp] = q;
-    }
+    if (lane == 31) sh->warp[warp] = Totals{im, q, ic};
     __syncthreads();
     c0 = ic - cn;
     m0 = im - mn;
     Totals mine{0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kSWarps; ++w) {
+#pragma unroll 4
+    for (int w = 0; w < kWarps; ++w) {
+      const Totals t = sh->warp[w];
       if (w < warp) {
-        c0 += sh->warp_c[w];
-        m0 += sh->warp_m[w];
+        c0 += t.count;
+        m0 += t.mass;
       }
-      mine.count += sh->warp_c[w];
-      mine.mass += sh->warp_m[w];
-      mine.kept += sh->warp_q[w];
+      mine.count += t.count;
+      mine.mass += t.mass;
+      mine.kept += t.kept;
+    }
+    if constexpr (kC == 1) {
+      __syncthreads();  // the warps' totals have been read
+      return mine;
     }
     if (threadIdx.x < kC) {
       const uint32_t to = peer<kC>(&sh->part[cta], threadIdx.x);
-      st_peer_u64(to, mine.count);
-      st_peer_u64(to + 8, mine.mass);
-      st_peer_u64(to + 16, mine.kept);
+      st_peer_u64(to, mine.mass);
+      st_peer_u64(to + 8, mine.kept);
+      st_shared_cluster_u32(to + 16, mine.count);
     }
     row_sync<kC>();
     Totals all{0, 0, 0};
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
+      const Totals t = sh->part[c];
       if (c < cta) {
-        c0 += sh->part[c].count;
-        m0 += sh->part[c].mass;
+        c0 += t.count;
+        m0 += t.mass;
       }
-      all.count += sh->part[c].count;
-      all.mass += sh->part[c].mass;
-      all.kept += sh->part[c].kept;
+      all.count += t.count;
+      all.mass += t.mass;
+      all.kept += t.kept;
     }
     return all;
   }
 
-  // The token of rank `at` in the built window (kMass false), or where its
+  // The token of rank `at` in the built window (by_mass false), or where its
   // running mass passes `at`. The thread that owns the crossing's bins has its
-  // warp look at them, one lane each, and tells every CTA. With kLast the CTA that
-  // holds the token is told to look for it.
-  template <bool kMass, bool kLast>
-  __device__ __forceinline__ Crossing cross(u64 at) {
+  // warp look at them and tells every CTA. With `last` the CTA that holds the
+  // token is told to look for it.
+  __device__ __forceinline__ Crossing cross(bool by_mass, bool last, u64 at) {
     const int lane = threadIdx.x & 31;
-    const bool mine = kMass ? m0 <= at && at - m0 < mn : c0 <= at && at - c0 < cn;
+    const bool mine = by_mass ? m0 <= at && at - m0 < mn : c0 <= at && at - c0 < cn;
     const uint32_t who = __ballot_sync(0xffffffffu, mine);
     if (who) {
       const int src = __ffs(who) - 1;
-      const u64 bm = __shfl_sync(0xffffffffu, m0, src), bc = __shfl_sync(0xffffffffu, c0, src);
-      const int bin = cta * kShare + ((threadIdx.x & ~31) + src) * kOwn + lane;
-      // a thread's last vectors may lie beyond the share: it counted none of them
-      const u64 n = lane < kOwn && bin < (cta + 1) * kShare ? hist[bin] : 0u;
-      const u64 w = n ? fixed(weight(key_value(bin_key(bin)))) : 0u;
-      u64 c = n, m = n * w;
+      u64 m = __shfl_sync(0xffffffffu, m0, src);
+      uint32_t c = __shfl_sync(0xffffffffu, c0, src);
+      const int bin0 = cta * kShare + ((threadIdx.x & ~31) + src) * kOwn;
+      u64 upto = 0;
+      uint32_t rank = 0;
+      int hit = -1;
+#pragma unroll 1
+      for (int i = 0; i < kLaneBins; ++i) {
+        const int bin = bin0 + 32 * i + lane;
+        // a thread's last vectors may lie beyond the share: it counted none of them
+        const uint32_t n = 32 * i + lane < kOwn && bin < (cta + 1) * kShare ? hist[bin] : 0u;
+        const u64 w = n ? fixed(weight(key_value(bin_key(bin)))) : 0u;
+        uint32_t ic = n;
+        u64 im = n * w;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const u64 oc = __shfl_up_sync(0xffffffffu, c, off);
-        const u64 om = __shfl_up_sync(0xffffffffu, m, off);
-        if (lane >= off) {
-          c += oc;
-          m += om;
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t oc = __shfl_up_sync(0xffffffffu, ic, off);
+          const u64 om = __shfl_up_sync(0xffffffffu, im, off);
+          if (lane >= off) {
+            ic += oc;
+            im += om;
+          }
         }
+        const u64 before = by_mass ? m + im - n * w : static_cast<u64>(c + ic - n);
+        const bool here = before <= at && at - before < (by_mass ? n * w : static_cast<u64>(n));
+        const uint32_t at_lane = __ballot_sync(0xffffffffu, here);
+        if (at_lane) {
+          u64 j = at - before;  // the rank among the bin's tokens
+          if (by_mass && here) {
+            const u64 rest = j;
+            j = static_cast<u64>(__fdividef(static_cast<float>(rest), static_cast<float>(w)));
+            while (j * w > rest) --j;
+            while ((j + 1) * w <= rest) ++j;
+          }
+          const int l = __ffs(at_lane) - 1;
+          upto = __shfl_sync(0xffffffffu, m + im - n * w + (j + 1) * w, l);
+          rank = __shfl_sync(0xffffffffu, static_cast<uint32_t>(j), l);
+          hit = bin0 + 32 * i + l;
+          break;
+        }
+        m += __shfl_sync(0xffffffffu, im, 31);
+        c += __shfl_sync(0xffffffffu, ic, 31);
       }
-      c += bc - n;  // before this bin
-      m += bm - n * w;
-      const bool here = kMass ? m <= at && at - m < n * w : c <= at && at - c < n;
-      const int at_lane = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
-      // the rank among the bin's tokens; the quotient is below 2^32
-      u64 j = at - c;
-      if (kMass && here) {
-        const u64 rest = at - m;
-        j = static_cast<u64>(__fdividef(static_cast<float>(rest), static_cast<float>(w)));
-        while (j * w > rest) --j;
-        while ((j + 1) * w <= rest) ++j;
-      }
-      const u64 upto = __shfl_sync(0xffffffffu, m + (j + 1) * w, at_lane);
-      uint32_t rank = __shfl_sync(0xffffffffu, static_cast<uint32_t>(j), at_lane);
-      const int hit = __shfl_sync(0xffffffffu, bin, at_lane);
       const int key = bin_key(hit);
       if (lane < kC) {
         const uint32_t to = peer<kC>(&sh->found[turn], lane);
@@ -484,19 +537,20 @@ struct Row {
         st_peer_u64(to + 8, static_cast<u64>(static_cast<uint32_t>(key)) |
                                 (static_cast<u64>(rank) << 32));
       }
-      if constexpr (kLast) {
-        // each CTA's own count: this CTA's was replaced by the sum
-        uint32_t own = lane < kC && lane != cta ? ld_peer_u32(peer<kC>(hist + hit, min(lane, kC - 1))) : 0u;
+      if (last) {
+        // each CTA's own count of the value: this CTA's was replaced by the sum
+        uint32_t own = 0;
+        if (lane < kC && lane != cta) own = ld_peer_u32(peer<kC>(hist + hit, min(lane, kC - 1)));
         const uint32_t others = __reduce_add_sync(0xffffffffu, own);
         if (lane == cta) own = hist[hit] - others;
-        uint32_t upto_c = own;
+        uint32_t to = own;
 #pragma unroll
         for (int off = 1; off < kC; off <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, upto_c, off);
-          if (lane >= off) upto_c += o;
+          const uint32_t o = __shfl_up_sync(0xffffffffu, to, off);
+          if (lane >= off) to += o;
         }
-        if (lane < kC && rank >= upto_c - own && rank < upto_c) {
-          st_shared_cluster_u32(peer<kC>(&sh->cmd_rank, lane), rank - (upto_c - own));
+        if (lane < kC && rank >= to - own && rank < to) {
+          st_shared_cluster_u32(peer<kC>(&sh->cmd_rank, lane), rank - (to - own));
           st_shared_cluster_u32(peer<kC>(&sh->cmd_key, lane), static_cast<uint32_t>(key));
         }
       }
@@ -528,91 +582,104 @@ __device__ __forceinline__ u64 scaled_floor(float f, u64 m, bool& exact) {
   return (hi << (64 - s)) | (lo >> s);
 }
 
-// Index in the row of the slice's rank-th element (from 0) with this key.
-// A batch's matches are counted per vector row and warp, in index order.
+// One bit per matching half of a word: `mask` drops the sign where zero is sought.
+__device__ __forceinline__ uint32_t match2(uint32_t w, uint32_t mask, uint32_t want) {
+  return __vcmpeq2(w & mask, want) & 0x00010001u;
+}
+// Whether a vector holds a match at all, in fewer steps.
+__device__ __forceinline__ bool any_match(const uint4& w, uint32_t mask, uint32_t want) {
+  const uint32_t m = __vminu2(__vminu2((w.x & mask) ^ want, (w.y & mask) ^ want),
+                              __vminu2((w.z & mask) ^ want, (w.w & mask) ^ want));
+  return (m & 0xffffu) == 0u || m < 0x10000u;
+}
+// The matches of a vector: word k's halves at bits k and 16 + k.
+__device__ __forceinline__ uint32_t match8(const uint4& w, uint32_t mask, uint32_t want) {
+  return match2(w.x, mask, want) | (match2(w.y, mask, want) << 1) |
+         (match2(w.z, mask, want) << 2) | (match2(w.w, mask, want) << 3);
+}
+
+// Index in the row of the slice's rank-th element (from 0) with this key. Each
+// warp counts a contiguous run of the slice's vectors; the one that holds the
+// element looks again.
+template <int kThr>
 __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int key,
                                             uint32_t rank) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto match = [&](uint32_t b) { return full_key(b) == key ? 1u : 0u; };
-  // the elements before and after the vectors: every warp counts the former
-  const uint32_t h = __ballot_sync(0xffffffffu, lane < sl.n_head && match(sl.x[lane]));
-  if (rank < __popc(h)) {
-    uint32_t m = h;
-    for (uint32_t s = rank; s > 0; --s) m &= m - 1;
-    return __ffs(m) - 1;
-  }
-  uint32_t left = rank - __popc(h);
-  for (int64_t i0 = sl.v0; i0 < sl.v1; i0 += kBatch * kSThreads) {
-    uint4 w[kBatch];
-    uint32_t bits[kBatch];
+  const uint32_t bits = __float_as_uint(key_value(key)) >> 16;
+  const uint32_t want = bits | (bits << 16);
+  const uint32_t mask = bits ? 0xffffffffu : 0x7fff7fffu;
+  auto element = [&](const uint16_t* x) { return (*x & mask & 0xffffu) == bits; };
+  // the elements before the vectors (every warp alike)
+  uint32_t at = __ballot_sync(0xffffffffu, lane < sl.n_head && element(sl.x + min(lane, 7)));
+  uint32_t left = rank;
+  if (left >= __popc(at)) {
+    left -= __popc(at);
+    const int64_t per = (sl.v1 - sl.v0 + kThr / 32 - 1) / (kThr / 32);
+    const int64_t b = min(sl.v1, sl.v0 + per * warp), e = min(sl.v1, b + per);
+    const uint4* v = sl.vec();
+    uint32_t n = 0;
+    int64_t i = b + lane;
+    for (; i + 96 < e; i += 128) {
+      uint4 w[4];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int64_t i = i0 + k * kSThreads + threadIdx.x;
-      if (i < sl.v1) w[k] = sl.vec()[i];
+      for (int k = 0; k < 4; ++k) w[k] = v[i + 32 * k];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (any_match(w[k], mask, want)) n += __popc(match8(w[k], mask, want));
     }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int64_t i = i0 + k * kSThreads + threadIdx.x;
-      bits[k] = 0;
-      if (i < sl.v1) {
-        const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          bits[k] |= (match(ws[q] & 0xffffu) << (2 * q)) | (match(ws[q] >> 16) << (2 * q + 1));
-      }
-      const uint32_t n = __reduce_add_sync(0xffffffffu, __popc(bits[k]));
-      if (lane == 0) sh->hits[k][warp] = n;
-    }
+    for (; i < e; i += 32) n += __popc(match8(v[i], mask, want));
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sh->hits[warp] = n;
     __syncthreads();
-    uint32_t before = 0, at_k = kBatch, at_w = 0, at_before = 0;
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-#pragma unroll
-      for (int x = 0; x < kSWarps; ++x) {
-        const uint32_t n = sh->hits[k][x];
-        if (at_k == kBatch && left < before + n) {
-          at_k = k;
-          at_w = x;
-          at_before = before;
-        }
-        before += n;
-      }
+    uint32_t before = 0, all = 0;
+#pragma unroll 4
+    for (int x = 0; x < kThr / 32; ++x) {
+      const uint32_t h = sh->hits[x];
+      before += x < warp ? h : 0u;
+      all += h;
     }
-    if (at_k < kBatch) {
-      if (warp == static_cast<int>(at_w)) {
-        uint32_t mine = 0;
+    if (left < all) {
+      if (left >= before && left - before < n) {
+        left -= before;
+        for (int64_t i0 = b; i0 < e; i0 += 32) {
+          uint32_t m = i0 + lane < e ? match8(v[i0 + lane], mask, want) : 0u;
+          uint32_t inc = __popc(m);
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-          if (k == static_cast<int>(at_k)) mine = bits[k];
-        uint32_t inc = __popc(mine);
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-          if (lane >= off) inc += o;
-        }
-        const uint32_t want = left - at_before, low = inc - __popc(mine);
-        if (low <= want && want < inc) {
-          for (uint32_t s = want - low; s > 0; --s) mine &= mine - 1;
-          sh->index = sl.head + 8 * (i0 + at_k * kSThreads + threadIdx.x) + __ffs(mine) - 1;
+          for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += o;
+          }
+          const uint32_t step = __shfl_sync(0xffffffffu, inc, 31);
+          if (left < step) {
+            const uint32_t low = inc - __popc(m);
+            if (low <= left && left < inc) {
+              uint32_t in_order = 0;  // bit k: element k of the lane's vector
+              for (int k = 0; k < 8; ++k) in_order |= ((m >> (16 * (k & 1) + k / 2)) & 1u) << k;
+              for (uint32_t s = left - low; s > 0; --s) in_order &= in_order - 1;
+              sh->index = sl.head + 8 * (i0 + lane) + __ffs(in_order) - 1;
+            }
+            break;
+          }
+          left -= step;
         }
       }
       __syncthreads();
       return sh->index;
     }
-    left -= before;
-    __syncthreads();  // the counts have been read
+    left -= all;
+    at = __ballot_sync(0xffffffffu, lane < sl.n_tail && element(sl.tail() + min(lane, 7)));
+    for (; left > 0; --left) at &= at - 1;
+    return sl.tail() - sl.x + __ffs(at) - 1;
   }
-  const uint32_t m0 = __ballot_sync(0xffffffffu, lane < sl.n_tail && match(sl.tail()[lane]));
-  uint32_t m = m0;
-  for (uint32_t s = left; s > 0; --s) m &= m - 1;
-  return sl.tail() - sl.x + __ffs(m) - 1;
+  for (; left > 0; --left) at &= at - 1;
+  return __ffs(at) - 1;
 }
 
 // One row per cluster of kC CTAs, each counting a contiguous part of it, each
 // weighing a share of the bins; every step that needs the whole row ends with a
 // cluster barrier, after which all CTAs hold the same numbers and go the same way.
-template <int kC>
-__global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleParams p) {
+template <int kC, int kThr, int kMin>
+__global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p) {
   __shared__ __align__(16) uint32_t hist[kBinsPad];
   __shared__ RowShared sh;
   const int cta = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -625,114 +692,109 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleParams
     }
     return;  // the whole cluster leaves
   }
-  const bool greedy = s.t == 0.f;
   const Slice sl(p.logits + row * p.ld, p.V, cta, kC);
-  Row<kC> r;
+  Row<kC, kThr> r;
   r.hist = hist;
   r.sh = &sh;
   r.cta = cta;
-  r.t = greedy ? 1.f : s.t;
+  r.t = s.t == 0.f ? 1.f : s.t;
+  r.div = ScaleDiv::make(r.t);
   r.min_p = s.min_p;
   r.fix = p.fix;
   r.turn = 0;
   if (threadIdx.x == 0) sh.cmd_key = -1;
 
-  r.count(sl, kDirect);
-  if (r.top != kNoBin) r.set_max(r.bin_key(r.top));
-  // does a value outside the direct range matter?
-  const bool none = r.top == kNoBin;
-  const bool windows =
-      (r.flags & 1) ||
-      ((r.flags & 2) && (none || !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail))) ||
-      ((r.flags & 4) && (none || !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail)));
-  if (none && !windows) {  // nothing to draw
-    if (cta == 0 && threadIdx.x == 0) {
-      p.token[row] = -1;
-      if (p.logprob) p.logprob[row] = 0.f;
-    }
-    row_sync<kC>();  // the others have read this CTA's flags
-    return;
-  }
-
+  // The row's totals, from the direct range or window by window; then three
+  // crossings, each in the window that holds it (built again if need be).
   Totals all{0, 0, 0};
-  u64 wc[kWindows], wm[kWindows];
-  const int n_win = windows ? kWindows : 1;
-  if (!windows) {
-    all = r.finish();
-    wc[0] = all.count;
-    wm[0] = all.mass;
-  } else {
-    row_sync<kC>();
-    bool any = false;
+  uint32_t wc[kWindows];
+  u64 wm[kWindows];
+  int n_win = 1, win = kDirect;
+  bool max_known = false, totals = true;
+  int step = s.t == 0.f ? 2 : 0;  // 0: top-k, 1: top-p, 2: the draw
+  u64 kept = 0;
+  Crossing c{0, -1, 0};
 #pragma unroll 1
-    for (int w = 0; w < kWindows; ++w) {
-      r.count(sl, w);
-      if (!any && r.top != kNoBin) {
-        r.set_max(r.bin_key(r.top));
-        any = true;
-      }
-      if (!any) {
-        wc[w] = wm[w] = 0;
-        row_sync<kC>();
+  while (step < 3) {
+    r.count(sl, win);
+    if (!max_known && r.top != kNone) r.set_max(r.top);
+    if (win == kDirect) {
+      // does a value outside the direct range matter?
+      const bool none = r.top == kNone;
+      if ((r.flags & 1) ||
+          ((r.flags & 2) && (none || !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail))) ||
+          ((r.flags & 4) && (none || !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail)))) {
+        n_win = kWindows;
+        win = 0;
+        row_sync<kC>();  // the others have read this CTA's counts
         continue;
       }
-      const Totals a = r.finish();
+      if (none) {  // nothing to draw
+        if (cta == 0 && threadIdx.x == 0) {
+          p.token[row] = -1;
+          if (p.logprob) p.logprob[row] = 0.f;
+        }
+        row_sync<kC>();
+        return;
+      }
+    }
+    max_known |= r.top != kNone;
+    const Totals a = r.finish();
+    if (totals) {
+      const int w = max(win, 0);
       wc[w] = a.count;
       wm[w] = a.mass;
       all.count += a.count;
       all.mass += a.mass;
       all.kept += a.kept;
-    }
-  }
-  auto enter = [&](int w) {  // make window w the built one
-    if (!windows || r.window == w) return;
-    r.count(sl, w);
-    r.finish();
-  };
-  // the window where the running mass passes `at`, and the mass before it
-  auto find_mass = [&](u64 at, u64& before) {
-    int w = 0;
-    before = 0;
-    while (w + 1 < n_win && at - before >= wm[w]) before += wm[w++];
-    return w;
-  };
-
-  u64 at = 0;  // the draw: the first token whose running mass exceeds it
-  if (!greedy) {
-    u64 kept = all.mass, before;
-    bool exact;
-    if (s.top_k > 0 && static_cast<u64>(s.top_k) < all.count) {
-      u64 c = 0, m = 0;
-      int w = 0;
-      while (static_cast<u64>(s.top_k) - c > wc[w]) {
-        c += wc[w];
-        m += wm[w++];
+      if (w + 1 < n_win) {
+        ++win;
+        continue;
       }
-      enter(w);
-      kept = m + r.template cross<false, false>(s.top_k - c - 1).upto;
+      totals = false;
+      kept = all.mass;
     }
-    if (s.top_p < 1.f) {
-      u64 reach = scaled_floor(s.top_p, kept, exact);
-      if (!exact) ++reach;
-      reach = reach < 1 ? 1 : reach;
-      const int w = find_mass(reach - 1, before);
-      enter(w);
-      kept = before + r.template cross<true, false>(reach - 1 - before).upto;
+#pragma unroll 1
+    for (; step < 3; ++step) {
+      u64 at, before = 0;
+      bool exact;
+      int w = 0;
+      if (step == 0) {
+        if (s.top_k == 0 || static_cast<uint32_t>(s.top_k) >= all.count) continue;
+        at = static_cast<u64>(s.top_k) - 1;
+        u64 counted = 0;
+        while (w + 1 < n_win && at - counted >= wc[w]) {
+          counted += wc[w];
+          before += wm[w++];
+        }
+        at -= counted;
+      } else {
+        if (step == 1) {
+          if (!(s.top_p < 1.f)) continue;
+          at = scaled_floor(s.top_p, kept, exact);
+          if (exact && at > 0) --at;  // the token that brings the mass to at + 1 or more
+        } else {
+          if (all.kept < kept) kept = all.kept;
+          at = s.t == 0.f ? 0 : scaled_floor(s.u, kept, exact);
+          if (s.t != 0.f && at >= kept) at = kept - 1;
+        }
+        while (w + 1 < n_win && at - before >= wm[w]) before += wm[w++];
+        at -= before;
+      }
+      if (n_win > 1 && r.window != w) {
+        win = w;
+        break;
+      }
+      c = r.cross(step > 0, step == 2, at);
+      kept = before + c.upto;
     }
-    if (all.kept < kept) kept = all.kept;
-    at = scaled_floor(s.u, kept, exact);
-    if (at >= kept) at = kept - 1;
   }
-  u64 before;
-  const int w_at = find_mass(at, before);
-  enter(w_at);
-  const Crossing c = r.template cross<true, true>(at - before);
   // no CTA reads another's memory from here on
   if (sh.cmd_key >= 0) {
-    const int64_t index = index_of(sl, &sh, sh.cmd_key, sh.cmd_rank);
+    const int64_t index = index_of<kThr>(sl, &sh, sh.cmd_key, sh.cmd_rank);
     if (threadIdx.x == 0) p.token[row] = static_cast<int32_t>(index);
   }
-  if (p.logprob && cta == kC - 1 && threadIdx.x == kSThreads - 1) {
+  if (p.logprob && cta == kC - 1 && threadIdx.x == kThr - 1) {
     // d - ln(mass * 2^-fix), the logarithm as that of a number in [1, 2) and a
     // multiple of ln 2 whose first part is exact
     const float v = key_value(c.key);
@@ -749,11 +811,11 @@ __global__ void __launch_bounds__(kSThreads, 2) sample_kernel(const SampleParams
   }
 }
 
-template <int kC>
+template <int kC, int kThr, int kMin>
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
-  cfg.blockDim = dim3(kSThreads);
+  cfg.blockDim = dim3(kThr);
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -762,7 +824,7 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<kC>, p);
+  return cudaLaunchKernelEx(&cfg, sample_kernel<kC, kThr, kMin>, p);
 }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -827,13 +889,13 @@ extern "C" int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64
     KernelTimer timer(K_SAMPLE, st);
     const int64_t slots = 2 * static_cast<int64_t>(sms);  // CTAs at work at once
     if (T * 8 <= slots)
-      e = launch_sample<8>(p, st);
+      e = launch_sample<8, 512, 1>(p, st);
     else if (T * 4 <= slots)
-      e = launch_sample<4>(p, st);
+      e = launch_sample<4, 512, 2>(p, st);
     else if (T * 2 <= slots)
-      e = launch_sample<2>(p, st);
+      e = launch_sample<2, 512, 2>(p, st);
     else
-      e = launch_sample<1>(p, st);
+      e = launch_sample<1, 256, 4>(p, st);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) {
