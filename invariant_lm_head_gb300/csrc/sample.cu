@@ -102,30 +102,32 @@ struct Settings {
   }
 };
 
-// Where the running count or mass passes a point: the value's key, the token's
-// rank among its equals, the mass up to and with it.
-struct Crossing {
-  u64 upto;
-  int key;
-  uint32_t rank;
-};
-
 struct Totals {
   u64 mass, kept;  // kept: the mass that min-p keeps
   uint32_t count;
 };
 
+// The histogram is weighed in rows of 32 bins.
+constexpr int kRows = kBinsPad / 32;
+constexpr int kGroups = 16;  // of a warp's part of a slice, in the search for an index
+
 struct RowShared {
-  Totals part[kMaxC];       // every CTA's share of the built window
-  Crossing found[2];
+  u64 row_m[kRows];         // CTA 0: mass and count of every row of bins
+  uint32_t row_c[kRows];
+  u64 kept[kMaxC];          // CTA 0: every CTA's share of the mass that min-p keeps
+  int2 seen[kMaxC];         // every CTA's flags and largest value's position
   Totals warp[kMaxWarps];
-  uint32_t hits[kMaxWarps];
+  u64 found;                // a crossing: the mass up to and with its token,
+  int found_bin;            // its bin,
+  uint32_t found_rank;      // and the token's rank among the bin's
+  int4 order;               // from CTA 0: what comes next (kLook, kBuild, kDone), and for kLook
+                            // the CTA that holds the token, its key, its rank there
+  uint32_t hits[kMaxWarps][kGroups];
   int64_t index;
   int flags;                // 1: above the direct range, 2: tiny, 4: below the range
   int top;                  // smallest position of the CTA's own values
-  int cmd_key;              // the token to look for: its key (-1: not in this CTA)
-  uint32_t cmd_rank;        // and its rank among the CTA's own tokens of that key
 };
+constexpr int kLook = 0, kBuild = 1, kDone = 2;
 
 // ------------------------------------------------------------ the cluster
 template <int kC>
@@ -140,18 +142,15 @@ template <int kC>
 __device__ __forceinline__ uint32_t peer(const void* here, int c) {
   return kC > 1 ? mapa_shared(smem_u32(here), static_cast<uint32_t>(c)) : smem_u32(here);
 }
-__device__ __forceinline__ uint4 ld_peer_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
 __device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+__device__ __forceinline__ void st_peer_v4(uint32_t addr, int4 v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
 __device__ __forceinline__ void st_peer_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
@@ -302,10 +301,8 @@ __device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* 
 template <int kC, int kThr>
 struct Row {
   static constexpr int kWarps = kThr / 32;
-  static constexpr int kShare = kBinsPad / kC;  // bins that a CTA sums over the cluster
-  static constexpr int kVec = (kShare / 4 + kThr - 1) / kThr;  // 16-byte vectors of a thread
-  static constexpr int kOwn = 4 * kVec;         // bins of one thread
-  static constexpr int kLaneBins = (kOwn + 31) / 32;  // of them, a lane's in a crossing
+  static constexpr int kShare = kRows / kC;                    // rows of bins that a CTA sums
+  static constexpr int kOwn = (kRows + kThr - 1) / kThr;       // rows of a thread of CTA 0
 
   uint32_t* hist;
   RowShared* sh;
@@ -316,8 +313,8 @@ struct Row {
   int window;       // what the histogram holds
   int top;          // the window's smallest position, kNone if it is empty
   int flags;        // what the row holds outside the direct range
-  int turn;         // which of the two result slots is next
-  // this thread's bins in the built window: what comes before them, and their totals
+  // CTA 0: what comes before this thread's rows of bins in the built window, and
+  // their own totals
   u64 m0, mn;
   uint32_t c0, cn;
 
@@ -355,73 +352,109 @@ struct Row {
   }
 
   // Counts window `win` of the row over the cluster: afterwards top and flags
-  // are the whole row's. Two barriers follow (finish): between them the CTAs read
-  // each other's counts.
+  // are the whole row's. Another barrier follows (weigh, or the caller's): until
+  // then the CTAs read each other's counts.
   __device__ __forceinline__ void count(const Slice& sl, int win) {
     window = win;
     if (threadIdx.x == 0) {
       sh->flags = 0;
       sh->top = kNone;
     }
-    const Seen seen = count_slice<kThr>(sl, win, hist);  // its barrier also covers the two above
-    const int f = __reduce_or_sync(0xffffffffu, seen.flags);
-    const int b = __reduce_min_sync(0xffffffffu, seen.top);
+    const Seen mine = count_slice<kThr>(sl, win, hist);  // its barrier also covers the two above
+    const int f = __reduce_or_sync(0xffffffffu, mine.flags);
+    const int b = __reduce_min_sync(0xffffffffu, mine.top);
     if ((threadIdx.x & 31) == 0) {
       if (f) atomicOr(&sh->flags, f);
       if (b != kNone) atomicMin(&sh->top, b);
     }
-    row_sync<kC>();
-    flags = 0;
-    top = kNone;
+    __syncthreads();
+    if constexpr (kC == 1) {
+      flags = sh->flags;
+      top = sh->top;
+    } else {
+      // every CTA of the cluster has started: its memory can be written
+      if (win == kDirect) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (threadIdx.x < kC) {
+        const uint32_t to = peer<kC>(&sh->seen[cta], threadIdx.x);
+        st_peer_u64(to, static_cast<u64>(static_cast<uint32_t>(sh->flags)) |
+                            (static_cast<u64>(static_cast<uint32_t>(sh->top)) << 32));
+      }
+      cluster_sync();
+      flags = 0;
+      top = kNone;
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      flags |= static_cast<int>(ld_peer_u32(peer<kC>(&sh->flags, c)));
-      top = min(top, static_cast<int>(ld_peer_u32(peer<kC>(&sh->top, c))));
+      for (int c = 0; c < kC; ++c) {
+        flags |= sh->seen[c].x;
+        top = min(top, sh->seen[c].y);
+      }
     }
   }
 
   // Sums this CTA's share of the bins over the cluster (in place: no one else
-  // reads that share here), weighs them, and returns the window's totals. x_max
-  // must be set.
-  __device__ __forceinline__ Totals finish() {
-    const int first = static_cast<int>(threadIdx.x) * kVec;  // this thread's vectors
-    const int n_vec = max(0, min(kVec, kShare / 4 - first));
-    uint4* h = reinterpret_cast<uint4*>(hist + cta * kShare) + first;
-    if constexpr (kC > 1) {
+  // reads that share here), weighs them, one lane a bin, and leaves every row's
+  // totals in CTA 0, whose threads then hold the prefixes. Returns the window's
+  // totals (in CTA 0). x_max must be set.
+  __device__ __forceinline__ Totals weigh() {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    u64 q = 0;
+#pragma unroll 1
+    for (int row = cta * kShare + warp; row < (cta + 1) * kShare; row += kWarps) {
+      const int bin = 32 * row + lane;
+      uint32_t n = 0;
+      if constexpr (kC > 1) {
+        uint32_t v[kC];
 #pragma unroll
-      for (int k = 0; k < kVec; ++k) {
-        if (k < n_vec) {
-          uint4 v[kC];
+        for (int c = 0; c < kC; ++c) v[c] = ld_peer_u32(peer<kC>(hist + bin, c));
 #pragma unroll
-          for (int c = 0; c < kC; ++c) v[c] = ld_peer_v4(peer<kC>(h + k, c));
-#pragma unroll
-          for (int c = 1; c < kC; ++c) {
-            v[0].x += v[c].x;
-            v[0].y += v[c].y;
-            v[0].z += v[c].z;
-            v[0].w += v[c].w;
-          }
-          h[k] = v[0];
+        for (int c = 0; c < kC; ++c) n += v[c];
+        hist[bin] = n;
+      } else {
+        n = hist[bin];
+      }
+      uint32_t c = 0;
+      u64 m = 0;
+      if (__any_sync(0xffffffffu, n)) {
+        if (n) {
+          const float w = weight(key_value(bin_key(bin)));
+          m = n * fixed(w);
+          if (w >= min_p) q += m;
         }
+        c = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
+      }
+      if (lane == 0) {
+        st_peer_u64(peer<kC>(&sh->row_m[row], 0), m);
+        st_shared_cluster_u32(peer<kC>(&sh->row_c[row], 0), c);
       }
     }
-    u64 q = 0;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+    if constexpr (kC == 1) {
+      if (lane == 0) sh->warp[warp].kept = q;
+      __syncthreads();
+    } else {
+      if (lane == 0) sh->warp[warp].kept = q;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        u64 all = 0;
+        for (int w = 0; w < kWarps; ++w) all += sh->warp[w].kept;
+        st_peer_u64(peer<kC>(&sh->kept[cta], 0), all);
+      }
+      cluster_sync();
+      if (cta != 0) return Totals{0, 0, 0};
+    }
+    // exclusive prefixes over CTA 0's threads, in order of the rows
     cn = 0;
     mn = 0;
-    const int bin0 = cta * kShare + 4 * first;
-#pragma unroll 1
-    for (int i = 0; i < 4 * n_vec; ++i) {
-      const uint32_t n = hist[bin0 + i];
-      if (n) {
-        const float w = weight(key_value(bin_key(bin0 + i)));
-        const u64 mass = n * fixed(w);
-        cn += n;
-        mn += mass;
-        if (w >= min_p) q += mass;
+#pragma unroll
+    for (int i = 0; i < kOwn; ++i) {
+      const int row = threadIdx.x * kOwn + i;
+      if (row < kRows) {
+        cn += sh->row_c[row];
+        mn += sh->row_m[row];
       }
     }
-    // exclusive prefixes over the CTA's threads
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t ic = cn;
     u64 im = mn;
 #pragma unroll
@@ -433,132 +466,113 @@ struct Row {
         im += om;
       }
     }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
-    if (lane == 31) sh->warp[warp] = Totals{im, q, ic};
+    if (lane == 31) {
+      sh->warp[warp].mass = im;
+      sh->warp[warp].count = ic;
+    }
     __syncthreads();
     c0 = ic - cn;
     m0 = im - mn;
-    Totals mine{0, 0, 0};
+    Totals all{0, 0, 0};
 #pragma unroll 4
     for (int w = 0; w < kWarps; ++w) {
-      const Totals t = sh->warp[w];
+      const Totals x = sh->warp[w];
       if (w < warp) {
-        c0 += t.count;
-        m0 += t.mass;
+        c0 += x.count;
+        m0 += x.mass;
       }
-      mine.count += t.count;
-      mine.mass += t.mass;
-      mine.kept += t.kept;
+      all.count += x.count;
+      all.mass += x.mass;
+      if (kC == 1) all.kept += x.kept;
     }
-    if constexpr (kC == 1) {
-      __syncthreads();  // the warps' totals have been read
-      return mine;
-    }
-    if (threadIdx.x < kC) {
-      const uint32_t to = peer<kC>(&sh->part[cta], threadIdx.x);
-      st_peer_u64(to, mine.mass);
-      st_peer_u64(to + 8, mine.kept);
-      st_shared_cluster_u32(to + 16, mine.count);
-    }
-    row_sync<kC>();
-    Totals all{0, 0, 0};
+    if constexpr (kC > 1) {
 #pragma unroll
-    for (int c = 0; c < kC; ++c) {
-      const Totals t = sh->part[c];
-      if (c < cta) {
-        c0 += t.count;
-        m0 += t.mass;
-      }
-      all.count += t.count;
-      all.mass += t.mass;
-      all.kept += t.kept;
+      for (int c = 0; c < kC; ++c) all.kept += sh->kept[c];
     }
     return all;
   }
 
-  // The token of rank `at` in the built window (by_mass false), or where its
-  // running mass passes `at`. The thread that owns the crossing's bins has its
-  // warp look at them and tells every CTA. With `last` the CTA that holds the
-  // token is told to look for it.
-  __device__ __forceinline__ Crossing cross(bool by_mass, bool last, u64 at) {
+  // CTA 0: the token of rank `at` in the built window (by_mass false), or where
+  // its running mass passes `at`; returns the mass up to and with it, and leaves
+  // its bin and its rank among the bin's tokens in sh. The thread that owns the
+  // crossing's row has its warp look at the bins, one lane each.
+  __device__ __forceinline__ u64 cross(bool by_mass, u64 at) {
     const int lane = threadIdx.x & 31;
     const bool mine = by_mass ? m0 <= at && at - m0 < mn : c0 <= at && at - c0 < cn;
     const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    __syncthreads();  // the last crossing has been read
     if (who) {
       const int src = __ffs(who) - 1;
       u64 m = __shfl_sync(0xffffffffu, m0, src);
       uint32_t c = __shfl_sync(0xffffffffu, c0, src);
-      const int bin0 = cta * kShare + ((threadIdx.x & ~31) + src) * kOwn;
-      u64 upto = 0;
-      uint32_t rank = 0;
-      int hit = -1;
-#pragma unroll 1
-      for (int i = 0; i < kLaneBins; ++i) {
-        const int bin = bin0 + 32 * i + lane;
-        // a thread's last vectors may lie beyond the share: it counted none of them
-        const uint32_t n = 32 * i + lane < kOwn && bin < (cta + 1) * kShare ? hist[bin] : 0u;
-        const u64 w = n ? fixed(weight(key_value(bin_key(bin)))) : 0u;
-        uint32_t ic = n;
-        u64 im = n * w;
+      int row = ((threadIdx.x & ~31) + src) * kOwn;
+      if constexpr (kOwn > 1) {  // which of the thread's rows
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t oc = __shfl_up_sync(0xffffffffu, ic, off);
-          const u64 om = __shfl_up_sync(0xffffffffu, im, off);
-          if (lane >= off) {
-            ic += oc;
-            im += om;
+        for (int i = 1; i < kOwn; ++i) {
+          const u64 rm = sh->row_m[row];
+          const uint32_t rc = sh->row_c[row];
+          if (by_mass ? at - m >= rm : at - c >= rc) {
+            m += rm;
+            c += rc;
+            ++row;
+          } else {
+            break;
           }
         }
-        const u64 before = by_mass ? m + im - n * w : static_cast<u64>(c + ic - n);
-        const bool here = before <= at && at - before < (by_mass ? n * w : static_cast<u64>(n));
-        const uint32_t at_lane = __ballot_sync(0xffffffffu, here);
-        if (at_lane) {
-          u64 j = at - before;  // the rank among the bin's tokens
-          if (by_mass && here) {
-            const u64 rest = j;
-            j = static_cast<u64>(__fdividef(static_cast<float>(rest), static_cast<float>(w)));
-            while (j * w > rest) --j;
-            while ((j + 1) * w <= rest) ++j;
-          }
-          const int l = __ffs(at_lane) - 1;
-          upto = __shfl_sync(0xffffffffu, m + im - n * w + (j + 1) * w, l);
-          rank = __shfl_sync(0xffffffffu, static_cast<uint32_t>(j), l);
-          hit = bin0 + 32 * i + l;
-          break;
-        }
-        m += __shfl_sync(0xffffffffu, im, 31);
-        c += __shfl_sync(0xffffffffu, ic, 31);
       }
-      const int key = bin_key(hit);
-      if (lane < kC) {
-        const uint32_t to = peer<kC>(&sh->found[turn], lane);
-        st_peer_u64(to, upto);
-        st_peer_u64(to + 8, static_cast<u64>(static_cast<uint32_t>(key)) |
-                                (static_cast<u64>(rank) << 32));
-      }
-      if (last) {
-        // each CTA's own count of the value: this CTA's was replaced by the sum
-        uint32_t own = 0;
-        if (lane < kC && lane != cta) own = ld_peer_u32(peer<kC>(hist + hit, min(lane, kC - 1)));
-        const uint32_t others = __reduce_add_sync(0xffffffffu, own);
-        if (lane == cta) own = hist[hit] - others;
-        uint32_t to = own;
+      const int bin = 32 * row + lane;
+      const uint32_t n = ld_peer_u32(peer<kC>(hist + bin, row / kShare));
+      const u64 w = n ? fixed(weight(key_value(bin_key(bin)))) : 0u;
+      uint32_t ic = n;
+      u64 im = n * w;
 #pragma unroll
-        for (int off = 1; off < kC; off <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, to, off);
-          if (lane >= off) to += o;
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t oc = __shfl_up_sync(0xffffffffu, ic, off);
+        const u64 om = __shfl_up_sync(0xffffffffu, im, off);
+        if (lane >= off) {
+          ic += oc;
+          im += om;
         }
-        if (lane < kC && rank >= to - own && rank < to) {
-          st_shared_cluster_u32(peer<kC>(&sh->cmd_rank, lane), rank - (to - own));
-          st_shared_cluster_u32(peer<kC>(&sh->cmd_key, lane), static_cast<uint32_t>(key));
+      }
+      m += im - n * w;  // before this bin
+      c += ic - n;
+      const u64 rest = by_mass ? at - m : at - c;  // huge where the crossing comes before
+      if (rest < (by_mass ? n * w : static_cast<u64>(n))) {
+        u64 j = rest;  // the rank among the bin's tokens
+        if (by_mass) {
+          j = static_cast<u64>(__fdividef(static_cast<float>(rest), static_cast<float>(w)));
+          while (j * w > rest) --j;
+          while ((j + 1) * w <= rest) ++j;
         }
+        sh->found = m + (j + 1) * w;
+        sh->found_bin = bin;
+        sh->found_rank = static_cast<uint32_t>(j);
       }
     }
-    row_sync<kC>();
-    const Crossing r = sh->found[turn];
-    turn ^= 1;
-    return r;
+    __syncthreads();
+    return sh->found;
+  }
+
+  // CTA 0's first warp: who holds the token that the last crossing found, from
+  // the CTAs' own counts of its value (one CTA's was replaced by the sum).
+  __device__ __forceinline__ int4 locate() const {
+    const int lane = threadIdx.x & 31;
+    const int bin = sh->found_bin, summed = bin / 32 / kShare;
+    const uint32_t rank = sh->found_rank;
+    if constexpr (kC == 1) return make_int4(kLook, 0, bin_key(bin), static_cast<int>(rank));
+    uint32_t own = lane < kC ? ld_peer_u32(peer<kC>(hist + bin, min(lane, kC - 1))) : 0u;
+    const uint32_t others = __reduce_add_sync(0xffffffffu, lane == summed ? 0u : own);
+    if (lane == summed) own -= others;
+    uint32_t to = own;
+#pragma unroll
+    for (int off = 1; off < kC; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, to, off);
+      if (lane >= off) to += o;
+    }
+    const uint32_t here = __ballot_sync(0xffffffffu, rank >= to - own && rank < to);
+    const int who = __ffs(here) - 1;
+    const uint32_t there = __shfl_sync(0xffffffffu, rank - (to - own), who);
+    return make_int4(kLook, who, bin_key(bin), static_cast<int>(there));
   }
 };
 
@@ -599,11 +613,12 @@ __device__ __forceinline__ uint32_t match8(const uint4& w, uint32_t mask, uint32
 }
 
 // Index in the row of the slice's rank-th element (from 0) with this key. Each
-// warp counts a contiguous run of the slice's vectors; the one that holds the
-// element looks again.
+// warp counts a contiguous part of the slice's vectors, in groups; the warp that
+// holds the element looks again at its group.
 template <int kThr>
 __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int key,
                                             uint32_t rank) {
+  constexpr int kWarps = kThr / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bits = __float_as_uint(key_value(key)) >> 16;
   const uint32_t want = bits | (bits << 16);
@@ -612,134 +627,148 @@ __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int 
   // the elements before the vectors (every warp alike)
   uint32_t at = __ballot_sync(0xffffffffu, lane < sl.n_head && element(sl.x + min(lane, 7)));
   uint32_t left = rank;
-  if (left >= __popc(at)) {
-    left -= __popc(at);
-    const int64_t per = (sl.v1 - sl.v0 + kThr / 32 - 1) / (kThr / 32);
-    const int64_t b = min(sl.v1, sl.v0 + per * warp), e = min(sl.v1, b + per);
-    const uint4* v = sl.vec();
-    uint32_t n = 0;
-    int64_t i = b + lane;
-    for (; i + 96 < e; i += 128) {
-      uint4 w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w[k] = v[i + 32 * k];
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (any_match(w[k], mask, want)) n += __popc(match8(w[k], mask, want));
-    }
-    for (; i < e; i += 32) n += __popc(match8(v[i], mask, want));
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (lane == 0) sh->hits[warp] = n;
-    __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll 4
-    for (int x = 0; x < kThr / 32; ++x) {
-      const uint32_t h = sh->hits[x];
-      before += x < warp ? h : 0u;
-      all += h;
-    }
-    if (left < all) {
-      if (left >= before && left - before < n) {
-        left -= before;
-        for (int64_t i0 = b; i0 < e; i0 += 32) {
-          uint32_t m = i0 + lane < e ? match8(v[i0 + lane], mask, want) : 0u;
-          uint32_t inc = __popc(m);
-#pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += o;
-          }
-          const uint32_t step = __shfl_sync(0xffffffffu, inc, 31);
-          if (left < step) {
-            const uint32_t low = inc - __popc(m);
-            if (low <= left && left < inc) {
-              uint32_t in_order = 0;  // bit k: element k of the lane's vector
-              for (int k = 0; k < 8; ++k) in_order |= ((m >> (16 * (k & 1) + k / 2)) & 1u) << k;
-              for (uint32_t s = left - low; s > 0; --s) in_order &= in_order - 1;
-              sh->index = sl.head + 8 * (i0 + lane) + __ffs(in_order) - 1;
-            }
-            break;
-          }
-          left -= step;
-        }
-      }
-      __syncthreads();
-      return sh->index;
-    }
-    left -= all;
-    at = __ballot_sync(0xffffffffu, lane < sl.n_tail && element(sl.tail() + min(lane, 7)));
+  if (left < __popc(at)) {
     for (; left > 0; --left) at &= at - 1;
-    return sl.tail() - sl.x + __ffs(at) - 1;
+    return __ffs(at) - 1;
   }
+  left -= __popc(at);
+  // a warp's part in steps of 32 vectors, in groups of per_group steps
+  const int64_t n_vec = sl.v1 - sl.v0;
+  const int64_t steps = (n_vec + 32 * kWarps - 1) / (32 * kWarps);
+  const int64_t per_group = (steps + kGroups - 1) / kGroups;
+  const uint4* v = sl.vec();
+  const int64_t b = sl.v0 + steps * 32 * warp;
+  uint32_t n = 0, total = 0;
+  int group = 0;
+  int64_t flush = per_group;
+#pragma unroll 1
+  for (int64_t s0 = 0; s0 < steps; s0 += 4) {
+    uint4 w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s0 + k < steps && b + 32 * (s0 + k) + lane < sl.v1) w[k] = v[b + 32 * (s0 + k) + lane];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (s0 + k >= steps) break;
+      if (b + 32 * (s0 + k) + lane < sl.v1 && any_match(w[k], mask, want))
+        n += __popc(match8(w[k], mask, want));
+      if (s0 + k + 1 == flush || s0 + k + 1 == steps) {
+        n = __reduce_add_sync(0xffffffffu, n);
+        if (lane == 0) sh->hits[warp][group] = n;
+        total += n;
+        n = 0;
+        ++group;
+        flush += per_group;
+      }
+    }
+  }
+  if (lane == 0) sh->warp[warp].count = total;
+  __syncthreads();
+  uint32_t inc = lane < kWarps ? sh->warp[lane].count : 0u;
+#pragma unroll
+  for (int off = 1; off < kWarps; off <<= 1) {
+    const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += o;
+  }
+  const uint32_t all = __shfl_sync(0xffffffffu, inc, kWarps - 1);
+  if (left < all) {
+    const uint32_t before = __shfl_sync(0xffffffffu, inc, warp) - total;
+    if (left >= before && left - before < total) {
+      left -= before;
+      int g = 0;
+      while (left >= sh->hits[warp][g]) left -= sh->hits[warp][g++];
+      const int64_t from = b + 32 * per_group * g, to = min(sl.v1, from + 32 * per_group);
+#pragma unroll 1
+      for (int64_t i0 = from; i0 < to; i0 += 32) {
+        const uint32_t m = i0 + lane < to ? match8(v[i0 + lane], mask, want) : 0u;
+        if (!__any_sync(0xffffffffu, m)) continue;
+        uint32_t sum = __popc(m);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+          if (lane >= off) sum += o;
+        }
+        const uint32_t step = __shfl_sync(0xffffffffu, sum, 31);
+        if (left < step) {
+          const uint32_t low = sum - __popc(m);
+          if (low <= left && left < sum) {
+            uint32_t in_order = 0;  // bit k: element k of the lane's vector
+            for (int k = 0; k < 8; ++k) in_order |= ((m >> (16 * (k & 1) + k / 2)) & 1u) << k;
+            for (uint32_t x = left - low; x > 0; --x) in_order &= in_order - 1;
+            sh->index = sl.head + 8 * (i0 + lane) + __ffs(in_order) - 1;
+          }
+          break;
+        }
+        left -= step;
+      }
+    }
+    __syncthreads();
+    return sh->index;
+  }
+  left -= all;
+  at = __ballot_sync(0xffffffffu, lane < sl.n_tail && element(sl.tail() + min(lane, 7)));
   for (; left > 0; --left) at &= at - 1;
-  return __ffs(at) - 1;
+  return sl.tail() - sl.x + __ffs(at) - 1;
 }
 
 // One row per cluster of kC CTAs, each counting a contiguous part of it, each
-// weighing a share of the bins; every step that needs the whole row ends with a
-// cluster barrier, after which all CTAs hold the same numbers and go the same way.
+// weighing a share of the bins. CTA 0 takes the cuts and the draw and sends its
+// order to all: look for the token (the CTA that holds it), or count a window.
 template <int kC, int kThr, int kMin>
 __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p) {
   __shared__ __align__(16) uint32_t hist[kBinsPad];
   __shared__ RowShared sh;
   const int cta = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t row = blockIdx.x / kC;
-  Settings s;
-  if (!s.load(p, row)) {
-    if (cta == 0 && threadIdx.x == 0) {
-      p.token[row] = -1;
-      if (p.logprob) p.logprob[row] = __int_as_float(0x7fffffff);
-    }
-    return;  // the whole cluster leaves
-  }
   const Slice sl(p.logits + row * p.ld, p.V, cta, kC);
+  Settings s;
+  const bool valid = s.load(p, row);  // on its way while the row is counted
   Row<kC, kThr> r;
   r.hist = hist;
   r.sh = &sh;
   r.cta = cta;
-  r.t = s.t == 0.f ? 1.f : s.t;
-  r.div = ScaleDiv::make(r.t);
-  r.min_p = s.min_p;
   r.fix = p.fix;
-  r.turn = 0;
-  if (threadIdx.x == 0) sh.cmd_key = -1;
 
-  // The row's totals, from the direct range or window by window; then three
-  // crossings, each in the window that holds it (built again if need be).
+  if constexpr (kC > 1)  // the first count waits for it
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+
+  // The row's totals, from the direct range or window by window; then up to
+  // three crossings, each in the window that holds it (built again if need be).
   Totals all{0, 0, 0};
   uint32_t wc[kWindows];
   u64 wm[kWindows];
   int n_win = 1, win = kDirect;
-  bool max_known = false, totals = true;
-  int step = s.t == 0.f ? 2 : 0;  // 0: top-k, 1: top-p, 2: the draw
+  bool totals = true;
+  int step = 0;  // 0: top-k, 1: top-p, 2: the draw
   u64 kept = 0;
-  Crossing c{0, -1, 0};
+  int4 order;
 #pragma unroll 1
-  while (step < 3) {
+  for (;;) {
     r.count(sl, win);
-    if (!max_known && r.top != kNone) r.set_max(r.top);
     if (win == kDirect) {
-      // does a value outside the direct range matter?
+      r.t = s.t == 0.f ? 1.f : s.t;
+      r.div = ScaleDiv::make(r.t);
+      r.min_p = s.min_p;
+      if (s.t == 0.f) step = 2;
       const bool none = r.top == kNone;
-      if ((r.flags & 1) ||
-          ((r.flags & 2) && (none || !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail))) ||
-          ((r.flags & 4) && (none || !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail)))) {
-        n_win = kWindows;
-        win = 0;
-        row_sync<kC>();  // the others have read this CTA's counts
-        continue;
-      }
-      if (none) {  // nothing to draw
+      if (!none) r.set_max(r.top);
+      if (!valid || none) {  // nothing to draw, or a setting out of range
         if (cta == 0 && threadIdx.x == 0) {
           p.token[row] = -1;
-          if (p.logprob) p.logprob[row] = 0.f;
+          if (p.logprob) p.logprob[row] = valid ? 0.f : __int_as_float(0x7fffffff);
         }
-        row_sync<kC>();
-        return;
+        return;  // all of the cluster, after a barrier that ended all its reads
+      }
+      // does a value outside the direct range matter?
+      if ((r.flags & 1) || ((r.flags & 2) && !(__fdiv_rn(0x1p-32f, r.t) - r.z_max < kTail)) ||
+          ((r.flags & 4) && !(__fdiv_rn(-256.f, r.t) - r.z_max < kTail))) {
+        n_win = kWindows;
+        win = 0;
+        row_sync<kC>();  // every CTA has read what the others have seen
+        continue;
       }
     }
-    max_known |= r.top != kNone;
-    const Totals a = r.finish();
+    const Totals a = r.weigh();
     if (totals) {
       const int w = max(win, 0);
       wc[w] = a.count;
@@ -754,50 +783,65 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
       totals = false;
       kept = all.mass;
     }
+    if (cta == 0) {
+      order = make_int4(kBuild, 0, 0, 0);
 #pragma unroll 1
-    for (; step < 3; ++step) {
-      u64 at, before = 0;
-      bool exact;
-      int w = 0;
-      if (step == 0) {
-        if (s.top_k == 0 || static_cast<uint32_t>(s.top_k) >= all.count) continue;
-        at = static_cast<u64>(s.top_k) - 1;
-        u64 counted = 0;
-        while (w + 1 < n_win && at - counted >= wc[w]) {
-          counted += wc[w];
-          before += wm[w++];
-        }
-        at -= counted;
-      } else {
-        if (step == 1) {
-          if (!(s.top_p < 1.f)) continue;
-          at = scaled_floor(s.top_p, kept, exact);
-          if (exact && at > 0) --at;  // the token that brings the mass to at + 1 or more
+      for (; step < 3; ++step) {
+        u64 at, before = 0;
+        bool exact;
+        int w = 0;
+        if (step == 0) {
+          if (s.top_k == 0 || static_cast<uint32_t>(s.top_k) >= all.count) continue;
+          at = static_cast<u64>(s.top_k) - 1;
+          while (w + 1 < n_win && at >= wc[w]) {
+            at -= wc[w];
+            before += wm[w++];
+          }
         } else {
-          if (all.kept < kept) kept = all.kept;
-          at = s.t == 0.f ? 0 : scaled_floor(s.u, kept, exact);
-          if (s.t != 0.f && at >= kept) at = kept - 1;
+          if (step == 1) {
+            if (!(s.top_p < 1.f)) continue;
+            at = scaled_floor(s.top_p, kept, exact);
+            if (exact && at > 0) --at;  // the token that brings the mass to at + 1 or more
+          } else {
+            if (all.kept < kept) kept = all.kept;
+            at = s.t == 0.f ? 0 : scaled_floor(s.u, kept, exact);
+            if (s.t != 0.f && at >= kept) at = kept - 1;
+          }
+          while (w + 1 < n_win && at >= wm[w]) {
+            at -= wm[w];
+            before += wm[w++];
+          }
         }
-        while (w + 1 < n_win && at - before >= wm[w]) before += wm[w++];
-        at -= before;
+        if (n_win > 1 && r.window != w) {
+          order.y = w;
+          break;
+        }
+        kept = before + r.cross(step > 0, at);
       }
-      if (n_win > 1 && r.window != w) {
-        win = w;
-        break;
+      if (threadIdx.x < 32) {
+        if (step == 3) order = r.locate();
+        if (kC > 1) {
+          if (threadIdx.x < kC) st_peer_v4(peer<kC>(&sh.order, threadIdx.x), order);
+        } else if (threadIdx.x == 0) {
+          sh.order = order;
+        }
       }
-      c = r.cross(step > 0, step == 2, at);
-      kept = before + c.upto;
     }
+    row_sync<kC>();
+    order = sh.order;
+    if (order.x == kLook) break;
+    win = order.y;
+    row_sync<kC>();  // every CTA has the order
   }
   // no CTA reads another's memory from here on
-  if (sh.cmd_key >= 0) {
-    const int64_t index = index_of<kThr>(sl, &sh, sh.cmd_key, sh.cmd_rank);
+  if (order.y == cta) {
+    const int64_t index = index_of<kThr>(sl, &sh, order.z, static_cast<uint32_t>(order.w));
     if (threadIdx.x == 0) p.token[row] = static_cast<int32_t>(index);
   }
-  if (p.logprob && cta == kC - 1 && threadIdx.x == kThr - 1) {
+  if (p.logprob && cta == 0 && threadIdx.x == kThr - 1) {
     // d - ln(mass * 2^-fix), the logarithm as that of a number in [1, 2) and a
     // multiple of ln 2 whose first part is exact
-    const float v = key_value(c.key);
+    const float v = key_value(order.z);
     const float z = __fdiv_rn(v, r.t);
     const float d = v == r.x_max ? 0.f : __fsub_rn(z, r.z_max);
     const float lost =  // what the difference rounded off; 0 where z overflows
