@@ -109,7 +109,6 @@ struct Totals {
 
 // The histogram is weighed in rows of 32 bins.
 constexpr int kRows = kBinsPad / 32;
-constexpr int kGroups = 16;  // of a warp's part of a slice, in the search for an index
 
 struct RowShared {
   u64 row_m[kRows];         // CTA 0: mass and count of every row of bins
@@ -120,14 +119,14 @@ struct RowShared {
   u64 found;                // a crossing: the mass up to and with its token,
   int found_bin;            // its bin,
   uint32_t found_rank;      // and the token's rank among the bin's
-  int4 order;               // from CTA 0: what comes next (kLook, kBuild, kDone), and for kLook
-                            // the CTA that holds the token, its key, its rank there
-  uint32_t hits[kMaxWarps][kGroups];
+  int4 order;               // from CTA 0: kLook, the CTA that holds the token, its key, its
+                            // rank there; or kBuild and the window to count
+  uint32_t hits[2][kMaxWarps];
   int64_t index;
   int flags;                // 1: above the direct range, 2: tiny, 4: below the range
   int top;                  // smallest position of the CTA's own values
 };
-constexpr int kLook = 0, kBuild = 1, kDone = 2;
+constexpr int kLook = 0, kBuild = 1;
 
 // ------------------------------------------------------------ the cluster
 template <int kC>
@@ -156,29 +155,42 @@ __device__ __forceinline__ void st_peer_u64(uint32_t addr, u64 v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
+// ------------------------------------------------------------ two values a word
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // ------------------------------------------------------------ reading a row
 // A CTA's part of a row in index order: 2-byte steps up to the row's first
 // 16-byte boundary (the first CTA), a run of 16-byte vectors, and the row's last
 // elements (the last CTA).
 struct Slice {
   const uint16_t* x;   // the row
-  int64_t head;        // elements before the row's first vector
-  int64_t v0, v1;      // this CTA's vectors
+  const uint4* vec;    // this CTA's vectors
+  int n_vec;
   int n_head, n_tail;  // this CTA's elements before and after them (at most 7)
   __device__ __forceinline__ Slice(const uint16_t* row, int64_t V, int rank, int n_ranks) : x(row) {
-    const int64_t to16 = ((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) >> 1;
-    head = to16 < V ? to16 : V;
-    const int64_t nv = (V - head) >> 3;
-    const int64_t per = (nv + n_ranks - 1) / n_ranks;
-    v0 = min(nv, per * rank);
-    v1 = min(nv, v0 + per);
-    n_head = rank == 0 ? static_cast<int>(head) : 0;
-    n_tail = rank == n_ranks - 1 ? static_cast<int>(V - head - 8 * nv) : 0;
+    const int to16 = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) >> 1;
+    const int n = static_cast<int>(V);
+    const int head = min(to16, n);
+    const int nv = (n - head) >> 3;
+    const int per = (nv + n_ranks - 1) / n_ranks;
+    const int v0 = min(nv, per * rank);
+    n_vec = min(nv, v0 + per) - v0;
+    vec = reinterpret_cast<const uint4*>(row + head) + v0;
+    n_head = rank == 0 ? head : 0;
+    n_tail = rank == n_ranks - 1 ? n - head - 8 * nv : 0;
   }
-  __device__ __forceinline__ const uint4* vec() const {
-    return reinterpret_cast<const uint4*>(x + head);
+  __device__ __forceinline__ const uint16_t* tail() const {
+    return reinterpret_cast<const uint16_t*>(vec + n_vec);
   }
-  __device__ __forceinline__ const uint16_t* tail() const { return x + head + 8 * v1; }
 };
 
 // What a thread has seen besides its counts: flags, and the smallest position
@@ -188,22 +200,31 @@ struct Seen {
   int top = kNone;
 };
 
-// Counts eight values, all in the direct range, two to a word: with a = |x|'s
-// bits the bins are kHalf - (a - kMagLo + 1) for a positive value and kHalf +
-// (a - kMagLo + 1) for a negative one, both halves at once (no half carries).
-__device__ __forceinline__ void count_pairs(const uint4& w, uint32_t* hist) {
-  constexpr uint32_t kPlus = (kHalf + kMagLo - 1) * 0x10001u, kMinus = (kMagLo - 1 - kHalf) * 0x10001u;
+// Counts eight values, two to a word, if all are in the direct range; else does
+// nothing and returns false. With t = |x|'s bits - kMagLo the bin is kHalf - 1 - t
+// for a positive value and kHalf + 1 + t for a negative one, in byte offsets below
+// 2^16: both halves go through every step at once. (A half below the range borrows
+// from its neighbour, but is itself far above it then, and the vector is refused.)
+__device__ __forceinline__ bool count_vector(const uint4& w, uint32_t* hist) {
   const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  uint32_t t[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) t[q] = (ws[q] & 0x7fff7fffu) - kMagLo * 0x10001u;
+  constexpr uint32_t kMost = (kHalf - 1) * 0x10001u;
+  if (max2(max2(max2(t[0], t[1]), max2(t[2], t[3])), kMost) != kMost) return false;
+  const uint32_t h = smem_u32(hist);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    const uint32_t a = ws[q] & 0x7fff7fffu;
     uint32_t neg;  // each half's sign bit in all of its bits
     asm("prmt.b32 %0, %1, %1, 0xbb99;" : "=r"(neg) : "r"(ws[q]));
-    const uint32_t bin = ((kPlus - a) & ~neg) | ((a - kMinus) & neg);
-    atomicAdd(&hist[bin & 0xffffu], 1u);
-    atomicAdd(&hist[bin >> 16], 1u);
+    const uint32_t at =
+        (((kMost - t[q]) & ~neg) | ((t[q] + (kHalf + 1) * 0x10001u) & neg)) << 2;
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(h + (at & 0xffffu)) : "memory");
+    asm volatile("red.shared.add.u32 [%0], 1;" ::"r"(h + (at >> 16)) : "memory");
   }
+  return true;
 }
+static_assert(4 * kBins < 65536, "byte offsets of the direct range");
 // n values of which some may be zero, masked, or outside the direct range.
 __device__ __noinline__ Seen count_any(uint4 w, int n, uint32_t* hist, Seen seen) {
 #pragma unroll 1
@@ -249,40 +270,37 @@ template <int kThr>
 __device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* hist) {
   Seen seen;
   __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(0xff80u), __ushort_as_bfloat16(0xff80u));
-  const uint4* v = sl.vec();
+  auto one_vector = [&](const uint4& w) {
+    if (win != kDirect) {
+      seen = count_in_window(w, 8, win * kBinsPad, hist, seen);
+      return;
+    }
+    if (count_vector(w, hist)) {
+      const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(&w);
+      most = __hmax2(most, __hmax2(__hmax2(f[0], f[1]), __hmax2(f[2], f[3])));
+    } else {
+      seen = count_any(w, 8, hist, seen);
+    }
+  };
+  const uint4* v = sl.vec;
+  const int n = sl.n_vec;
   bool zeroed = false;
-  for (int64_t i0 = sl.v0 + threadIdx.x; !zeroed || i0 < sl.v1; i0 += kBatch * kThr) {
+#pragma unroll 1
+  for (int i = threadIdx.x; i < n || !zeroed; i += kBatch * kThr) {
     uint4 w[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (i0 + k * kThr < sl.v1) w[k] = v[i0 + k * kThr];
+      if (i + k * kThr < n) w[k] = v[i + k * kThr];
     if (!zeroed) {  // while the first loads are under way
       uint4* h = reinterpret_cast<uint4*>(hist);
 #pragma unroll 4
-      for (int i = threadIdx.x; i < kBinsPad / 4; i += kThr) h[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int j = threadIdx.x; j < kBinsPad / 4; j += kThr) h[j] = make_uint4(0u, 0u, 0u, 0u);
       __syncthreads();
       zeroed = true;
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (i0 + k * kThr >= sl.v1) continue;
-      if (win == kDirect) {
-        const uint32_t a0 = w[k].x & 0x7fff7fffu, a1 = w[k].y & 0x7fff7fffu;
-        const uint32_t a2 = w[k].z & 0x7fff7fffu, a3 = w[k].w & 0x7fff7fffu;
-        const uint32_t lo = __vminu2(__vminu2(a0, a1), __vminu2(a2, a3));
-        const uint32_t hi = __vmaxu2(__vmaxu2(a0, a1), __vmaxu2(a2, a3));
-        if (__vminu2(lo, kMagLo * 0x10001u) == kMagLo * 0x10001u &&
-            __vmaxu2(hi, kMagHi * 0x10001u) == kMagHi * 0x10001u) {
-          const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(&w[k]);
-          most = __hmax2(most, __hmax2(__hmax2(f[0], f[1]), __hmax2(f[2], f[3])));
-          count_pairs(w[k], hist);
-        } else {
-          seen = count_any(w[k], 8, hist, seen);
-        }
-      } else {
-        seen = count_in_window(w[k], 8, win * kBinsPad, hist, seen);
-      }
-    }
+    for (int k = 0; k < kBatch; ++k)
+      if (i + k * kThr < n) one_vector(w[k]);
   }
   if (threadIdx.x < sl.n_head + sl.n_tail) {
     const int i = threadIdx.x;
@@ -420,8 +438,11 @@ struct Row {
           if (w >= min_p) q += m;
         }
         c = __reduce_add_sync(0xffffffffu, n);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m += __shfl_xor_sync(0xffffffffu, m, off);
+        // a sum of 32 pieces of 22 bits fits 32
+        const u64 p0 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(m) & 0x3fffffu);
+        const u64 p1 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(m >> 22) & 0x3fffffu);
+        const u64 p2 = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(m >> 44));
+        m = p0 + (p1 << 22) + (p2 << 44);
       }
       if (lane == 0) {
         st_peer_u64(peer<kC>(&sh->row_m[row], 0), m);
@@ -598,12 +619,12 @@ __device__ __forceinline__ u64 scaled_floor(float f, u64 m, bool& exact) {
 
 // One bit per matching half of a word: `mask` drops the sign where zero is sought.
 __device__ __forceinline__ uint32_t match2(uint32_t w, uint32_t mask, uint32_t want) {
-  return __vcmpeq2(w & mask, want) & 0x00010001u;
+  return min2((w & mask) ^ want, 0x00010001u) ^ 0x00010001u;
 }
 // Whether a vector holds a match at all, in fewer steps.
 __device__ __forceinline__ bool any_match(const uint4& w, uint32_t mask, uint32_t want) {
-  const uint32_t m = __vminu2(__vminu2((w.x & mask) ^ want, (w.y & mask) ^ want),
-                              __vminu2((w.z & mask) ^ want, (w.w & mask) ^ want));
+  const uint32_t m = min2(min2((w.x & mask) ^ want, (w.y & mask) ^ want),
+                              min2((w.z & mask) ^ want, (w.w & mask) ^ want));
   return (m & 0xffffu) == 0u || m < 0x10000u;
 }
 // The matches of a vector: word k's halves at bits k and 16 + k.
@@ -612,13 +633,13 @@ __device__ __forceinline__ uint32_t match8(const uint4& w, uint32_t mask, uint32
          (match2(w.z, mask, want) << 2) | (match2(w.w, mask, want) << 3);
 }
 
-// Index in the row of the slice's rank-th element (from 0) with this key. Each
-// warp counts a contiguous part of the slice's vectors, in groups; the warp that
-// holds the element looks again at its group.
+// Index in the row of the slice's rank-th element (from 0) with this key. The
+// slice goes by in chunks, each warp holding 128 consecutive vectors of one, until
+// the chunk that has the element; half a slice on average.
 template <int kThr>
 __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int key,
                                             uint32_t rank) {
-  constexpr int kWarps = kThr / 32;
+  constexpr int kWarps = kThr / 32, kDepth = 4, kChunk = kThr * kDepth;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t bits = __float_as_uint(key_value(key)) >> 16;
   const uint32_t want = bits | (bits << 16);
@@ -632,80 +653,62 @@ __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int 
     return __ffs(at) - 1;
   }
   left -= __popc(at);
-  // a warp's part in steps of 32 vectors, in groups of per_group steps
-  const int64_t n_vec = sl.v1 - sl.v0;
-  const int64_t steps = (n_vec + 32 * kWarps - 1) / (32 * kWarps);
-  const int64_t per_group = (steps + kGroups - 1) / kGroups;
-  const uint4* v = sl.vec();
-  const int64_t b = sl.v0 + steps * 32 * warp;
-  uint32_t n = 0, total = 0;
-  int group = 0;
-  int64_t flush = per_group;
+  const int base = 32 * kDepth * warp + lane;
+  int turn = 0;
 #pragma unroll 1
-  for (int64_t s0 = 0; s0 < steps; s0 += 4) {
-    uint4 w[4];
+  for (int c0 = 0; c0 < sl.n_vec; c0 += kChunk, turn ^= 1) {
+    uint4 w[kDepth];
+    uint32_t m[kDepth];
+    uint32_t n = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (s0 + k < steps && b + 32 * (s0 + k) + lane < sl.v1) w[k] = v[b + 32 * (s0 + k) + lane];
+    for (int k = 0; k < kDepth; ++k)
+      if (c0 + base + 32 * k < sl.n_vec) w[k] = sl.vec[c0 + base + 32 * k];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (s0 + k >= steps) break;
-      if (b + 32 * (s0 + k) + lane < sl.v1 && any_match(w[k], mask, want))
-        n += __popc(match8(w[k], mask, want));
-      if (s0 + k + 1 == flush || s0 + k + 1 == steps) {
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (lane == 0) sh->hits[warp][group] = n;
-        total += n;
-        n = 0;
-        ++group;
-        flush += per_group;
+    for (int k = 0; k < kDepth; ++k) {
+      m[k] = 0;
+      if (c0 + base + 32 * k < sl.n_vec && any_match(w[k], mask, want)) {
+        m[k] = match8(w[k], mask, want);
+        n += __popc(m[k]);
       }
     }
-  }
-  if (lane == 0) sh->warp[warp].count = total;
-  __syncthreads();
-  uint32_t inc = lane < kWarps ? sh->warp[lane].count : 0u;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) sh->hits[turn][warp] = n;
+    __syncthreads();  // the turn before the last has been read by then
+    uint32_t inc = lane < kWarps ? sh->hits[turn][lane] : 0u;
 #pragma unroll
-  for (int off = 1; off < kWarps; off <<= 1) {
-    const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
-    if (lane >= off) inc += o;
-  }
-  const uint32_t all = __shfl_sync(0xffffffffu, inc, kWarps - 1);
-  if (left < all) {
-    const uint32_t before = __shfl_sync(0xffffffffu, inc, warp) - total;
-    if (left >= before && left - before < total) {
-      left -= before;
-      int g = 0;
-      while (left >= sh->hits[warp][g]) left -= sh->hits[warp][g++];
-      const int64_t from = b + 32 * per_group * g, to = min(sl.v1, from + 32 * per_group);
-#pragma unroll 1
-      for (int64_t i0 = from; i0 < to; i0 += 32) {
-        const uint32_t m = i0 + lane < to ? match8(v[i0 + lane], mask, want) : 0u;
-        if (!__any_sync(0xffffffffu, m)) continue;
-        uint32_t sum = __popc(m);
+    for (int off = 1; off < kWarps; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += o;
+    }
+    const uint32_t all = __shfl_sync(0xffffffffu, inc, kWarps - 1);
+    if (left < all) {
+      const uint32_t before = __shfl_sync(0xffffffffu, inc, warp) - n;
+      if (left >= before && left - before < n) {
+        left -= before;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-          if (lane >= off) sum += o;
-        }
-        const uint32_t step = __shfl_sync(0xffffffffu, sum, 31);
-        if (left < step) {
-          const uint32_t low = sum - __popc(m);
-          if (low <= left && left < sum) {
-            uint32_t in_order = 0;  // bit k: element k of the lane's vector
-            for (int k = 0; k < 8; ++k) in_order |= ((m >> (16 * (k & 1) + k / 2)) & 1u) << k;
-            for (uint32_t x = left - low; x > 0; --x) in_order &= in_order - 1;
-            sh->index = sl.head + 8 * (i0 + lane) + __ffs(in_order) - 1;
+        for (int k = 0; k < kDepth; ++k) {
+          uint32_t sum = __popc(m[k]);
+#pragma unroll
+          for (int off = 1; off < 32; off <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+            if (lane >= off) sum += o;
           }
-          break;
+          const uint32_t low = sum - __popc(m[k]);
+          if (low <= left && left < sum) {
+            uint32_t in_order = 0;  // bit i: element i of the lane's vector
+            for (int i = 0; i < 8; ++i) in_order |= ((m[k] >> (16 * (i & 1) + i / 2)) & 1u) << i;
+            for (uint32_t x = left - low; x > 0; --x) in_order &= in_order - 1;
+            const uint16_t* v = reinterpret_cast<const uint16_t*>(sl.vec + c0 + base + 32 * k);
+            sh->index = v + __ffs(in_order) - 1 - sl.x;
+          }
+          left -= __shfl_sync(0xffffffffu, sum, 31);  // wraps past zero once it is found
         }
-        left -= step;
       }
+      __syncthreads();
+      return sh->index;
     }
-    __syncthreads();
-    return sh->index;
+    left -= all;
   }
-  left -= all;
   at = __ballot_sync(0xffffffffu, lane < sl.n_tail && element(sl.tail() + min(lane, 7)));
   for (; left > 0; --left) at &= at - 1;
   return sl.tail() - sl.x + __ffs(at) - 1;
