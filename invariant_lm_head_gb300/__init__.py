@@ -118,16 +118,27 @@ def _check(fn: str, rc: int) -> None:
         raise LMHeadError(fn, rc, msg)
 
 
-def _torch():
-    import torch
+_torch_module = None
 
-    return torch
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream) -> Optional[int]:
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if torch.cuda.is_initialized():
+        # the current stream's handle without a Stream object around it (0.2 us
+        # instead of 2.8, of a short call's ten)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t) -> Optional[int]:
@@ -514,22 +525,33 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
     return out_logprob, out_entropy, out_lse
 
 
-def _need_rows(t, name: str, dtype, device) -> int:
+def _need_rows(t, name: str, dtype, device, shape=None) -> int:
     """A matrix whose rows are contiguous, at any row stride; returns the stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a 2-D tensor with contiguous rows")
-    if t.shape[0] <= 1:
-        return max(t.shape[1], t.stride(0))
-    if t.stride(0) < t.shape[1]:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a 2-D tensor")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if rows <= 1:  # one row has no stride to respect
+        return -(-cols // 8) * 8
+    if ld < cols:
         raise ValueError(f"{name} must have rows that do not overlap")
-    return t.stride(0)
+    return ld
+
+
+def _need_out(t, name: str, dtype, device, shape):
+    _need(t, name, dtype, device, len(shape))
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}")
 
 
 def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, stream=None):
@@ -543,22 +565,21 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
     dev = x.device
     ld = _need_rows(x, "x", torch.bfloat16, dev)
     rows, cols = x.shape
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    if rows <= 1:  # one row has no stride to respect
-        ld = -(-cols // 8) * 8
     shape = (-(-rows // block_rows), -(-cols // 128))
     if out is None:
-        out = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=dev)
+        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _need_out(out, "out", torch.float8_e4m3fn, dev, (rows, cols))
     if out_scale is None:
         out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
-    _need(out, "out", torch.float8_e4m3fn, dev, 2)
-    _need(out_scale, "out_scale", torch.float32, dev, 2)
-    if tuple(out.shape) != (rows, cols) or tuple(out_scale.shape) != shape:
-        raise ValueError("shape mismatch between x, out and out_scale")
-    rc = library().lmhead_quantize_fp8(_ptr(x), rows, cols, ld, int(block_rows), _ptr(out),
-                                       _ptr(out_scale), _stream_ptr(stream))
-    _check("lmhead_quantize_fp8", rc)
+    else:
+        _need_out(out_scale, "out_scale", torch.float32, dev, shape)
+    rc = library().lmhead_quantize_fp8(x.data_ptr(), rows, cols, ld, block_rows, out.data_ptr(),
+                                       out_scale.data_ptr(), _stream_ptr(stream))
+    if rc:
+        _check("lmhead_quantize_fp8", rc)
     return out, out_scale
 
 
@@ -572,28 +593,37 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_log
     """
     torch = _torch()
     dev = hidden_q.device
-    _need(hidden_q, "hidden_q", torch.float8_e4m3fn, dev, 2)
-    _need(weight_q, "weight_q", torch.float8_e4m3fn, dev, 2)
-    _need(hidden_scale, "hidden_scale", torch.float32, dev, 2)
-    _need(weight_scale, "weight_scale", torch.float32, dev, 2)
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    _need(hidden_q, "hidden_q", f8, dev, 2)
+    _need(weight_q, "weight_q", f8, dev, 2)
     T, H = hidden_q.shape
-    V = weight_q.shape[0]
-    kb = -(-H // 128)
-    if weight_q.shape[1] != H:
+    V, weight_cols = weight_q.shape
+    if weight_cols != H:
         raise ValueError("shape mismatch between hidden_q and weight_q")
-    if tuple(hidden_scale.shape) != (T, kb) or tuple(weight_scale.shape) != (-(-V // 128), kb):
-        raise ValueError("hidden_scale must be [T, ceil(H / 128)] and weight_scale "
-                         "[ceil(V / 128), ceil(H / 128)]")
+    kb = -(-H // 128)
+    _need_out(hidden_scale, "hidden_scale", f32, dev, (T, kb))
+    _need_out(weight_scale, "weight_scale", f32, dev, (-(-V // 128), kb))
     if out_logits is None:
-        out_logits = torch.empty(T, V, dtype=torch.bfloat16, device=dev)
-    ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev)
-    if tuple(out_logits.shape) != (T, V):
-        raise ValueError(f"out_logits must be [{T}, {V}]")
-    rc = library().lmhead_logits_fp8(_ptr(hidden_q), _ptr(hidden_scale), _ptr(weight_q),
-                                     _ptr(weight_scale), T, H, V, _ptr(out_logits), ld,
-                                     _stream_ptr(stream))
-    _check("lmhead_logits_fp8", rc)
+        out_logits = torch.empty((T, V), dtype=torch.bfloat16, device=dev)
+        ld = V
+    else:
+        ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev, (T, V))
+    rc = library().lmhead_logits_fp8(hidden_q.data_ptr(), hidden_scale.data_ptr(),
+                                     weight_q.data_ptr(), weight_scale.data_ptr(), T, H, V,
+                                     out_logits.data_ptr(), ld, _stream_ptr(stream))
+    if rc:
+        _check("lmhead_logits_fp8", rc)
     return out_logits
+
+
+def _setting(v, name: str, dtype, device, rows: int):
+    """A sampler setting: (number, None), or (None, one value per row)."""
+    if not isinstance(v, _torch().Tensor):
+        return v, None
+    _need(v, name, dtype, device, 1)
+    if v.shape[0] != rows:
+        raise ValueError(f"{name} must have one value per row")
+    return 0, v.data_ptr()
 
 
 def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0,
@@ -607,41 +637,32 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
     """
     torch = _torch()
     dev = logits.device
+    f32, i32 = torch.float32, torch.int32
     ld = _need_rows(logits, "logits", torch.bfloat16, dev)
     T, V = logits.shape
-    _need(uniform, "uniform", torch.float32, dev, 1)
+    _need(uniform, "uniform", f32, dev, 1)
     if uniform.shape[0] != T:
         raise ValueError("uniform must have one value per row")
-
-    def setting(v, name, dtype):
-        if not isinstance(v, torch.Tensor):
-            return v, None
-        _need(v, name, dtype, dev, 1)
-        if v.shape[0] != T:
-            raise ValueError(f"{name} must have one value per row")
-        return 1, v
-
-    t, row_t = setting(temperature, "temperature", torch.float32)
-    k, row_k = setting(top_k, "top_k", torch.int32)
-    p, row_p = setting(top_p, "top_p", torch.float32)
-    m, row_m = setting(min_p, "min_p", torch.float32)
+    t, row_t = _setting(temperature, "temperature", f32, dev, T)
+    k, row_k = _setting(top_k, "top_k", i32, dev, T)
+    p, row_p = _setting(top_p, "top_p", f32, dev, T)
+    m, row_m = _setting(min_p, "min_p", f32, dev, T)
     k = int(k)
     if not 0 <= k <= 0x7fffffff:
         raise ValueError("top_k must be in [0, 2^31)")
     if out_token is None:
-        out_token = torch.empty(T, dtype=torch.int32, device=dev)
-    if out_logprob is None and want_logprob:
-        out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
-    for o, name, dtype in ((out_token, "out_token", torch.int32),
-                           (out_logprob, "out_logprob", torch.float32)):
-        if o is not None:
-            _need(o, name, dtype, dev, 1)
-            if o.shape[0] != T:
-                raise ValueError(f"{name} must have one value per row")
-    rc = library().lmhead_sample(_ptr(logits), T, V, ld, float(t), _ptr(row_t), k, _ptr(row_k),
-                                 float(p), _ptr(row_p), float(m), _ptr(row_m), _ptr(uniform),
-                                 _ptr(out_token), _ptr(out_logprob), _stream_ptr(stream))
-    _check("lmhead_sample", rc)
+        out_token = torch.empty((T,), dtype=i32, device=dev)
+    else:
+        _need_out(out_token, "out_token", i32, dev, (T,))
+    if out_logprob is not None:
+        _need_out(out_logprob, "out_logprob", f32, dev, (T,))
+    elif want_logprob:
+        out_logprob = torch.empty((T,), dtype=f32, device=dev)
+    rc = library().lmhead_sample(logits.data_ptr(), T, V, ld, t, row_t, k, row_k, p, row_p, m,
+                                 row_m, uniform.data_ptr(), out_token.data_ptr(),
+                                 _ptr(out_logprob), _stream_ptr(stream))
+    if rc:
+        _check("lmhead_sample", rc)
     return out_token, out_logprob
 
 

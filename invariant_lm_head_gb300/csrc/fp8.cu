@@ -103,29 +103,38 @@ __device__ __forceinline__ uint32_t amax8(uint32_t m, const uint4& v) {
 }
 
 constexpr int kQuantThreads = 256;
+constexpr int kQuantDepth = 4;  // 16-byte loads in flight per thread
 
-// 1 x 128 blocks: 16 lanes hold one block, 8 elements (16 bytes) each.
+// 1 x 128 blocks: 16 lanes hold one block, 8 elements (16 bytes) each; a warp
+// takes 2 x kQuantDepth consecutive blocks of a row, all loaded before the first
+// is used (one at a time, with a division for each: 67 us instead of 44 us at
+// 16384 x 5120).
 __global__ void __launch_bounds__(kQuantThreads)
     quantize_rows_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
-                         int64_t kb, uint8_t* __restrict__ q, float* __restrict__ scale) {
-  const int sub = threadIdx.x & 15;
-  const int64_t n = rows * kb;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 16);
-  for (int64_t b = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 16) + (threadIdx.x >> 4);
-       b - (threadIdx.x >> 4) % 2 < n; b += stride) {  // both halves of a warp take part
-    const int64_t row = b / kb;
-    const int64_t blk = b - row * kb;
-    const int64_t col = blk * kQBlock + sub * 8;
-    const bool on = b < n && col < cols;
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (on) v = *reinterpret_cast<const uint4*>(x + row * ld + col);
-    uint32_t m = amax8(0u, v);
+                         int64_t kb, int64_t parts, uint8_t* __restrict__ q,
+                         float* __restrict__ scale) {
+  const int sub = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+  const int64_t row = unit / parts;
+  if (row >= rows) return;
+  const int64_t blk0 = (unit - row * parts) * (2 * kQuantDepth) + half;
+  uint4 v[kQuantDepth];
+#pragma unroll
+  for (int i = 0; i < kQuantDepth; ++i) {
+    const int64_t col = (blk0 + 2 * i) * kQBlock + sub * 8;
+    v[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (col < cols) v[i] = *reinterpret_cast<const uint4*>(x + row * ld + col);
+  }
+#pragma unroll
+  for (int i = 0; i < kQuantDepth; ++i) {
+    const int64_t blk = blk0 + 2 * i, col = blk * kQBlock + sub * 8;
+    uint32_t m = amax8(0u, v[i]);
     m = max(m & 0xffffu, m >> 16);
 #pragma unroll
     for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     const BlockScale s = block_scale(m);
-    if (on) *reinterpret_cast<uint2*>(q + row * cols + col) = quantize8(v, s);
-    if (b < n && sub == 0) scale[b] = s.scale;
+    if (col < cols) *reinterpret_cast<uint2*>(q + row * cols + col) = quantize8(v[i], s);
+    if (blk < kb && sub == 0) scale[row * kb + blk] = s.scale;
   }
 }
 
@@ -624,6 +633,8 @@ extern "C" int lmhead_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols
   if (ld < cols) return api_set_error(LMH_ERR_INVALID_ARG, "ld must be at least cols");
   if (cols % 16 != 0 || ld % 8 != 0)
     return api_set_error(LMH_ERR_ALIGNMENT, "cols must be a multiple of 16 and ld of 8");
+  if (ceil_div(rows, 8) * ceil_div(cols, kQBlock) > 0x7fffffffLL)
+    return api_set_error(LMH_ERR_INVALID_ARG, "rows x cols has too many blocks");
   if (rows == 0) return api_set_error(LMH_OK, "");
   if (!x || !q || !scale)
     return api_set_error(LMH_ERR_INVALID_ARG, "x, q and scale are required");
@@ -639,9 +650,10 @@ extern "C" int lmhead_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols
   {
     KernelTimer timer(K_QUANTIZE_FP8, st);
     if (block_rows == 1) {
-      const int64_t want = ceil_div(rows * kb, kQuantThreads / 16);
-      const int grid = static_cast<int>(want < 8 * sms ? want : 8 * sms);
-      quantize_rows_kernel<<<grid, kQuantThreads, 0, st>>>(x, rows, cols, ld, kb, q, scale);
+      const int64_t parts = ceil_div(kb, 2 * kQuantDepth);
+      const int64_t grid = ceil_div(rows * parts, kQuantThreads / 32);
+      quantize_rows_kernel<<<static_cast<unsigned>(grid), kQuantThreads, 0, st>>>(
+          x, rows, cols, ld, kb, parts, q, scale);
     } else {
       const int64_t tiles = ceil_div(rows, kQBlock) * kb;
       const int grid = static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms);
