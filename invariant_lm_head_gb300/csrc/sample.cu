@@ -193,13 +193,6 @@ struct Slice {
   }
 };
 
-// What a thread has seen besides its counts: flags, and the smallest position
-// (that of the largest value).
-struct Seen {
-  int flags = 0;
-  int top = kNone;
-};
-
 // Counts eight values, two to a word, if all are in the direct range; else does
 // nothing and returns false. With t = |x|'s bits - kMagLo the bin is kHalf - 1 - t
 // for a positive value and kHalf + 1 + t for a negative one, in byte offsets below
@@ -225,62 +218,57 @@ __device__ __forceinline__ bool count_vector(const uint4& w, uint32_t* hist) {
   return true;
 }
 static_assert(4 * kBins < 65536, "byte offsets of the direct range");
-// n values of which some may be zero, masked, or outside the direct range.
-__device__ __noinline__ Seen count_any(uint4 w, int n, uint32_t* hist, Seen seen) {
-#pragma unroll 1
-  for (int q = 0; q < n; ++q) {
-    const uint32_t b = w.x & 0xffffu;
-    w.x = __funnelshift_r(w.x, w.y, 16);
-    w.y = __funnelshift_r(w.y, w.z, 16);
-    w.z = __funnelshift_r(w.z, w.w, 16);
-    w.w >>= 16;
-    if (is_masked(b)) continue;
-    const int t = static_cast<int>(b & 0x7fffu) - (kMagLo - 1);
-    const bool neg = b & 0x8000u;
-    if ((b & 0x7fffu) == 0u)
-      atomicAdd(&hist[kHalf], 1u);
-    else if (t < 1 || t > kHalf)
-      seen.flags |= t < 1 ? 2 : (neg ? 4 : 1);
-    else
-      atomicAdd(&hist[neg ? kHalf + t : kHalf - t], 1u);
-    seen.top = min(seen.top, full_key(b));
+// Counts eight values of which some may be zero, masked or outside the direct
+// range; returns the flags of the latter.
+__device__ __noinline__ int count_any(uint4 w, uint32_t* hist) {
+  constexpr uint32_t kMasked = 0xff80ff80u;
+  if (w.x == kMasked && w.y == kMasked && w.z == kMasked && w.w == kMasked) return 0;
+  const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+  int flags = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const uint32_t b = q & 1 ? ws[q / 2] >> 16 : ws[q / 2] & 0xffffu;
+    const int t = static_cast<int>(b & 0x7fffu) - kMagLo;
+    if (static_cast<unsigned>(t) < static_cast<unsigned>(kHalf)) {
+      atomicAdd(&hist[b & 0x8000u ? kHalf + 1 + t : kHalf - 1 - t], 1u);
+    } else if (b != 0xff80u) {
+      if (t == -kMagLo)
+        atomicAdd(&hist[kHalf], 1u);
+      else if (!is_masked(b))
+        flags |= t < 0 ? 2 : (b & 0x8000u ? 4 : 1);
+    }
   }
-  return seen;
+  return flags;
 }
-// n values in a window over all bf16 values that starts at position lo.
-__device__ __noinline__ Seen count_in_window(uint4 w, int n, int lo, uint32_t* hist, Seen seen) {
+// The same in a window over all bf16 values that starts at position lo.
+__device__ __noinline__ void count_in_window(uint4 w, int lo, uint32_t* hist) {
 #pragma unroll 1
-  for (int q = 0; q < n; ++q) {
+  for (int q = 0; q < 8; ++q) {
     const uint32_t b = w.x & 0xffffu;
     w.x = __funnelshift_r(w.x, w.y, 16);
     w.y = __funnelshift_r(w.y, w.z, 16);
     w.z = __funnelshift_r(w.z, w.w, 16);
     w.w >>= 16;
     const int k = full_key(b) - lo;
-    if (k >= 0 && k < kBinsPad && !is_masked(b)) {
-      atomicAdd(&hist[k], 1u);
-      seen.top = min(seen.top, full_key(b));
-    }
+    if (k >= 0 && k < kBinsPad && !is_masked(b)) atomicAdd(&hist[k], 1u);
   }
-  return seen;
 }
 
 // Zeroes the histogram and counts the slice's values of window `win` in it.
+// Returns what the thread met outside the direct range, and the position of its
+// largest value.
 template <int kThr>
-__device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* hist) {
-  Seen seen;
+__device__ __forceinline__ int2 count_slice(const Slice& sl, int win, uint32_t* hist) {
+  int flags = 0;
   __nv_bfloat162 most = __halves2bfloat162(__ushort_as_bfloat16(0xff80u), __ushort_as_bfloat16(0xff80u));
   auto one_vector = [&](const uint4& w) {
     if (win != kDirect) {
-      seen = count_in_window(w, 8, win * kBinsPad, hist, seen);
+      count_in_window(w, win * kBinsPad, hist);
       return;
     }
-    if (count_vector(w, hist)) {
-      const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(&w);
-      most = __hmax2(most, __hmax2(__hmax2(f[0], f[1]), __hmax2(f[2], f[3])));
-    } else {
-      seen = count_any(w, 8, hist, seen);
-    }
+    const __nv_bfloat162* f = reinterpret_cast<const __nv_bfloat162*>(&w);
+    most = __hmax2(most, __hmax2(__hmax2(f[0], f[1]), __hmax2(f[2], f[3])));  // NaN is passed over
+    if (!count_vector(w, hist)) flags |= count_any(w, hist);
   };
   const uint4* v = sl.vec;
   const int n = sl.n_vec;
@@ -305,14 +293,10 @@ __device__ __forceinline__ Seen count_slice(const Slice& sl, int win, uint32_t* 
   if (threadIdx.x < sl.n_head + sl.n_tail) {
     const int i = threadIdx.x;
     const uint32_t b = i < sl.n_head ? sl.x[i] : sl.tail()[i - sl.n_head];
-    const uint4 one = make_uint4(b, 0u, 0u, 0u);
-    seen = win == kDirect ? count_any(one, 1, hist, seen)
-                          : count_in_window(one, 1, win * kBinsPad, hist, seen);
+    one_vector(make_uint4(0xff800000u | b, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u));
   }
-  const __nv_bfloat16 m = __hmax(__low2bfloat16(most), __high2bfloat16(most));
-  if (win == kDirect && __bfloat16_as_ushort(m) != 0xff80u)
-    seen.top = min(seen.top, full_key(__bfloat16_as_ushort(m)));
-  return seen;
+  const uint16_t m = __bfloat16_as_ushort(__hmax(__low2bfloat16(most), __high2bfloat16(most)));
+  return make_int2(flags, is_masked(m) ? kNone : full_key(m));
 }
 
 // ------------------------------------------------------------ one row
@@ -329,7 +313,7 @@ struct Row {
   ScaleDiv div;     // z = x / t
   int fix;
   int window;       // what the histogram holds
-  int top;          // the window's smallest position, kNone if it is empty
+  int top;          // the position of the row's largest value, kNone if there is none
   int flags;        // what the row holds outside the direct range
   // CTA 0: what comes before this thread's rows of bins in the built window, and
   // their own totals
@@ -369,8 +353,8 @@ struct Row {
     return __float2ull_rn(w * __uint_as_float(static_cast<uint32_t>(127 + fix) << 23));
   }
 
-  // Counts window `win` of the row over the cluster: afterwards top and flags
-  // are the whole row's. Another barrier follows (weigh, or the caller's): until
+  // Counts window `win` of the row over the cluster: after the direct range top
+  // and flags are the whole row's. Another barrier follows (weigh, or the caller's): until
   // then the CTAs read each other's counts.
   __device__ __forceinline__ void count(const Slice& sl, int win) {
     window = win;
@@ -378,9 +362,9 @@ struct Row {
       sh->flags = 0;
       sh->top = kNone;
     }
-    const Seen mine = count_slice<kThr>(sl, win, hist);  // its barrier also covers the two above
-    const int f = __reduce_or_sync(0xffffffffu, mine.flags);
-    const int b = __reduce_min_sync(0xffffffffu, mine.top);
+    const int2 mine = count_slice<kThr>(sl, win, hist);  // its barrier also covers the two above
+    const int f = __reduce_or_sync(0xffffffffu, mine.x);
+    const int b = __reduce_min_sync(0xffffffffu, mine.y);
     if ((threadIdx.x & 31) == 0) {
       if (f) atomicOr(&sh->flags, f);
       if (b != kNone) atomicMin(&sh->top, b);
