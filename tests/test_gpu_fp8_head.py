@@ -375,3 +375,43 @@ def test_streams_and_graphs():
     again = step()
     assert all(torch.equal(a, b) for a, b in zip(out, again))
     lmh.lmhead_device_status()
+
+
+def test_head_class():
+    import torch
+
+    from invariant_lm_head_gb300.fp8_head import FP8Head
+
+    w = to_dev_bf16(W.random_bf16(91, (2007, 384), 0.05))
+    h = to_dev_bf16(W.random_bf16(92, (9, 384), 1.0))
+    u = torch.rand(9, device=dev())
+    head = FP8Head(w)
+    assert (head.vocab_size, head.hidden_size) == (2007, 384)
+    lg = head.logits(h)
+    check_logits(lg, *lmh.lmhead_quantize_fp8(h), head.weight_q, head.weight_scale)
+    tok, lp = head.sample(h, u, 0.8, top_k=40)
+    want = lmh.lmhead_sample(lg, u, 0.8, top_k=40)
+    assert torch.equal(tok, want[0]) and torch.equal(lp, want[1])
+    mask = torch.ones(2007, dtype=torch.bool, device=dev())
+    mask[[3, 77]] = False
+    out = torch.empty(9, 2008, dtype=torch.bfloat16, device=dev())[:, :2007]
+    tok, lp = head.sample(h, u, mask=mask, out_logits=out)
+    assert set(tok.tolist()) <= {3, 77} and (out[:, 4] == float("-inf")).all()
+    w2 = to_dev_bf16(W.random_bf16(93, (2007, 384), 0.05))
+    q0 = head.weight_q.data_ptr()
+    head.refresh(w2)
+    assert head.weight_q.data_ptr() == q0
+    assert torch.equal(head.logits(h), FP8Head(w2).logits(h))
+
+
+def test_example_runs():
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, os.path.join(root, "examples", "serve_fp8_head.py"),
+                        "--batch", "5", "--hidden", "256", "--vocab", "1003", "--steps", "8"],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert "tokens/s" in r.stdout
