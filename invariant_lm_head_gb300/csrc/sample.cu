@@ -129,12 +129,24 @@ struct RowShared {
 constexpr int kLook = 0, kBuild = 1;
 
 // ------------------------------------------------------------ the cluster
+// Not the .aligned forms: they count a whole warp at once, and a warp that comes
+// out of a branch on its lanes (one thread that pushes a total to a peer, say) need
+// not be one again.
+__device__ __forceinline__ void row_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void row_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
 template <int kC>
 __device__ __forceinline__ void row_sync() {
-  if constexpr (kC > 1)
-    cluster_sync();
-  else
+  if constexpr (kC > 1) {
+    __syncwarp();
+    row_arrive();
+    row_wait();
+  } else {
     __syncthreads();
+  }
 }
 // The address of the same shared variable in CTA c.
 template <int kC>
@@ -375,13 +387,13 @@ struct Row {
       top = sh->top;
     } else {
       // every CTA of the cluster has started: its memory can be written
-      if (win == kDirect) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      if (win == kDirect) row_wait();
       if (threadIdx.x < kC) {
         const uint32_t to = peer<kC>(&sh->seen[cta], threadIdx.x);
         st_peer_u64(to, static_cast<u64>(static_cast<uint32_t>(sh->flags)) |
                             (static_cast<u64>(static_cast<uint32_t>(sh->top)) << 32));
       }
-      cluster_sync();
+      row_sync<kC>();
       flags = 0;
       top = kNone;
 #pragma unroll
@@ -446,7 +458,7 @@ struct Row {
         for (int w = 0; w < kWarps; ++w) all += sh->warp[w].kept;
         st_peer_u64(peer<kC>(&sh->kept[cta], 0), all);
       }
-      cluster_sync();
+      row_sync<kC>();
       if (cta != 0) return Totals{0, 0, 0};
     }
     // exclusive prefixes over CTA 0's threads, in order of the rows
@@ -716,8 +728,7 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
   r.cta = cta;
   r.fix = p.fix;
 
-  if constexpr (kC > 1)  // the first count waits for it
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  if constexpr (kC > 1) row_arrive();  // the first count waits for it
 
   // The row's totals, from the direct range or window by window; then up to
   // three crossings, each in the window that holds it (built again if need be).

@@ -415,3 +415,18 @@ def test_example_runs():
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "tokens/s" in r.stdout
+
+
+@pytest.mark.parametrize("T", [1, 19, 38, 39, 76, 77, 152, 153, 400])
+def test_sample_every_split_of_a_row(T):
+    # rows go to 8, 4, 2 or 1 CTAs by their number; each must give the oracle's token every time
+    import torch
+
+    V = 2043
+    x, g = logit_rows(T, T, V)
+    u = g.random(T, dtype=np.float32)
+    tok, lp = check_sample(x, u, t=0.9, p=0.95, k=500)
+    lg = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    for _ in range(20):
+        t2, l2 = lmh.lmhead_sample(lg, to_dev(u), 0.9, top_k=500, top_p=0.95)
+        assert np.array_equal(t2.cpu().numpy(), tok) and np.array_equal(l2.cpu().numpy(), lp)
