@@ -87,18 +87,19 @@ struct SampleParams {
   int fix;  // weights are in units of 2^-fix
 };
 
-// What a row asks for; load() is false when a setting is out of range.
+// What a row asks for; the temperature is NaN where a setting is out of range.
 struct Settings {
   float t, top_p, min_p, u;
   int top_k;
-  __device__ __forceinline__ bool load(const SampleParams& p, int64_t row) {
+  __device__ __forceinline__ void load(const SampleParams& p, int64_t row) {
     t = p.row_t ? p.row_t[row] : p.temperature;
     top_p = p.row_p ? p.row_p[row] : p.top_p;
     min_p = p.row_m ? p.row_m[row] : p.min_p;
     top_k = p.row_k ? p.row_k[row] : p.top_k;
     u = p.uniform[row];
-    return t >= 0.f && t <= 3.402823466e38f && top_p > 0.f && min_p <= 1.f && u >= 0.f &&
-           u <= 1.f && top_k >= 0;
+    if (!(t >= 0.f && t <= 3.402823466e38f && top_p > 0.f && min_p <= 1.f && u >= 0.f && u <= 1.f &&
+          top_k >= 0))
+      t = __int_as_float(0x7fffffff);
   }
 };
 
@@ -111,10 +112,11 @@ struct Totals {
 constexpr int kRows = kBinsPad / 32;
 
 struct RowShared {
+  Settings set;             // thread 0's reading of them
   u64 row_m[kRows];         // CTA 0: mass and count of every row of bins
   uint32_t row_c[kRows];
   u64 kept[kMaxC];          // CTA 0: every CTA's share of the mass that min-p keeps
-  int2 seen[kMaxC];         // every CTA's flags and largest value's position
+  int4 seen[kMaxC];         // every CTA's flags, largest value's position, temperature, min-p
   Totals warp[kMaxWarps];
   u64 found;                // a crossing: the mass up to and with its token,
   int found_bin;            // its bin,
@@ -324,6 +326,7 @@ struct Row {
   float t, z_max, x_max, min_p;
   ScaleDiv div;     // z = x / t
   int fix;
+  bool valid;       // the settings are in range
   int window;       // what the histogram holds
   int top;          // the position of the row's largest value, kNone if there is none
   int flags;        // what the row holds outside the direct range
@@ -365,9 +368,9 @@ struct Row {
     return __float2ull_rn(w * __uint_as_float(static_cast<uint32_t>(127 + fix) << 23));
   }
 
-  // Counts window `win` of the row over the cluster: after the direct range top
-  // and flags are the whole row's. Another barrier follows (weigh, or the caller's): until
-  // then the CTAs read each other's counts.
+  // Counts window `win` of the row over the cluster: after the direct range top,
+  // flags and the settings that all CTAs use are the whole row's. Another barrier
+  // follows (weigh, or the caller's): until then the CTAs read each other's counts.
   __device__ __forceinline__ void count(const Slice& sl, int win) {
     window = win;
     if (threadIdx.x == 0) {
@@ -385,14 +388,15 @@ struct Row {
     if constexpr (kC == 1) {
       flags = sh->flags;
       top = sh->top;
+      t = sh->set.t;
+      min_p = sh->set.min_p;
     } else {
       // every CTA of the cluster has started: its memory can be written
       if (win == kDirect) row_wait();
-      if (threadIdx.x < kC) {
-        const uint32_t to = peer<kC>(&sh->seen[cta], threadIdx.x);
-        st_peer_u64(to, static_cast<u64>(static_cast<uint32_t>(sh->flags)) |
-                            (static_cast<u64>(static_cast<uint32_t>(sh->top)) << 32));
-      }
+      if (threadIdx.x < kC)
+        st_peer_v4(peer<kC>(&sh->seen[cta], threadIdx.x),
+                   make_int4(sh->flags, sh->top, __float_as_int(sh->set.t),
+                             __float_as_int(sh->set.min_p)));
       row_sync<kC>();
       flags = 0;
       top = kNone;
@@ -401,7 +405,11 @@ struct Row {
         flags |= sh->seen[c].x;
         top = min(top, sh->seen[c].y);
       }
+      t = __int_as_float(sh->seen[0].z);
+      min_p = __int_as_float(sh->seen[0].w);
     }
+    valid = t >= 0.f;  // NaN where a setting is out of range
+    if (t == 0.f) t = 1.f;  // greedy: the log-prob is that of temperature 1
   }
 
   // Sums this CTA's share of the bins over the cluster (in place: no one else
@@ -629,9 +637,11 @@ __device__ __forceinline__ uint32_t match8(const uint4& w, uint32_t mask, uint32
          (match2(w.z, mask, want) << 2) | (match2(w.w, mask, want) << 3);
 }
 
-// Index in the row of the slice's rank-th element (from 0) with this key. The
-// slice goes by in chunks, each warp holding 128 consecutive vectors of one, until
-// the chunk that has the element; half a slice on average.
+// Index in the row of the slice's rank-th element (from 0) with this key, -1 if it
+// has fewer (a row that changed since it was counted). The slice goes by in
+// chunks, each warp holding 128 consecutive vectors of one, until the chunk that
+// has the element; half a slice on average. The elements before the vectors go
+// with the first chunk's first warp, those after them with the last one's last.
 template <int kThr>
 __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int key,
                                             uint32_t rank) {
@@ -640,25 +650,29 @@ __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int 
   const uint32_t bits = __float_as_uint(key_value(key)) >> 16;
   const uint32_t want = bits | (bits << 16);
   const uint32_t mask = bits ? 0xffffffffu : 0x7fff7fffu;
-  auto element = [&](const uint16_t* x) { return (*x & mask & 0xffffu) == bits; };
-  // the elements before the vectors (every warp alike)
-  uint32_t at = __ballot_sync(0xffffffffu, lane < sl.n_head && element(sl.x + min(lane, 7)));
+  // which of n (at most 7) single elements match
+  auto ends = [&](const uint16_t* x, int n) {
+    return __ballot_sync(0xffffffffu, lane < n && (x[min(lane, 7)] & mask & 0xffffu) == bits);
+  };
+  auto nth = [](uint32_t m, uint32_t n) {  // position of the n-th set bit
+    for (; n > 0; --n) m &= m - 1;
+    return __ffs(m) - 1;
+  };
   uint32_t left = rank;
-  if (left < __popc(at)) {
-    for (; left > 0; --left) at &= at - 1;
-    return __ffs(at) - 1;
-  }
-  left -= __popc(at);
   const int base = 32 * kDepth * warp + lane;
   int turn = 0;
 #pragma unroll 1
-  for (int c0 = 0; c0 < sl.n_vec; c0 += kChunk, turn ^= 1) {
+  for (int c0 = 0;; c0 += kChunk, turn ^= 1) {
+    const bool last = c0 + kChunk >= sl.n_vec;
     uint4 w[kDepth];
     uint32_t m[kDepth];
     uint32_t n = 0;
 #pragma unroll
     for (int k = 0; k < kDepth; ++k)
       if (c0 + base + 32 * k < sl.n_vec) w[k] = sl.vec[c0 + base + 32 * k];
+    uint32_t head = 0, tail = 0;
+    if (c0 == 0 && warp == 0) head = ends(sl.x, sl.n_head);
+    if (last && warp == kWarps - 1) tail = ends(sl.tail(), sl.n_tail);
 #pragma unroll
     for (int k = 0; k < kDepth; ++k) {
       m[k] = 0;
@@ -667,7 +681,7 @@ __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int 
         n += __popc(m[k]);
       }
     }
-    n = __reduce_add_sync(0xffffffffu, n);
+    n = __reduce_add_sync(0xffffffffu, n) + __popc(head) + __popc(tail);
     if (lane == 0) sh->hits[turn][warp] = n;
     __syncthreads();  // the turn before the last has been read by then
     uint32_t inc = lane < kWarps ? sh->hits[turn][lane] : 0u;
@@ -681,33 +695,36 @@ __device__ __forceinline__ int64_t index_of(const Slice& sl, RowShared* sh, int 
       const uint32_t before = __shfl_sync(0xffffffffu, inc, warp) - n;
       if (left >= before && left - before < n) {
         left -= before;
+        if (left < __popc(head)) {
+          if (lane == 0) sh->index = nth(head, left);
+        } else {
+          left -= __popc(head);
 #pragma unroll
-        for (int k = 0; k < kDepth; ++k) {
-          uint32_t sum = __popc(m[k]);
+          for (int k = 0; k < kDepth; ++k) {
+            uint32_t sum = __popc(m[k]);
 #pragma unroll
-          for (int off = 1; off < 32; off <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
-            if (lane >= off) sum += o;
+            for (int off = 1; off < 32; off <<= 1) {
+              const uint32_t o = __shfl_up_sync(0xffffffffu, sum, off);
+              if (lane >= off) sum += o;
+            }
+            const uint32_t low = sum - __popc(m[k]);
+            if (low <= left && left < sum) {
+              uint32_t in_order = 0;  // bit i: element i of the lane's vector
+              for (int i = 0; i < 8; ++i) in_order |= ((m[k] >> (16 * (i & 1) + i / 2)) & 1u) << i;
+              const uint16_t* v = reinterpret_cast<const uint16_t*>(sl.vec + c0 + base + 32 * k);
+              sh->index = v - sl.x + nth(in_order, left - low);
+            }
+            left -= __shfl_sync(0xffffffffu, sum, 31);  // wraps past zero once it is found
           }
-          const uint32_t low = sum - __popc(m[k]);
-          if (low <= left && left < sum) {
-            uint32_t in_order = 0;  // bit i: element i of the lane's vector
-            for (int i = 0; i < 8; ++i) in_order |= ((m[k] >> (16 * (i & 1) + i / 2)) & 1u) << i;
-            for (uint32_t x = left - low; x > 0; --x) in_order &= in_order - 1;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(sl.vec + c0 + base + 32 * k);
-            sh->index = v + __ffs(in_order) - 1 - sl.x;
-          }
-          left -= __shfl_sync(0xffffffffu, sum, 31);  // wraps past zero once it is found
+          if (left < __popc(tail) && lane == 0) sh->index = sl.tail() - sl.x + nth(tail, left);
         }
       }
       __syncthreads();
       return sh->index;
     }
+    if (last) return -1;
     left -= all;
   }
-  at = __ballot_sync(0xffffffffu, lane < sl.n_tail && element(sl.tail() + min(lane, 7)));
-  for (; left > 0; --left) at &= at - 1;
-  return sl.tail() - sl.x + __ffs(at) - 1;
 }
 
 // One row per cluster of kC CTAs, each counting a contiguous part of it, each
@@ -720,8 +737,6 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
   const int cta = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int64_t row = blockIdx.x / kC;
   const Slice sl(p.logits + row * p.ld, p.V, cta, kC);
-  Settings s;
-  const bool valid = s.load(p, row);  // on its way while the row is counted
   Row<kC, kThr> r;
   r.hist = hist;
   r.sh = &sh;
@@ -729,6 +744,16 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
   r.fix = p.fix;
 
   if constexpr (kC > 1) row_arrive();  // the first count waits for it
+  // Whatever the CTAs and threads have to agree on goes through one copy in shared
+  // memory: a caller's other stream that writes a setting or a logit meanwhile gets
+  // a senseless token, but all threads meet at the same barriers. A crossing that
+  // finds nothing leaves the values below, which are always a bin.
+  if (threadIdx.x == 0) {
+    sh.set.load(p, row);  // the first count's barrier covers it
+    sh.found = 0;
+    sh.found_bin = 0;
+    sh.found_rank = 0;
+  }
 
   // The row's totals, from the direct range or window by window; then up to
   // three crossings, each in the window that holds it (built again if need be).
@@ -743,17 +768,16 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
 #pragma unroll 1
   for (;;) {
     r.count(sl, win);
+    const Settings s = sh.set;
     if (win == kDirect) {
-      r.t = s.t == 0.f ? 1.f : s.t;
       r.div = ScaleDiv::make(r.t);
-      r.min_p = s.min_p;
       if (s.t == 0.f) step = 2;
       const bool none = r.top == kNone;
       if (!none) r.set_max(r.top);
-      if (!valid || none) {  // nothing to draw, or a setting out of range
+      if (!r.valid || none) {  // nothing to draw, or a setting out of range
         if (cta == 0 && threadIdx.x == 0) {
           p.token[row] = -1;
-          if (p.logprob) p.logprob[row] = valid ? 0.f : __int_as_float(0x7fffffff);
+          if (p.logprob) p.logprob[row] = r.valid ? 0.f : __int_as_float(0x7fffffff);
         }
         return;  // all of the cluster, after a barrier that ended all its reads
       }

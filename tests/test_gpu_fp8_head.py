@@ -430,3 +430,29 @@ def test_sample_every_split_of_a_row(T):
     for _ in range(20):
         t2, l2 = lmh.lmhead_sample(lg, to_dev(u), 0.9, top_k=500, top_p=0.95)
         assert np.array_equal(t2.cpu().numpy(), tok) and np.array_equal(l2.cpu().numpy(), lp)
+
+
+@pytest.mark.parametrize("T", [3, 60, 120, 200])
+def test_sample_while_its_inputs_change(T):
+    # A caller that forgets to order two streams gets senseless tokens, nothing worse:
+    # every thread follows one copy of what decides its way, and every index is bounded.
+    import torch
+
+    V = 3003
+    x, g = logit_rows(T, T, V)
+    good = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    wild = torch.randint(-32768, 32767, (T, V), device=dev(), dtype=torch.int16).view(torch.bfloat16)
+    lg, u = good.clone(), torch.rand(T, device=dev())
+    t = torch.full((T,), 0.9, device=dev())
+    ts = [t.clone(), torch.full_like(t, 0.0), torch.full_like(t, float("nan")),
+          torch.full_like(t, 1e-30)]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for i in range(200):
+        with torch.cuda.stream(other):
+            lg.copy_(wild if i % 2 else good)
+            t.copy_(ts[i % 4])
+        lmh.lmhead_sample(lg, u, t, top_p=0.9, top_k=1000)
+    torch.cuda.synchronize()
+    uu = u.cpu().numpy()
+    check_sample(x, uu, t=0.9, p=0.9, k=1000, logits=good)
