@@ -479,7 +479,8 @@ int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_scale, const 
  * ones) and ignores the rest. out_logprob is the token's log-prob in the whole
  * distribution at that temperature (at 1 for temperature 0), before any cut:
  * the sampler formula's value, as logprob_from_logits_div gives it.
- *   logits   bf16 [T, V], rows ld_logits elements apart, 2-byte aligned
+ *   logits   bf16 [T, V], rows ld_logits elements apart, 2-byte aligned; T up
+ *            to LMH_MAX_DIM / 8
  *   temperature, top_k, top_p, min_p  for every row, in [0, inf), [0, ..),
  *            (0, 1], [0, 1]; each can be replaced by a device array with one
  *            value per row (f32, int32, f32, f32; NULL: none). The host

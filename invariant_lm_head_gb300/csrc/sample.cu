@@ -22,9 +22,10 @@
 // one bin per value. A row that holds another value whose weight matters (the
 // lowest finite value as a mask does not, next to real logits) is taken in
 // seven windows over all bf16 values instead, the row read again for each.
+#include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdio>
-#include <cmath>
 
 #include <cuda_bf16.h>
 
@@ -877,20 +878,70 @@ __global__ void __launch_bounds__(kThr, kMin) sample_kernel(const SampleParams p
   }
 }
 
+struct LaunchConfig {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr{};
+  LaunchConfig(int64_t rows, int ctas, int threads, cudaStream_t st) {
+    cfg.gridDim = dim3(static_cast<unsigned>(rows * ctas));
+    cfg.blockDim = dim3(threads);
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = ctas;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+  }
+};
+
 template <int kC, int kThr, int kMin>
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
-  cfg.blockDim = dim3(kThr);
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kC;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<kC, kThr, kMin>, p);
+  LaunchConfig c(p.T, kC, kThr, st);
+  return cudaLaunchKernelEx(&c.cfg, sample_kernel<kC, kThr, kMin>, p);
+}
+
+// Rows whose clusters of kC CTAs are on the device at once, one CTA to an SM.
+template <int kC>
+cudaError_t rows_at_once(int sms, int64_t* rows) {
+  static std::atomic<int> cached[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev >= 0 && dev < 64 ? cached[dev].load(std::memory_order_relaxed) : 0;
+  if (n == 0) {
+    LaunchConfig c(sms / kC, kC, 512, nullptr);
+    if ((e = cudaOccupancyMaxActiveClusters(&n, sample_kernel<kC, 512, 1>, &c.cfg)) != cudaSuccess)
+      return e;
+    n = (n < sms / kC ? n : sms / kC) + 1;
+    if (dev >= 0 && dev < 64) cached[dev].store(n, std::memory_order_relaxed);
+  }
+  *rows = n - 1;
+  return cudaSuccess;
+}
+
+// How a batch is split. A call is a chain of short steps, so a row gets as many
+// CTAs as leave one to an SM; past one CTA a row they share SMs, two of 512 threads
+// and then four of 256. Measured at V = 32000 / 152064 (us; 8, 4, 2, 1, 1 shared by
+// two, 1 of 256 threads shared by four):
+//   4 rows    10.8 / 12.0   11.7 / 14.7   13.3 / 19.9   14.2 / 27.8   15.7 / 27.0   21.4 / 33.2
+//   32 rows   28.1 / 30.7   12.1 / 15.5   13.7 / 20.5   14.6 / 27.3   15.9 / 28.9   21.7 / 39.3
+//   64 rows   45.4 / 50.3   22.8 / 28.6   13.7 / 20.8   14.6 / 27.7   16.1 / 28.8   22.1 / 39.5
+//   150 rows  90.9 / 101    51.0 / 64.6   26.6 / 41.2   14.9 / 28.9   16.2 / 29.9   21.9 / 41.8
+//   300 rows   177 / 200    93.4 / 122    51.8 / 82.4   28.0 / 59.0   22.7 / 49.6   25.2 / 60.5
+//   1024 rows  610 / 673     309 / 393     179 / 272    98.2 / 186    72.6 / 153    62.3 / 156
+cudaError_t launch_by_rows(const SampleParams& p, int sms, cudaStream_t st) {
+  int64_t n8 = 0, n4 = 0, n2 = 0;
+  cudaError_t e;
+  if ((e = rows_at_once<8>(sms, &n8)) != cudaSuccess ||
+      (e = rows_at_once<4>(sms, &n4)) != cudaSuccess ||
+      (e = rows_at_once<2>(sms, &n2)) != cudaSuccess)
+    return e;
+  if (p.T <= n8) return launch_sample<8, 512, 1>(p, st);
+  if (p.T <= n4) return launch_sample<4, 512, 1>(p, st);
+  if (p.T <= n2) return launch_sample<2, 512, 1>(p, st);
+  if (p.T <= sms) return launch_sample<1, 512, 1>(p, st);
+  if (p.T <= 2 * sms) return launch_sample<1, 512, 2>(p, st);
+  return launch_sample<1, 256, 4>(p, st);
 }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
@@ -953,15 +1004,7 @@ extern "C" int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64
   cudaError_t e;
   {
     KernelTimer timer(K_SAMPLE, st);
-    const int64_t slots = 2 * static_cast<int64_t>(sms);  // CTAs at work at once
-    if (T * 8 <= slots)
-      e = launch_sample<8, 512, 1>(p, st);
-    else if (T * 4 <= slots)
-      e = launch_sample<4, 512, 2>(p, st);
-    else if (T * 2 <= slots)
-      e = launch_sample<2, 512, 2>(p, st);
-    else
-      e = launch_sample<1, 256, 4>(p, st);
+    e = launch_by_rows(p, sms, st);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) {

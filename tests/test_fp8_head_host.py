@@ -95,7 +95,8 @@ def test_sample_refusals(lib):
                                  a["p"], a["rp"], a["m"], a["rm"], a["u"], a["tok"], a["lp"], None)
 
     nan, inf = float("nan"), float("inf")
-    for bad in (dict(T=-1), dict(V=0), dict(V=2147483393), dict(ld=999), dict(t=-1.0), dict(t=nan),
+    for bad in (dict(T=-1), dict(T=2147483392 // 8 + 1), dict(V=0), dict(V=2147483393),
+                dict(ld=999), dict(t=-1.0), dict(t=nan),
                 dict(t=inf), dict(k=-1), dict(p=0.0), dict(p=1.5), dict(p=nan), dict(m=-0.1),
                 dict(m=1.1), dict(m=nan), dict(x=None), dict(u=None), dict(tok=None)):
         assert call(**bad) == lmh.LMH_ERR_INVALID_ARG, bad
