@@ -300,7 +300,7 @@ __device__ __forceinline__ void fp8_unit(const Fp8Params& p, int u, int& m, int&
 // lanes that no one reads.
 //
 // What bounds it. A short batch reads the weight once and is bound by that: 82.6
-// us at T=1 H=3584 V=152064, 6.6 TB/s; 26.0 us at T=64 H=4096 V=32000, 5.2 TB/s
+// us at T=1 H=3584 V=152064, 6.6 TB/s; 26.4 us at T=64 H=4096 V=32000, 5.1 TB/s
 // (one wave: its start and end show). A long one is bound by the promote groups:
 // a K block's 128 x 256 accumulator is read out of TMEM beside the MMAs, which
 // use TMEM as well (about 500 cycles, against 190 with no MMA running), scaled,
@@ -309,8 +309,10 @@ __device__ __forceinline__ void fp8_unit(const Fp8Params& p, int u, int& m, int&
 // runs at 3.15, but sums unscaled blocks).
 // Tried and slower at T=2048 H=3584 V=38912 (253 us): CTA pairs sharing 256 x 256
 // tiles (276 us: half the weight traffic, but the hand-over crosses two CTAs);
-// four promote groups of 64 columns (293 us); halves of 128 columns with their
-// own MMAs and buffers (336 us: the MMAs read the A tile twice).
+// three promote groups (276 us, spills) and four (293 us); halves of 128 columns
+// with their own MMAs and buffers (336 us: the MMAs read the A tile twice); 64
+// columns read before they are added (261 us). The additions themselves are 35 us
+// of it: without them the loop takes 218.
 __global__ void __launch_bounds__(kFThreads, 1)
     logits_fp8_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,

@@ -50,6 +50,10 @@ class FP8Head:
         (bool [T, V] or [V]) marks tokens that must not be drawn; they drop out of
         the log-prob's distribution too. out_logits receives the (masked) logits.
         """
+        if out_logits is None and self.vocab_size % 8:
+            # rows of their own that start on 16 bytes, for wide stores and loads
+            V = self.vocab_size
+            out_logits = hidden.new_empty((hidden.shape[0], -(-V // 8) * 8))[:, :V]
         logits = self.logits(hidden, out_logits=out_logits)
         if mask is not None:
             logits.masked_fill_(mask, float("-inf"))
