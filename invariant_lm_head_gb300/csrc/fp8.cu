@@ -245,24 +245,95 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
   return v;
 }
-// Predicated stores: divergent branches around single stores cost more than they.
-__device__ __forceinline__ void st_global_u32_if(uint16_t* at, uint32_t v, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(at),
-               "r"(v), "r"(static_cast<int>(on))
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                             uint32_t d) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
-__device__ __forceinline__ void st_global_u16_if(uint16_t* at, uint32_t v, bool on) {
+// Predicated stores: divergent branches around single stores cost more than they.
+__device__ __forceinline__ void st_global_v4_if(uint16_t* at, uint4 v, bool on) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::
+          "l"(at),
+      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(static_cast<int>(on))
+      : "memory");
+}
+__device__ __forceinline__ void st_global_u16_if(uint16_t* at, uint16_t v, bool on) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(at),
-               "h"(static_cast<uint16_t>(v)), "r"(static_cast<int>(on))
+               "h"(v), "r"(static_cast<int>(on))
                : "memory");
+}
+
+// A warp's `rows` (of 32) rows of output, one in each lane as kWords pairs of bf16, to
+// rows at any 2-byte address (out + lane * ld), the first n elements of each. A lane
+// turns its row, as a ring, by its address's offset in 16 bytes, so that the ring's
+// 16-byte chunks are the row's aligned ones; sixteen rows at a time go through 4 KB of
+// shared memory, and half a warp writes a row: a chunk a lane, and the first chunk,
+// which holds the row's two ends, element by element. T=200 H=3600 V=32003 takes 43.3
+// us with it (V=32000, by TMA, 40.5); in boxes of 32 columns, as the 4-byte words that
+// they straddle, 53.1: those are 17 writes of parts of a 32-byte sector for 224 bytes.
+template <int kWords>
+__device__ __forceinline__ void store_rows(uint32_t buf, int lane, uint32_t (&w)[kWords],
+                                           uint16_t* out, int64_t ld, int rows, int n) {
+  constexpr int kChunks = kWords / 4;
+  static_assert(kWords % 4 == 0 && kChunks <= 16, "sixteen rows of 256 bytes");
+  {
+    const uint32_t off =
+        static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out + static_cast<int64_t>(lane) * ld)) & 15u;
+    const uint32_t sel = off & 2u ? 0x5432u : 0x7654u;  // by an element
+    const uint32_t last = w[kWords - 1];
+#pragma unroll
+    for (int i = kWords - 1; i > 0; --i) w[i] = __byte_perm(w[i - 1], w[i], sel);
+    w[0] = __byte_perm(last, w[0], sel);
+#pragma unroll
+    for (int by = 1; by <= 2; ++by) {  // by a word, by two
+      const bool turn = off & (by == 1 ? 4u : 8u);
+      uint32_t end[2] = {w[kWords - by], w[kWords - 1]};
+#pragma unroll
+      for (int i = kWords - 1; i >= by; --i) w[i] = turn ? w[i - by] : w[i];
+#pragma unroll
+      for (int i = 0; i < by; ++i) w[i] = turn ? end[i] : w[i];
+    }
+  }
+  const int j = lane & 15;
+#pragma unroll 1
+  for (int first = 0; first < rows; first += 16) {
+    if ((lane & 16) == first) {
+#pragma unroll
+      for (int c = 0; c < kChunks; ++c)
+        st_shared_v4(buf + j * 256 + ((c ^ (j & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
+                     w[4 * c + 3]);
+    }
+    __syncwarp();
+    uint16_t* o = out + static_cast<int64_t>(first + (lane >> 4)) * ld;
+#pragma unroll 4
+    for (int i = 0; i < 8; ++i, o += 2 * ld) {
+      const int r = 2 * i + (lane >> 4);
+      const bool on = first + r < rows;
+      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(o) & 15) >> 1;  // elements
+      const uint32_t row = buf + r * 256;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (j < kChunks) v = ld_shared_v4(row + ((j ^ (r & 7)) << 4));
+      const int e = 8 * j - off;  // the chunk's first element
+      st_global_v4_if(o + e, v, on && j < kChunks && e >= 0 && e + 8 <= n);
+      // the first chunk, where it is not whole
+      const uint16_t x = ld_shared_u16(row + ((r & 7) << 4) + 2 * (j & 7));
+      const int ex = j >= off ? j - off : 2 * kWords + j - off;
+      st_global_u16_if(o + ex, x, on && j < 8 && (off != 0 || n < 8) && ex < n);
+      if (n < 2 * kWords) {  // the vocabulary's end: the chunk that it parts
+        const int c = (off + n) >> 3;
+        const int el = 8 * c + j - off;
+        if (c > 0 && c < kChunks && j < 8)
+          st_global_u16_if(o + el, ld_shared_u16(row + ((c ^ (r & 7)) << 4) + 2 * j), on && el < n);
+      }
+    }
+    __syncwarp();
+  }
 }
 // One row's 32 columns as bf16 into a 32 x 32 box with 64-byte swizzle (16-byte
 // chunk j of row r at j ^ ((r / 2) % 4)), as the TMA store reads it.
@@ -505,65 +576,32 @@ __global__ void __launch_bounds__(kFThreads, 1)
           aphase ^= 1u;
         }
       }
-      if (!warp_on) return true;
+      if (!warp_on || kCh == 0 || col0 >= p.V) return true;
+      if (!p.tma_out) {
+        uint32_t words[kCh > 0 ? kCh * kFChunk / 2 : 4];
+#pragma unroll
+        for (int i = 0; i < kCh * kFChunk / 2; ++i) words[i] = bf16x2_of(sum[2 * i], sum[2 * i + 1]);
+        const int64_t left = p.V - col0;
+        store_rows(stg, lane, words, p.out + static_cast<int64_t>(row0) * p.ld + col0, p.ld,
+                   min(32, p.T - row0),
+                   static_cast<int>(min(static_cast<int64_t>(kCh * kFChunk), left)));
+        return true;
+      }
 #pragma unroll
       for (int b = 0; b < kCh * kFChunk / kFBox; ++b) {
         const int64_t colb = col0 + b * kFBox;
         if (colb >= p.V) break;
-        if (p.tma_out) {
-          // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
-          const uint32_t obox = stg + obuf;
-          obuf ^= kFStagingWarp / 2;
-          if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
-          __syncwarp();
-          stage_box_row(obox, lane, sum + b * kFBox);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
-            bulk_commit_group();
-          }
-        } else {
-          // Rows at odd addresses: turned through shared memory (word w of row r
-          // at w ^ r), so that half a warp writes one row's 64 bytes as the
-          // 4-byte words they straddle.
-#pragma unroll
-          for (int w = 0; w < 16; ++w)
-            st_shared_u32(stg + lane * 64 + ((w ^ (lane & 15)) << 2),
-                          bf16x2_of(sum[b * kFBox + 2 * w], sum[b * kFBox + 2 * w + 1]));
-          __syncwarp();
-          const int n = static_cast<int>(min(static_cast<int64_t>(kFBox), p.V - colb));
-          const int j = lane & 15, half = lane >> 4;
-          const int rows = min(32, p.T - row0);
-          uint16_t* o = p.out + static_cast<int64_t>(row0 + half) * p.ld + colb;
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 16) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = r0 + 2 * i + half;
-              w[i] = ld_shared_u32(stg + r * 64 + ((j ^ (r & 15)) << 2));
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const bool on = r0 + 2 * i + half < rows;
-              // an odd start: word j holds elements 2j - 1 and 2j, the first and
-              // the last element are left over
-              const int odd = static_cast<int>((reinterpret_cast<uintptr_t>(o) >> 1) & 1);
-              const uint32_t before = __shfl_up_sync(0xffffffffu, w[i], 1, 16);
-              const uint32_t v = odd ? (before >> 16) | (w[i] << 16) : w[i];
-              st_global_u32_if(o + 2 * j - odd, v, on && 2 * j >= odd && 2 * j + 1 - odd < n);
-              if (n == kFBox) {
-                st_global_u16_if(o + (j == 0 ? 0 : kFBox - 1), j == 0 ? w[i] : w[i] >> 16,
-                                 on && odd && (j == 0 || j == 15));
-              } else {  // the vocabulary's end: the elements that made no whole word
-                st_global_u16_if(o, w[i], on && odd && j == 0);
-                st_global_u16_if(o + n - 1, v, on && 2 * j - odd == n - 1 && n > odd);
-              }
-              o += 2 * p.ld;
-            }
-          }
-          __syncwarp();
+        // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
+        const uint32_t obox = stg + obuf;
+        obuf ^= kFStagingWarp / 2;
+        if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
+        __syncwarp();
+        stage_box_row(obox, lane, sum + b * kFBox);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
+          bulk_commit_group();
         }
       }
       return true;

@@ -153,6 +153,27 @@ def test_logits_into_strided_rows(T, ld, off):
     assert (buf[rest] == 7.0).all()  # nothing outside the logits is written
 
 
+@pytest.mark.parametrize("V", [5, 33, 250, 1003])
+def test_logits_rows_at_any_address(V):
+    # whatever a row's offset in 16 bytes, and wherever the vocabulary ends in it
+    import torch
+
+    T = 45
+    ops = operands(T, 256, V)
+    ld8 = -(-V // 8) * 8
+    aligned = torch.empty(T, ld8, dtype=torch.bfloat16, device=dev())[:, :V]
+    lmh.lmhead_logits_fp8(*ops, out_logits=aligned)
+    check_logits(aligned, *ops)
+    for ld in (V, V + 1, ld8 + 2, ld8 + 4):
+        for off in range(8):
+            buf = torch.full((off + T * ld + 8,), 7.0, dtype=torch.bfloat16, device=dev())
+            out = buf[off:off + T * ld].view(T, ld)[:, :V]
+            lmh.lmhead_logits_fp8(*ops, out_logits=out)
+            assert torch.equal(out.view(torch.int16), aligned.view(torch.int16)), (ld, off)
+            out.fill_(7.0)
+            assert (buf == 7.0).all(), (ld, off)
+
+
 def test_logits_a_bad_row_stays_alone():
     import torch
 
