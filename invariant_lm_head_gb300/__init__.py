@@ -548,6 +548,12 @@ def _need_rows(t, name: str, dtype, device, shape=None) -> int:
     return ld
 
 
+def _need_cuda(t, name: str):
+    """Every other tensor of a call is on this one's device."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
+
+
 def _need_out(t, name: str, dtype, device, shape):
     _need(t, name, dtype, device, len(shape))
     if tuple(t.shape) != shape:
@@ -576,6 +582,7 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
         out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _need_out(out_scale, "out_scale", torch.float32, dev, shape)
+    _need_cuda(x, "x")
     rc = library().lmhead_quantize_fp8(x.data_ptr(), rows, cols, ld, block_rows, out.data_ptr(),
                                        out_scale.data_ptr(), _stream_ptr(stream))
     if rc:
@@ -608,6 +615,7 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_log
         ld = V
     else:
         ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev, (T, V))
+    _need_cuda(hidden_q, "hidden_q")
     rc = library().lmhead_logits_fp8(hidden_q.data_ptr(), hidden_scale.data_ptr(),
                                      weight_q.data_ptr(), weight_scale.data_ptr(), T, H, V,
                                      out_logits.data_ptr(), ld, _stream_ptr(stream))
@@ -658,6 +666,7 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
         _need_out(out_logprob, "out_logprob", f32, dev, (T,))
     elif want_logprob:
         out_logprob = torch.empty((T,), dtype=f32, device=dev)
+    _need_cuda(logits, "logits")
     rc = library().lmhead_sample(logits.data_ptr(), T, V, ld, t, row_t, k, row_k, p, row_p, m,
                                  row_m, uniform.data_ptr(), out_token.data_ptr(),
                                  _ptr(out_logprob), _stream_ptr(stream))

@@ -144,3 +144,18 @@ def test_binding_refusals(lib):
         lmh.lmhead_sample(x, u, top_k=torch.ones(4))
     with pytest.raises(ValueError):
         lmh.lmhead_sample(x, u, top_k=-1)
+
+
+def test_binding_refuses_host_tensors(lib):
+    # a host pointer must never reach a kernel, whatever else is right
+    torch = pytest.importorskip("torch")
+    before = lib.lmhead_kernel_launches()
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    hq, wq = (torch.zeros(n, 256, dtype=torch.float8_e4m3fn) for n in (4, 1000))
+    hs, ws = torch.zeros(4, 2), torch.zeros(8, 2)
+    for call in (lambda: lmh.lmhead_quantize_fp8(x), lambda: lmh.lmhead_quantize_fp8(x, 128),
+                 lambda: lmh.lmhead_logits_fp8(hq, hs, wq, ws),
+                 lambda: lmh.lmhead_sample(x, torch.zeros(4))):
+        with pytest.raises(ValueError, match="CUDA device"):
+            call()
+    assert lib.lmhead_kernel_launches() == before
