@@ -148,7 +148,8 @@ int make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer
 // Output map of a store epilogue: `cols` x `rows` elements, rows `row_bytes`
 // apart. fp32: 32 x 128 box, 128-byte swizzle; bf16: 32 x 128 box, 64-byte
 // swizzle (the staging layouts the epilogue writes). Stores outside the
-// tensor are clipped by TMA.
+// tensor are clipped by TMA, along a row in whole 16-byte chunks: where `cols`
+// ends inside one, the rest of that chunk is written too.
 int make_out_tmap(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows, uint64_t row_bytes,
                   bool f32, bool transposed = false) {
   cuuint64_t dims[2] = {cols, rows};

@@ -219,7 +219,8 @@ struct Fp8Params {
   const float* ws;       // [ceil(V / 128)][KB]
   uint16_t* out;
   int64_t ld;
-  int tma_out;           // rows on 16-byte boundaries: the output leaves by TMA
+  int tma_out;           // rows on 16-byte boundaries: the output leaves by TMA,
+  int v_tma;             // which writes whole 16-byte chunks: its columns, V / 8 * 8
   unsigned* status;
 };
 
@@ -600,8 +601,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
-          bulk_commit_group();
+          if (colb < p.v_tma) tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
+          bulk_commit_group();  // an empty one too: the buffers' turns are counted in groups
+        }
+        if (p.v_tma < p.V && p.v_tma < colb + kFBox && row < p.T) {
+          // the vocabulary's last columns (at most seven): a chunk that TMA would fill
+          // with zeros past the row's end
+          const int j = (p.v_tma - static_cast<int>(colb)) >> 3;
+          const uint4 v = ld_shared_v4(obox + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          uint16_t* o = p.out + static_cast<int64_t>(row) * p.ld + p.v_tma;
+#pragma unroll
+          for (int i = 0; i < 7; ++i)
+            st_global_u16_if(o + i, static_cast<uint16_t>(w[i / 2] >> (16 * (i & 1))),
+                             p.v_tma + i < p.V);
         }
       }
       return true;
@@ -757,10 +770,11 @@ extern "C" int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_sc
   p.ws = weight_scale;
   p.out = logits;
   p.ld = ld_logits;
-  p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16)) ? 1 : 0;
+  p.v_tma = static_cast<int>(V / 8 * 8);
+  p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16) && p.v_tma > 0) ? 1 : 0;
   p.status = status;
   CUtensorMap ta, tb, tc{};
-  if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, V, T, ld_logits * 2)) != LMH_OK)
+  if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, p.v_tma, T, ld_logits * 2)) != LMH_OK)
     return rc;
   if ((rc = api_make_tmap_u8(&ta, hidden_q, H, T, H, kFK, p.a_rows)) != LMH_OK) return rc;
   if ((rc = api_make_tmap_u8(&tb, weight_q, H, V, H, kFK, p.tile_n)) !=
