@@ -606,9 +606,11 @@ struct Row {
       if (lane >= off) to += o;
     }
     const uint32_t here = __ballot_sync(0xffffffffu, rank >= to - own && rank < to);
-    const int who = __ffs(here) - 1;
+    // No CTA holds it where the row changed between two counts of it: then CTA 0
+    // looks for a rank that no row has, finds nothing and writes token -1.
+    const int who = here ? __ffs(here) - 1 : 0;
     const uint32_t there = __shfl_sync(0xffffffffu, rank - (to - own), who);
-    return make_int4(kLook, who, bin_key(bin), static_cast<int>(there));
+    return make_int4(kLook, who, bin_key(bin), here ? static_cast<int>(there) : kNone);
   }
 };
 

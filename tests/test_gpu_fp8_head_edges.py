@@ -4,7 +4,7 @@ import pytest
 
 import invariant_lm_head_gb300 as lmh
 from helpers import dev
-from test_gpu_fp8_head import check_logits, operands
+from test_gpu_fp8_head import check_logits, logit_rows, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,28 @@ def test_logits_of_one_row_leave_the_next_alone():
         lmh.lmhead_logits_fp8(*ops, out_logits=buf[i:i + 1])
         check_logits(buf[i:i + 1], *ops)
     assert (buf[1:8] == 7.0).all()
+
+
+@pytest.mark.parametrize("T", [3, 60, 120, 200])
+def test_sample_writes_every_token(T):
+    # Rows that another stream rewrites during the call, between values inside and
+    # outside the direct range: a senseless token, but always a token or -1.
+    import torch
+
+    V = 3003
+    x, _ = logit_rows(T, T, V)
+    good = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    wild = torch.randint(-32768, 32767, (T, V), device=dev(), dtype=torch.int16).view(torch.bfloat16)
+    lg, u = good.clone(), torch.rand(T, device=dev())
+    tok = torch.empty(T, dtype=torch.int32, device=dev())
+    bad = torch.zeros((), dtype=torch.int64, device=dev())
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for i in range(200):
+        with torch.cuda.stream(other):
+            lg.copy_(wild if i % 2 else good)
+        tok.fill_(1 << 30)
+        lmh.lmhead_sample(lg, u, 0.9, top_p=0.9, top_k=1000, out_token=tok)
+        bad += ((tok < -1) | (tok >= V)).sum()
+    torch.cuda.synchronize()
+    assert bad.item() == 0
