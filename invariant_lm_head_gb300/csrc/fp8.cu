@@ -41,9 +41,11 @@ constexpr int kQBlock = 128;  // elements of a scale block along K (and along V)
 // rounded to nearest, y = x * c is exact wherever q does not round to zero, and
 // y / am is corrected from y * r by its exact remainder (P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000 processor",
-// IBM J. Res. Dev. 34(1), 1990).
+// IBM J. Res. Dev. 34(1), 1990). It is taken from -y and -r: a zero's remainder
+// is +0 either way, and +0 * -r is the zero whose addition keeps the quotient's
+// sign (-0 * 448 / a is -0).
 struct BlockScale {
-  float c, neg_am, r, scale;
+  float neg_c, am, neg_r, scale;
 };
 
 __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits16) {
@@ -53,19 +55,19 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits16) {
   BlockScale s;
   if (bits >= 0x7f800000u) {  // inf or NaN in the block: every q becomes NaN
     s.scale = __uint_as_float(bits);
-    s.c = 0.f;
-    s.neg_am = -1.f;
-    s.r = __uint_as_float(0x7fffffffu);
+    s.neg_c = 0.f;
+    s.am = 1.f;
+    s.neg_r = __uint_as_float(0x7fffffffu);
     return s;
   }
   const float a = fmaxf(__uint_as_float(bits), 0x1p-60f);
   const uint32_t ab = __float_as_uint(a);
   const int e = static_cast<int>(ab >> 23) - 127;
   const float am = __uint_as_float((ab & 0x007fffffu) | 0x3f800000u);
-  s.c = 448.f * __uint_as_float(static_cast<uint32_t>(127 - (e < 127 ? e : 126)) << 23);
-  if (e == 127) s.c *= 0.5f;
-  s.neg_am = -am;
-  s.r = __frcp_rn(am);
+  s.neg_c = -448.f * __uint_as_float(static_cast<uint32_t>(127 - (e < 127 ? e : 126)) << 23);
+  if (e == 127) s.neg_c *= 0.5f;
+  s.am = am;
+  s.neg_r = -__frcp_rn(am);
   s.scale = __fdiv_rn(a, 448.f);
   return s;
 }
@@ -77,12 +79,12 @@ __device__ __forceinline__ uint32_t amax_u16x2(uint32_t m, uint32_t w) {
 // Two quotients to a pair of e4m3 bytes (low half first).
 __device__ __forceinline__ uint32_t quantize2(uint32_t w, const BlockScale& s) {
   const f32x2 x = f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  const f32x2 y = f2_mul(x, f2_pack(s.c, s.c));
-  const f32x2 r2 = f2_pack(s.r, s.r);
-  const f32x2 q0 = f2_mul(y, r2);
-  const f32x2 rem = f2_fma(q0, f2_pack(s.neg_am, s.neg_am), y);
+  const f32x2 neg_y = f2_mul(x, f2_pack(s.neg_c, s.neg_c));
+  const f32x2 neg_r = f2_pack(s.neg_r, s.neg_r);
+  const f32x2 q0 = f2_mul(neg_y, neg_r);
+  const f32x2 neg_rem = f2_fma(q0, f2_pack(s.am, s.am), neg_y);
   float lo, hi;
-  f2_unpack(f2_fma(rem, r2, q0), lo, hi);
+  f2_unpack(f2_fma(neg_rem, neg_r, q0), lo, hi);
   uint16_t out;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
   return out;

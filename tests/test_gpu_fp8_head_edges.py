@@ -1,10 +1,13 @@
 """Edges of the fp8 head on the GPU."""
 
+import numpy as np
 import pytest
 
 import invariant_lm_head_gb300 as lmh
-from helpers import dev
-from test_gpu_fp8_head import check_logits, logit_rows, operands
+import workloads as W
+from helpers import dev, to_dev_bf16
+from oracle import fp8_head as o
+from test_gpu_fp8_head import bf16_values, check_logits, logit_rows, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +68,19 @@ def test_sample_writes_every_token(T):
         bad += ((tok < -1) | (tok >= V)).sum()
     torch.cuda.synchronize()
     assert bad.item() == 0
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_keeps_the_sign_of_zero(block_rows):
+    # x * 448 / a rounded once has x's sign, in -0 and in what rounds to it
+    bits = W.random_bf16(3, (130, 400), 1.0)
+    bits[:, ::3] = 0x8000
+    bits[:, 1::9] = 0x0000
+    bits[:, 2::9] = 0x8001  # the smallest of all, to -0
+    bits[:, 4::9] = 0x0001
+    bits[5] = 0x8000        # blocks of nothing else (of 1 x 128)
+    q, _ = lmh.lmhead_quantize_fp8(to_dev_bf16(bits), block_rows)
+    rq, _ = o.quantize(bf16_values(bits), block_rows)
+    got = q.float().cpu().numpy().astype(np.float64)
+    assert np.array_equal(got, rq) and np.array_equal(np.signbit(got), np.signbit(rq))
+    assert np.array_equal(np.signbit(got), bits >= 0x8000)
