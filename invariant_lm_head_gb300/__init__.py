@@ -133,12 +133,29 @@ def _torch():
 def _stream_ptr(stream) -> Optional[int]:
     if stream is not None:
         return stream.cuda_stream
+    return _torch().cuda.current_stream().cuda_stream
+
+
+def _launch_stream(t, name: str, stream) -> int:
+    """The handle of the stream that a call on t's device runs on (None: the current one).
+
+    A kernel runs on the current device. Addresses of the host or of another device
+    must never reach it, nor work be put on another device's stream. Every other
+    tensor of a call is on t's device.
+    """
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
     torch = _torch()
-    if torch.cuda.is_initialized():
-        # the current stream's handle without a Stream object around it (0.2 us
-        # instead of 2.8, of a short call's ten)
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return torch.cuda.current_stream().cuda_stream
+    current = torch.cuda.current_device()
+    if t.device.index != current:
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
+    if stream is None:
+        # the handle without a Stream object around it (0.2 us instead of 2.8, of a
+        # short call's ten)
+        return torch._C._cuda_getCurrentRawStream(current)
+    if stream.device.index != current:
+        raise ValueError(f"stream is on {stream.device}, but the current device is cuda:{current}")
+    return stream.cuda_stream
 
 
 def _ptr(t) -> Optional[int]:
@@ -220,6 +237,7 @@ def lmhead_logprob_fwd_host(hidden_host, weight_host, labels_host, inv_temperatu
     for t, n in ((out_logprob_host, "out_logprob_host"), (out_entropy_host, "out_entropy_host")):
         if t is not None:
             _need(t, n, torch.float32, cpu, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     if out_logprob is None:
         out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and (want_entropy or out_entropy_host is not None):
@@ -231,8 +249,8 @@ def lmhead_logprob_fwd_host(hidden_host, weight_host, labels_host, inv_temperatu
     rc = library().lmhead_logprob_fwd_host(
         _ptr(hidden_host), _ptr(weight_host), _ptr(labels_host), T, H, V, float(inv_temperature),
         _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(out_logprob), _ptr(out_entropy),
-        _ptr(out_lse), _ptr(out_logprob_host), _ptr(out_entropy_host), _ptr(ws), ws_bytes,
-        _stream_ptr(stream), cs)
+        _ptr(out_lse), _ptr(out_logprob_host), _ptr(out_entropy_host), _ptr(ws), ws_bytes, st,
+        cs)
     _check("lmhead_logprob_fwd_host", rc)
     return out_logprob, out_entropy, out_lse
 
@@ -248,6 +266,7 @@ def _fwd(name, hidden, weight, labels, inv_temperature, out_logprob, out_entropy
     V = weight.shape[0]
     if weight.shape[1] != H or labels.shape[0] != T:
         raise ValueError("shape mismatch between hidden, weight and labels")
+    st = _launch_stream(hidden, "hidden", stream)
     if out_logprob is None:
         out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and want_entropy:
@@ -262,7 +281,7 @@ def _fwd(name, hidden, weight, labels, inv_temperature, out_logprob, out_entropy
             _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse)]
     if name == "lmhead_logprob_fwd_stats":
         args.append(_ptr(out_sum_p2))
-    rc = getattr(lib, name)(*args, _ptr(ws), ws_bytes, _stream_ptr(stream))
+    rc = getattr(lib, name)(*args, _ptr(ws), ws_bytes, st)
     _check(name, rc)
     return out_logprob, out_entropy, out_lse, out_sum_p2
 
@@ -278,6 +297,7 @@ def lmhead_logprob_bwd(hidden, weight, labels, grad_logprob, inv_temperature: fl
     _need(grad_logprob, "grad_logprob", torch.float32, dev, 1)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -287,7 +307,7 @@ def lmhead_logprob_bwd(hidden, weight, labels, grad_logprob, inv_temperature: fl
     ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev)
     rc = library().lmhead_logprob_bwd(_ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob),
                                       _ptr(lse), T, H, V, float(inv_temperature), _ptr(grad_hidden),
-                                      _ptr(grad_weight), _ptr(ws), ws_bytes, _stream_ptr(stream))
+                                      _ptr(grad_weight), _ptr(ws), ws_bytes, st)
     _check("lmhead_logprob_bwd", rc)
     return grad_hidden, grad_weight
 
@@ -305,6 +325,7 @@ def lmhead_logprob_entropy_bwd(hidden, weight, labels, grad_logprob, grad_entrop
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -315,7 +336,7 @@ def lmhead_logprob_entropy_bwd(hidden, weight, labels, grad_logprob, grad_entrop
     rc = library().lmhead_logprob_entropy_bwd(
         _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, float(inv_temperature), _ptr(grad_hidden),
-        _ptr(grad_weight), _ptr(ws), ws_bytes, _stream_ptr(stream))
+        _ptr(grad_weight), _ptr(ws), ws_bytes, st)
     _check("lmhead_logprob_entropy_bwd", rc)
     return grad_hidden, grad_weight
 
@@ -341,6 +362,7 @@ def lmhead_logprob_bwd_chunked(hidden, weight, labels, grad_logprob, inv_tempera
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -354,7 +376,7 @@ def lmhead_logprob_bwd_chunked(hidden, weight, labels, grad_logprob, inv_tempera
         _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, float(inv_temperature), int(row_chunk),
         _ptr(grad_hidden), _ptr(grad_weight), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+        workspace.numel() * workspace.element_size(), st)
     _check("lmhead_logprob_bwd_chunked", rc)
     return grad_hidden, grad_weight
 
@@ -376,6 +398,7 @@ def lmhead_logprob_bwd_shard(hidden, weight_shard, labels, grad_logprob, lse, v_
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight_shard.shape[0]
     if grad_hidden_part is None:
@@ -386,7 +409,7 @@ def lmhead_logprob_bwd_shard(hidden, weight_shard, labels, grad_logprob, lse, v_
     rc = library().lmhead_logprob_bwd_shard(
         _ptr(hidden), _ptr(weight_shard), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, int(v_offset), float(inv_temperature),
-        _ptr(grad_hidden_part), _ptr(grad_weight), _ptr(ws), ws_bytes, _stream_ptr(stream))
+        _ptr(grad_hidden_part), _ptr(grad_weight), _ptr(ws), ws_bytes, st)
     _check("lmhead_logprob_bwd_shard", rc)
     return grad_hidden_part, grad_weight
 
@@ -399,13 +422,14 @@ def lmhead_sum_ranks_bf16(parts, *, out=None, stream=None):
         raise TypeError("parts must be a float32 tensor")
     if parts.device != dev or not parts.is_contiguous() or parts.dim() < 2:
         raise ValueError("parts must be a contiguous tensor [n, ...]")
+    st = _launch_stream(parts, "parts", stream)
     n = parts.shape[0]
     count = parts[0].numel()
     if out is None:
         out = torch.empty(parts.shape[1:], dtype=torch.bfloat16, device=dev)
     if out.dtype != torch.bfloat16 or out.numel() != count or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor of parts[0]'s size")
-    rc = library().lmhead_sum_ranks_bf16(_ptr(parts), n, count, _ptr(out), _stream_ptr(stream))
+    rc = library().lmhead_sum_ranks_bf16(_ptr(parts), n, count, _ptr(out), st)
     _check("lmhead_sum_ranks_bf16", rc)
     return out
 
@@ -456,6 +480,7 @@ def _logits(name, logits, labels, inv_temperature, out_logprob, out_entropy, out
     dev = logits.device
     _need(logits, "logits", torch.bfloat16, dev, 2)
     _need(labels, "labels", torch.int32, dev, 1)
+    st = _launch_stream(logits, "logits", stream)
     T, V = logits.shape
     if out_logprob is None:
         out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
@@ -471,7 +496,7 @@ def _logits(name, logits, labels, inv_temperature, out_logprob, out_entropy, out
     args += [_ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse)]
     if name in ("logprob_from_logits_stats", "logprob_from_logits_div"):
         args.append(_ptr(out_sum_p2))
-    rc = getattr(library(), name)(*args, _stream_ptr(stream))
+    rc = getattr(library(), name)(*args, st)
     _check(name, rc)
     return out_logprob, out_entropy, out_lse, out_sum_p2
 
@@ -497,10 +522,10 @@ def lmhead_logprob_fwd_partials(hidden, weight_shard, labels, v_offset: int,
         if tuple(t.shape) != (n, T):
             raise ValueError(f"{nm} must be [{n}, {T}]")
     _need(label_logit, "label_logit", torch.float32, dev, 1)
+    st = _launch_stream(hidden, "hidden", stream)
     rc = library().lmhead_logprob_fwd_partials(
         _ptr(hidden), _ptr(weight_shard), _ptr(labels), T, H, V, int(v_offset),
-        float(inv_temperature), _ptr(part_m), _ptr(part_s), _ptr(part_u), _ptr(label_logit),
-        _stream_ptr(stream))
+        float(inv_temperature), _ptr(part_m), _ptr(part_s), _ptr(part_u), _ptr(label_logit), st)
     _check("lmhead_logprob_fwd_partials", rc)
 
 
@@ -509,6 +534,7 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
     """Merge whole-vocabulary planes into (logprob, entropy, lse), f32 [T]."""
     torch = _torch()
     dev = labels.device
+    st = _launch_stream(labels, "labels", stream)
     T = labels.shape[0]
     out_logprob = torch.empty(T, device=dev) if out_logprob is None else out_logprob
     out_entropy = torch.empty(T, device=dev) if out_entropy is None else out_entropy
@@ -520,7 +546,7 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
             raise ValueError(f"{nm} must be [{n}, {T}]")
     rc = library().lmhead_logprob_merge(
         _ptr(part_m), _ptr(part_s), _ptr(part_u), _ptr(label_logit), _ptr(labels), T, int(V),
-        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), _stream_ptr(stream))
+        _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse), st)
     _check("lmhead_logprob_merge", rc)
     return out_logprob, out_entropy, out_lse
 
@@ -548,12 +574,6 @@ def _need_rows(t, name: str, dtype, device, shape=None) -> int:
     return ld
 
 
-def _need_cuda(t, name: str):
-    """Every other tensor of a call is on this one's device."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
-
-
 def _need_out(t, name: str, dtype, device, shape):
     _need(t, name, dtype, device, len(shape))
     if tuple(t.shape) != shape:
@@ -573,6 +593,7 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
     rows, cols = x.shape
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
+    st = _launch_stream(x, "x", stream)
     shape = (-(-rows // block_rows), -(-cols // 128))
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
@@ -582,9 +603,8 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
         out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
     else:
         _need_out(out_scale, "out_scale", torch.float32, dev, shape)
-    _need_cuda(x, "x")
     rc = library().lmhead_quantize_fp8(x.data_ptr(), rows, cols, ld, block_rows, out.data_ptr(),
-                                       out_scale.data_ptr(), _stream_ptr(stream))
+                                       out_scale.data_ptr(), st)
     if rc:
         _check("lmhead_quantize_fp8", rc)
     return out, out_scale
@@ -610,15 +630,15 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_log
     kb = -(-H // 128)
     _need_out(hidden_scale, "hidden_scale", f32, dev, (T, kb))
     _need_out(weight_scale, "weight_scale", f32, dev, (-(-V // 128), kb))
+    st = _launch_stream(hidden_q, "hidden_q", stream)
     if out_logits is None:
         out_logits = torch.empty((T, V), dtype=torch.bfloat16, device=dev)
         ld = V
     else:
         ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev, (T, V))
-    _need_cuda(hidden_q, "hidden_q")
     rc = library().lmhead_logits_fp8(hidden_q.data_ptr(), hidden_scale.data_ptr(),
                                      weight_q.data_ptr(), weight_scale.data_ptr(), T, H, V,
-                                     out_logits.data_ptr(), ld, _stream_ptr(stream))
+                                     out_logits.data_ptr(), ld, st)
     if rc:
         _check("lmhead_logits_fp8", rc)
     return out_logits
@@ -658,6 +678,7 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
     k = int(k)
     if not 0 <= k <= 0x7fffffff:
         raise ValueError("top_k must be in [0, 2^31)")
+    st = _launch_stream(logits, "logits", stream)
     if out_token is None:
         out_token = torch.empty((T,), dtype=i32, device=dev)
     else:
@@ -666,10 +687,9 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
         _need_out(out_logprob, "out_logprob", f32, dev, (T,))
     elif want_logprob:
         out_logprob = torch.empty((T,), dtype=f32, device=dev)
-    _need_cuda(logits, "logits")
     rc = library().lmhead_sample(logits.data_ptr(), T, V, ld, t, row_t, k, row_k, p, row_p, m,
                                  row_m, uniform.data_ptr(), out_token.data_ptr(),
-                                 _ptr(out_logprob), _stream_ptr(stream))
+                                 _ptr(out_logprob), st)
     if rc:
         _check("lmhead_sample", rc)
     return out_token, out_logprob
@@ -793,9 +813,9 @@ def lmhead_engine_gemm(A, B, out=None, a_kmajor: bool = True, b_kmajor: bool = T
     M, K = A.shape if a_kmajor else (A.shape[1], A.shape[0])
     N = B.shape[0] if b_kmajor else B.shape[1]
     layout = (0 if a_kmajor else 1) | (0 if b_kmajor else 2)
+    st = _launch_stream(A, "A", stream)
     if out is None:
         out = torch.empty(M, N, dtype=torch.float32, device=dev)
-    rc = library().lmhead_engine_gemm(_ptr(A), _ptr(B), M, N, K, layout, _ptr(out),
-                                      _stream_ptr(stream))
+    rc = library().lmhead_engine_gemm(_ptr(A), _ptr(B), M, N, K, layout, _ptr(out), st)
     _check("lmhead_engine_gemm", rc)
     return out
