@@ -158,6 +158,27 @@ def _launch_stream(t, name: str, stream) -> int:
     return stream.cuda_stream
 
 
+def _empty_on(stream):
+    """torch.empty for what a call on this stream writes.
+
+    On a stream other than the current one the memory is that stream's: the current
+    stream's may still be in use by work ahead of the call, and a workspace would go
+    back to it, free to be written, while the call runs. What the current stream does
+    with an output before it is dropped is waited for as well.
+    """
+    torch = _torch()
+    if stream is None:
+        return torch.empty
+
+    def empty(*size, **options):
+        with torch.cuda.stream(stream):
+            t = torch.empty(*size, **options)
+        t.record_stream(torch.cuda.current_stream())
+        return t
+
+    return empty
+
+
 def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
@@ -181,11 +202,10 @@ def lmhead_workspace_size(op: int, T: int, H: int, V: int) -> int:
     return n
 
 
-def _workspace(op, T, H, V, workspace, device):
-    torch = _torch()
+def _workspace(op, T, H, V, workspace, device, empty):
     need = lmhead_workspace_size(op, T, H, V)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        workspace = empty(max(need, 16), dtype=_torch().uint8, device=device)
     return workspace, workspace.numel() * workspace.element_size()
 
 
@@ -238,13 +258,14 @@ def lmhead_logprob_fwd_host(hidden_host, weight_host, labels_host, inv_temperatu
         if t is not None:
             _need(t, n, torch.float32, cpu, 1)
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     if out_logprob is None:
-        out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+        out_logprob = empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and (want_entropy or out_entropy_host is not None):
-        out_entropy = torch.empty(T, dtype=torch.float32, device=dev)
+        out_entropy = empty(T, dtype=torch.float32, device=dev)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(T, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(LMH_OP_FWD, T, H, V, workspace, dev)
+        out_lse = empty(T, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(LMH_OP_FWD, T, H, V, workspace, dev, empty)
     cs = None if copy_stream is None else ctypes.c_void_p(copy_stream.cuda_stream)
     rc = library().lmhead_logprob_fwd_host(
         _ptr(hidden_host), _ptr(weight_host), _ptr(labels_host), T, H, V, float(inv_temperature),
@@ -267,15 +288,16 @@ def _fwd(name, hidden, weight, labels, inv_temperature, out_logprob, out_entropy
     if weight.shape[1] != H or labels.shape[0] != T:
         raise ValueError("shape mismatch between hidden, weight and labels")
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     if out_logprob is None:
-        out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+        out_logprob = empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and want_entropy:
-        out_entropy = torch.empty(T, dtype=torch.float32, device=dev)
+        out_entropy = empty(T, dtype=torch.float32, device=dev)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(T, dtype=torch.float32, device=dev)
+        out_lse = empty(T, dtype=torch.float32, device=dev)
     if out_sum_p2 is None and want_sum_p2:
-        out_sum_p2 = torch.empty(T, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(LMH_OP_FWD, T, H, V, workspace, dev)
+        out_sum_p2 = empty(T, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(LMH_OP_FWD, T, H, V, workspace, dev, empty)
     lib = library()
     args = [_ptr(hidden), _ptr(weight), _ptr(labels), T, H, V, float(inv_temperature),
             _ptr(out_logprob), _ptr(out_entropy), _ptr(out_lse)]
@@ -298,13 +320,14 @@ def lmhead_logprob_bwd(hidden, weight, labels, grad_logprob, inv_temperature: fl
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, 1)
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
-        grad_hidden = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        grad_hidden = empty(T, H, dtype=torch.bfloat16, device=dev)
     if grad_weight is None:
-        grad_weight = torch.empty(V, H, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev)
+        grad_weight = empty(V, H, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev, empty)
     rc = library().lmhead_logprob_bwd(_ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob),
                                       _ptr(lse), T, H, V, float(inv_temperature), _ptr(grad_hidden),
                                       _ptr(grad_weight), _ptr(ws), ws_bytes, st)
@@ -326,13 +349,14 @@ def lmhead_logprob_entropy_bwd(hidden, weight, labels, grad_logprob, grad_entrop
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
-        grad_hidden = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        grad_hidden = empty(T, H, dtype=torch.bfloat16, device=dev)
     if grad_weight is None:
-        grad_weight = torch.empty(V, H, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev)
+        grad_weight = empty(V, H, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev, empty)
     rc = library().lmhead_logprob_entropy_bwd(
         _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, float(inv_temperature), _ptr(grad_hidden),
@@ -363,15 +387,16 @@ def lmhead_logprob_bwd_chunked(hidden, weight, labels, grad_logprob, inv_tempera
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
-        grad_hidden = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        grad_hidden = empty(T, H, dtype=torch.bfloat16, device=dev)
     if grad_weight is None:
-        grad_weight = torch.empty(V, H, dtype=torch.float32, device=dev)
+        grad_weight = empty(V, H, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = torch.empty(max(lmhead_workspace_size_bwd(T, H, V, row_chunk), 16),
-                                dtype=torch.uint8, device=dev)
+        workspace = empty(max(lmhead_workspace_size_bwd(T, H, V, row_chunk), 16),
+                          dtype=torch.uint8, device=dev)
     rc = library().lmhead_logprob_bwd_chunked(
         _ptr(hidden), _ptr(weight), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, float(inv_temperature), int(row_chunk),
@@ -399,13 +424,14 @@ def lmhead_logprob_bwd_shard(hidden, weight_shard, labels, grad_logprob, lse, v_
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
     st = _launch_stream(hidden, "hidden", stream)
+    empty = _empty_on(stream)
     T, H = hidden.shape
     V = weight_shard.shape[0]
     if grad_hidden_part is None:
-        grad_hidden_part = torch.empty(T, H, dtype=torch.float32, device=dev)
+        grad_hidden_part = empty(T, H, dtype=torch.float32, device=dev)
     if grad_weight is None:
-        grad_weight = torch.empty(V, H, dtype=torch.float32, device=dev)
-    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev)
+        grad_weight = empty(V, H, dtype=torch.float32, device=dev)
+    ws, ws_bytes = _workspace(LMH_OP_BWD, T, H, V, workspace, dev, empty)
     rc = library().lmhead_logprob_bwd_shard(
         _ptr(hidden), _ptr(weight_shard), _ptr(labels), _ptr(grad_logprob), _ptr(grad_entropy),
         _ptr(lse), _ptr(entropy), T, H, V, int(v_offset), float(inv_temperature),
@@ -423,10 +449,11 @@ def lmhead_sum_ranks_bf16(parts, *, out=None, stream=None):
     if parts.device != dev or not parts.is_contiguous() or parts.dim() < 2:
         raise ValueError("parts must be a contiguous tensor [n, ...]")
     st = _launch_stream(parts, "parts", stream)
+    empty = _empty_on(stream)
     n = parts.shape[0]
     count = parts[0].numel()
     if out is None:
-        out = torch.empty(parts.shape[1:], dtype=torch.bfloat16, device=dev)
+        out = empty(parts.shape[1:], dtype=torch.bfloat16, device=dev)
     if out.dtype != torch.bfloat16 or out.numel() != count or not out.is_contiguous():
         raise ValueError("out must be a contiguous bf16 tensor of parts[0]'s size")
     rc = library().lmhead_sum_ranks_bf16(_ptr(parts), n, count, _ptr(out), st)
@@ -481,15 +508,16 @@ def _logits(name, logits, labels, inv_temperature, out_logprob, out_entropy, out
     _need(logits, "logits", torch.bfloat16, dev, 2)
     _need(labels, "labels", torch.int32, dev, 1)
     st = _launch_stream(logits, "logits", stream)
+    empty = _empty_on(stream)
     T, V = logits.shape
     if out_logprob is None:
-        out_logprob = torch.empty(T, dtype=torch.float32, device=dev)
+        out_logprob = empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and want_entropy:
-        out_entropy = torch.empty(T, dtype=torch.float32, device=dev)
+        out_entropy = empty(T, dtype=torch.float32, device=dev)
     if out_lse is None and want_lse:
-        out_lse = torch.empty(T, dtype=torch.float32, device=dev)
+        out_lse = empty(T, dtype=torch.float32, device=dev)
     if out_sum_p2 is None and want_sum_p2:
-        out_sum_p2 = torch.empty(T, dtype=torch.float32, device=dev)
+        out_sum_p2 = empty(T, dtype=torch.float32, device=dev)
     args = [_ptr(logits), _ptr(labels), T, V, float(inv_temperature)]
     if name == "logprob_from_logits_div":
         args.append(_ptr(row_t))
@@ -535,10 +563,11 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
     torch = _torch()
     dev = labels.device
     st = _launch_stream(labels, "labels", stream)
+    empty = _empty_on(stream)
     T = labels.shape[0]
-    out_logprob = torch.empty(T, device=dev) if out_logprob is None else out_logprob
-    out_entropy = torch.empty(T, device=dev) if out_entropy is None else out_entropy
-    out_lse = torch.empty(T, device=dev) if out_lse is None else out_lse
+    out_logprob = empty(T, device=dev) if out_logprob is None else out_logprob
+    out_entropy = empty(T, device=dev) if out_entropy is None else out_entropy
+    out_lse = empty(T, device=dev) if out_lse is None else out_lse
     n = -(-int(V) // 1024)
     for t, nm in ((part_m, "part_m"), (part_s, "part_s"), (part_u, "part_u")):
         _need(t, nm, torch.float32, dev, 2)
@@ -594,13 +623,14 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
     st = _launch_stream(x, "x", stream)
+    empty = _empty_on(stream)
     shape = (-(-rows // block_rows), -(-cols // 128))
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+        out = empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
     else:
         _need_out(out, "out", torch.float8_e4m3fn, dev, (rows, cols))
     if out_scale is None:
-        out_scale = torch.empty(shape, dtype=torch.float32, device=dev)
+        out_scale = empty(shape, dtype=torch.float32, device=dev)
     else:
         _need_out(out_scale, "out_scale", torch.float32, dev, shape)
     rc = library().lmhead_quantize_fp8(x.data_ptr(), rows, cols, ld, block_rows, out.data_ptr(),
@@ -631,8 +661,9 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_log
     _need_out(hidden_scale, "hidden_scale", f32, dev, (T, kb))
     _need_out(weight_scale, "weight_scale", f32, dev, (-(-V // 128), kb))
     st = _launch_stream(hidden_q, "hidden_q", stream)
+    empty = _empty_on(stream)
     if out_logits is None:
-        out_logits = torch.empty((T, V), dtype=torch.bfloat16, device=dev)
+        out_logits = empty((T, V), dtype=torch.bfloat16, device=dev)
         ld = V
     else:
         ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev, (T, V))
@@ -679,14 +710,15 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
     if not 0 <= k <= 0x7fffffff:
         raise ValueError("top_k must be in [0, 2^31)")
     st = _launch_stream(logits, "logits", stream)
+    empty = _empty_on(stream)
     if out_token is None:
-        out_token = torch.empty((T,), dtype=i32, device=dev)
+        out_token = empty((T,), dtype=i32, device=dev)
     else:
         _need_out(out_token, "out_token", i32, dev, (T,))
     if out_logprob is not None:
         _need_out(out_logprob, "out_logprob", f32, dev, (T,))
     elif want_logprob:
-        out_logprob = torch.empty((T,), dtype=f32, device=dev)
+        out_logprob = empty((T,), dtype=f32, device=dev)
     rc = library().lmhead_sample(logits.data_ptr(), T, V, ld, t, row_t, k, row_k, p, row_p, m,
                                  row_m, uniform.data_ptr(), out_token.data_ptr(),
                                  _ptr(out_logprob), st)
@@ -814,8 +846,9 @@ def lmhead_engine_gemm(A, B, out=None, a_kmajor: bool = True, b_kmajor: bool = T
     N = B.shape[0] if b_kmajor else B.shape[1]
     layout = (0 if a_kmajor else 1) | (0 if b_kmajor else 2)
     st = _launch_stream(A, "A", stream)
+    empty = _empty_on(stream)
     if out is None:
-        out = torch.empty(M, N, dtype=torch.float32, device=dev)
+        out = empty(M, N, dtype=torch.float32, device=dev)
     rc = library().lmhead_engine_gemm(_ptr(A), _ptr(B), M, N, K, layout, _ptr(out), st)
     _check("lmhead_engine_gemm", rc)
     return out
