@@ -402,9 +402,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kFMaxStages + s); };
   auto tfull_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kFMaxStages + a); };
   auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2 * kFMaxStages + kFMaxAccs + a); };
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kFMaxStages + 2 * kFMaxAccs);
+  const uint32_t final_bar = bar0 + 8u * (2 * kFMaxStages + 2 * kFMaxAccs);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kFMaxStages + 2 * kFMaxAccs + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * kFMaxStages + 2 * kFMaxAccs) + 16 <= kFBarBytes, "barrier area");
+  static_assert(8 * (2 * kFMaxStages + 2 * kFMaxAccs + 1) + 8 <= kFBarBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -426,6 +427,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
       mbar_init(tfull_bar(a), 1);
       mbar_init(tempty_bar(a), kFPromoteWarps);
     }
+    mbar_init(final_bar, 1);
     *abort_flag = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
@@ -466,13 +468,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
       }
-      if (!ok) {
-        // wait for the copies still in flight, so that none lands after the CTA exits
-        volatile int no_abort = 0;
-        for (long long i = issued > n_st ? issued - n_st : 0; i < issued; ++i)
-          mbar_wait(full_bar(static_cast<uint32_t>(i % n_st)),
-                    static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
-      }
+      // Wait (bounded) for the copies still in flight, so that none lands after the
+      // CTA exits: in every case, as another role may give up after the last was issued.
+      volatile int no_abort = 0;
+      for (long long i = issued > n_st ? issued - n_st : 0; i < issued; ++i)
+        mbar_wait(full_bar(static_cast<uint32_t>(i % n_st)),
+                  static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
     }
     if (warp == 1 && lane == 0) {
       const uint32_t idesc = idesc_e4m3_f32(kFM, static_cast<uint32_t>(p.tile_n));
@@ -503,6 +504,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
           }
         }
       }
+      // Every MMA of this thread ends before TMEM is released, also where a role gave up.
+      volatile int no_abort = 0;
+      tc_commit(final_bar);
+      mbar_wait(final_bar, 0, &no_abort, p.status);
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFRegsMany));
