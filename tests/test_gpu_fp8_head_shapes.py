@@ -111,3 +111,103 @@ def test_sample_windows_at_every_split(T):
         tk, l2 = lmh.lmhead_sample(lg[i:i + 1], to_dev(u[i:i + 1]), float(t[i]), top_k=int(k[i]),
                                    top_p=float(p[i]), min_p=float(m[i]))
         assert tk.item() == tok[i] and l2.item() == lp[i], i
+
+
+@pytest.mark.parametrize("V", [152064, 152061])
+def test_offsets_past_2_31(V):
+    # 2.2e9 logits, written by TMA and (odd rows) by the warps, then sampled
+    import torch
+
+    T = 14300
+    h, hs, w, ws = operands(T, 16, V)
+    lg = lmh.lmhead_logits_fp8(h, hs, w, ws)
+    u = torch.rand(T, device=dev(), generator=torch.Generator(device=dev()).manual_seed(5))
+    tok, lp = lmh.lmhead_sample(lg, u, 0.8, top_p=0.9)
+    for a, b in [(0, 3), (14120, 14126), (T - 4, T)]:  # 2^31 / V is 14122.3
+        part = lmh.lmhead_logits_fp8(h[a:b], hs[a:b], w, ws)
+        check_logits(part, h[a:b], hs[a:b], w, ws)
+        assert same_bits(part, lg[a:b]), (a, b)
+        tk, l2 = lmh.lmhead_sample(part, u[a:b], 0.8, top_p=0.9)
+        assert torch.equal(tk, tok[a:b]) and torch.equal(l2, lp[a:b]), (a, b)
+    lmh.lmhead_device_status()
+
+
+@pytest.mark.parametrize("block_rows", [1, 128])
+def test_quantize_offsets_past_2_31(block_rows):
+    import torch
+
+    g = torch.Generator(device=dev()).manual_seed(6)
+    x = torch.randn(1024, 131072, device=dev(), generator=g).to(torch.bfloat16).repeat(17, 1)
+    q, s = lmh.lmhead_quantize_fp8(x, block_rows)
+    one, one_s = lmh.lmhead_quantize_fp8(x[:1024], block_rows)
+    per = one_s.shape[0]
+    for i in range(17):
+        assert torch.equal(q[1024 * i:1024 * (i + 1)].view(torch.uint8), one.view(torch.uint8)), i
+        assert torch.equal(s[per * i:per * (i + 1)], one_s), i
+
+
+@pytest.mark.parametrize("V", [2 ** 19, 2 ** 19 + 1, 1000003])
+def test_sample_large_vocabularies(V):
+    # above 2^19 tokens a weight's unit grows with V
+    x, g = logit_rows(V % 97, 6, V)
+    u = g.random(6, dtype=np.float32)
+    check_sample(x, u)
+    check_sample(x, u, t=0.7, k=5000, p=0.95)
+    check_sample(x, u, t=1.5, p=0.99, m=1e-4)
+    # equal logits: the sums are exact, so the token is
+    tok, _ = lmh.lmhead_sample(_flat(6, V), to_dev(u))
+    assert tok.tolist() == [int(np.floor(np.float64(v) * V)) for v in u]
+
+
+def _flat(T, V):
+    import torch
+
+    return torch.full((T, V), -3.0, dtype=torch.bfloat16, device=dev())
+
+
+def test_empty_batches():
+    import torch
+
+    from invariant_lm_head_gb300.fp8_head import FP8Head
+
+    for V in (1000, 1003):
+        w = torch.randn(V, 256, device=dev()).to(torch.bfloat16)
+        head, h, u = FP8Head(w), w[:0], torch.empty(0, device=dev())
+        n = lmh.lmhead_kernel_launches()
+        assert head.logits(h).shape == (0, V)
+        tok, lp = head.sample(h, u, u.clone(), top_k=torch.empty(0, dtype=torch.int32, device=dev()))
+        assert tok.shape == (0,) and lp.shape == (0,) and lmh.lmhead_kernel_launches() == n
+
+
+def test_capture_of_a_split_not_launched_before():
+    # a process whose only eager call was one row captures every other split
+    import os
+    import subprocess
+    import sys
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import torch, invariant_lm_head_gb300 as lmh
+from invariant_lm_head_gb300.fp8_head import FP8Head
+g = torch.Generator(device="cuda").manual_seed(1)
+head = FP8Head(torch.randn(2003, 256, device="cuda", generator=g).to(torch.bfloat16))
+h = torch.randn(400, 256, device="cuda", generator=g).to(torch.bfloat16)
+u = torch.rand(400, device="cuda", generator=g)
+head.sample(h[:1], u[:1])
+torch.cuda.synchronize()
+got = []
+for T in (30, 60, 120, 200, 400):
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = head.sample(h[:T], u[:T], 0.9, top_p=0.9)
+    graph.replay()
+    torch.cuda.synchronize()
+    got.append((graph, T, out))
+for graph, T, out in got:
+    want = head.sample(h[:T], u[:T], 0.9, top_p=0.9)
+    assert all(torch.equal(a, b) for a, b in zip(out, want)), T
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=root)
+    assert r.returncode == 0 and "ok" in r.stdout, r.stderr[-2000:]
