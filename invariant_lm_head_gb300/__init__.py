@@ -136,47 +136,38 @@ def _stream_ptr(stream) -> Optional[int]:
     return _torch().cuda.current_stream().cuda_stream
 
 
-def _launch_stream(t, name: str, stream) -> int:
-    """The handle of the stream that a call on t's device runs on (None: the current one).
+def _launch_on(t, name: str, stream):
+    """(handle, empty) of the stream that a call on t's device runs on (None: the current one).
 
     A kernel runs on the current device. Addresses of the host or of another device
     must never reach it, nor work be put on another device's stream. Every other
-    tensor of a call is on t's device.
+    tensor of a call is on t's device. empty is torch.empty for what the call writes.
     """
-    if not t.is_cuda:
+    device = t.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be on a CUDA device, got {t.device}")
     torch = _torch()
     current = torch.cuda.current_device()
-    if t.device.index != current:
+    if device != current:
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
     if stream is None:
         # the handle without a Stream object around it (0.2 us instead of 2.8, of a
         # short call's ten)
-        return torch._C._cuda_getCurrentRawStream(current)
+        return torch._C._cuda_getCurrentRawStream(current), torch.empty
     if stream.device.index != current:
         raise ValueError(f"stream is on {stream.device}, but the current device is cuda:{current}")
-    return stream.cuda_stream
-
-
-def _empty_on(stream):
-    """torch.empty for what a call on this stream writes.
-
-    On a stream other than the current one the memory is that stream's: the current
-    stream's may still be in use by work ahead of the call, and a workspace would go
-    back to it, free to be written, while the call runs. What the current stream does
-    with an output before it is dropped is waited for as well.
-    """
-    torch = _torch()
-    if stream is None:
-        return torch.empty
 
     def empty(*size, **options):
+        # The memory is the call's stream's: the current stream's may still be in use by
+        # work ahead of the call, and a workspace would go back to it, free to be written,
+        # while the call runs. What the current stream does with an output before it is
+        # dropped is waited for as well.
         with torch.cuda.stream(stream):
             t = torch.empty(*size, **options)
         t.record_stream(torch.cuda.current_stream())
         return t
 
-    return empty
+    return stream.cuda_stream, empty
 
 
 def _ptr(t) -> Optional[int]:
@@ -257,8 +248,7 @@ def lmhead_logprob_fwd_host(hidden_host, weight_host, labels_host, inv_temperatu
     for t, n in ((out_logprob_host, "out_logprob_host"), (out_entropy_host, "out_entropy_host")):
         if t is not None:
             _need(t, n, torch.float32, cpu, 1)
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     if out_logprob is None:
         out_logprob = empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and (want_entropy or out_entropy_host is not None):
@@ -287,8 +277,7 @@ def _fwd(name, hidden, weight, labels, inv_temperature, out_logprob, out_entropy
     V = weight.shape[0]
     if weight.shape[1] != H or labels.shape[0] != T:
         raise ValueError("shape mismatch between hidden, weight and labels")
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     if out_logprob is None:
         out_logprob = empty(T, dtype=torch.float32, device=dev)
     if out_entropy is None and want_entropy:
@@ -319,8 +308,7 @@ def lmhead_logprob_bwd(hidden, weight, labels, grad_logprob, inv_temperature: fl
     _need(grad_logprob, "grad_logprob", torch.float32, dev, 1)
     if lse is not None:
         _need(lse, "lse", torch.float32, dev, 1)
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -348,8 +336,7 @@ def lmhead_logprob_entropy_bwd(hidden, weight, labels, grad_logprob, grad_entrop
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -386,8 +373,7 @@ def lmhead_logprob_bwd_chunked(hidden, weight, labels, grad_logprob, inv_tempera
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight.shape[0]
     if grad_hidden is None:
@@ -423,8 +409,7 @@ def lmhead_logprob_bwd_shard(hidden, weight_shard, labels, grad_logprob, lse, v_
                  (entropy, "entropy")):
         if t is not None:
             _need(t, n, torch.float32, dev, 1)
-    st = _launch_stream(hidden, "hidden", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden, "hidden", stream)
     T, H = hidden.shape
     V = weight_shard.shape[0]
     if grad_hidden_part is None:
@@ -448,8 +433,7 @@ def lmhead_sum_ranks_bf16(parts, *, out=None, stream=None):
         raise TypeError("parts must be a float32 tensor")
     if parts.device != dev or not parts.is_contiguous() or parts.dim() < 2:
         raise ValueError("parts must be a contiguous tensor [n, ...]")
-    st = _launch_stream(parts, "parts", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(parts, "parts", stream)
     n = parts.shape[0]
     count = parts[0].numel()
     if out is None:
@@ -507,8 +491,7 @@ def _logits(name, logits, labels, inv_temperature, out_logprob, out_entropy, out
     dev = logits.device
     _need(logits, "logits", torch.bfloat16, dev, 2)
     _need(labels, "labels", torch.int32, dev, 1)
-    st = _launch_stream(logits, "logits", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(logits, "logits", stream)
     T, V = logits.shape
     if out_logprob is None:
         out_logprob = empty(T, dtype=torch.float32, device=dev)
@@ -550,7 +533,7 @@ def lmhead_logprob_fwd_partials(hidden, weight_shard, labels, v_offset: int,
         if tuple(t.shape) != (n, T):
             raise ValueError(f"{nm} must be [{n}, {T}]")
     _need(label_logit, "label_logit", torch.float32, dev, 1)
-    st = _launch_stream(hidden, "hidden", stream)
+    st, _ = _launch_on(hidden, "hidden", stream)
     rc = library().lmhead_logprob_fwd_partials(
         _ptr(hidden), _ptr(weight_shard), _ptr(labels), T, H, V, int(v_offset),
         float(inv_temperature), _ptr(part_m), _ptr(part_s), _ptr(part_u), _ptr(label_logit), st)
@@ -562,8 +545,7 @@ def lmhead_logprob_merge(part_m, part_s, part_u, label_logit, labels, V: int, *,
     """Merge whole-vocabulary planes into (logprob, entropy, lse), f32 [T]."""
     torch = _torch()
     dev = labels.device
-    st = _launch_stream(labels, "labels", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(labels, "labels", stream)
     T = labels.shape[0]
     out_logprob = empty(T, device=dev) if out_logprob is None else out_logprob
     out_entropy = empty(T, device=dev) if out_entropy is None else out_entropy
@@ -622,8 +604,7 @@ def lmhead_quantize_fp8(x, block_rows: int = 1, *, out=None, out_scale=None, str
     rows, cols = x.shape
     if block_rows != 1 and block_rows != 128:
         raise ValueError("block_rows must be 1 or 128")
-    st = _launch_stream(x, "x", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(x, "x", stream)
     shape = (-(-rows // block_rows), -(-cols // 128))
     if out is None:
         out = empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
@@ -660,8 +641,7 @@ def lmhead_logits_fp8(hidden_q, hidden_scale, weight_q, weight_scale, *, out_log
     kb = -(-H // 128)
     _need_out(hidden_scale, "hidden_scale", f32, dev, (T, kb))
     _need_out(weight_scale, "weight_scale", f32, dev, (-(-V // 128), kb))
-    st = _launch_stream(hidden_q, "hidden_q", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(hidden_q, "hidden_q", stream)
     if out_logits is None:
         out_logits = empty((T, V), dtype=torch.bfloat16, device=dev)
         ld = V
@@ -709,8 +689,7 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
     k = int(k)
     if not 0 <= k <= 0x7fffffff:
         raise ValueError("top_k must be in [0, 2^31)")
-    st = _launch_stream(logits, "logits", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(logits, "logits", stream)
     if out_token is None:
         out_token = empty((T,), dtype=i32, device=dev)
     else:
@@ -845,8 +824,7 @@ def lmhead_engine_gemm(A, B, out=None, a_kmajor: bool = True, b_kmajor: bool = T
     M, K = A.shape if a_kmajor else (A.shape[1], A.shape[0])
     N = B.shape[0] if b_kmajor else B.shape[1]
     layout = (0 if a_kmajor else 1) | (0 if b_kmajor else 2)
-    st = _launch_stream(A, "A", stream)
-    empty = _empty_on(stream)
+    st, empty = _launch_on(A, "A", stream)
     if out is None:
         out = empty(M, N, dtype=torch.float32, device=dev)
     rc = library().lmhead_engine_gemm(_ptr(A), _ptr(B), M, N, K, layout, _ptr(out), st)
