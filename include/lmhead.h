@@ -460,7 +460,8 @@ int lmhead_quantize_fp8(const uint16_t* x, int64_t rows, int64_t cols, int64_t l
  *   weight_q      e4m3 [V, H], 16-byte aligned
  *   weight_scale  f32 [ceil(V / 128), ceil(H / 128)]
  *   logits        bf16 [T, V], rows ld_logits elements apart (ld_logits >= V),
- *                 2-byte aligned; 16-byte aligned rows are written faster
+ *                 2-byte aligned; 16-byte aligned rows are written faster.
+ *                 Nothing between or after the rows is written
  * T == 0 is a no-op.
  */
 int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_scale, const uint8_t* weight_q,
@@ -478,7 +479,9 @@ int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_scale, const 
  * mass. temperature 0 returns the likeliest token (the lowest index of equal
  * ones) and ignores the rest. out_logprob is the token's log-prob in the whole
  * distribution at that temperature (at 1 for temperature 0), before any cut:
- * the sampler formula's value, as logprob_from_logits_div gives it.
+ * the sampler formula's value, from the sampler's own sums. logprob_from_logits_div
+ * sums in another order and agrees within rounding (1e-5), not bit for bit; a
+ * caller that compares bits takes both sides from that entry point.
  *   logits   bf16 [T, V], rows ld_logits elements apart, 2-byte aligned; T up
  *            to LMH_MAX_DIM / 8
  *   temperature, top_k, top_p, min_p  for every row, in [0, inf), [0, ..),
@@ -494,9 +497,12 @@ int lmhead_logits_fp8(const uint8_t* hidden_q, const float* hidden_scale, const 
  * NaN and -inf logits are never drawn; a row of nothing else gets token -1 and
  * log-prob 0 (what the log-prob entry points give for a label outside the
  * vocabulary). Logits equal to the largest weigh 1 even where z overflows.
- * Weights are held in units of 2^-44 of the largest (V <= 2^19; 2^-(63 -
- * ceil(log2 V)) above) and summed as integers, so neither the order of sums
- * nor the batch can change a token. T == 0 is a no-op.
+ * A weight is an fp32 exponential (relative error below 2^-21), held in units of
+ * 2^-44 of the largest (V <= 2^19; 2^-(63 - ceil(log2 V)) above). The units are
+ * summed as integers, so neither the order of sums nor the batch can change a
+ * token; but a cut, or a uniform number, nearer to a border between two tokens
+ * than the weights' own error may fall on the other side than in exact
+ * arithmetic. T == 0 is a no-op.
  */
 int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logits,
                   float temperature, const float* row_temperature, int32_t top_k,

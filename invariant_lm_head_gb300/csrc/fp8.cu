@@ -278,7 +278,7 @@ __device__ __forceinline__ void st_global_u16_if(uint16_t* at, uint16_t v, bool 
 // 16-byte chunks are the row's aligned ones; sixteen rows at a time go through 4 KB of
 // shared memory, and half a warp writes a row: a chunk a lane, and the first chunk,
 // which holds the row's two ends, element by element. T=200 H=3600 V=32003 takes 43.3
-// us with it (V=32000, by TMA, 40.5); in boxes of 32 columns, as the 4-byte words that
+// us with it (V=32000, by TMA, 40.3); in boxes of 32 columns, as the 4-byte words that
 // they straddle, 53.1: those are 17 writes of parts of a 32-byte sector for 224 bytes.
 template <int kWords>
 __device__ __forceinline__ void store_rows(uint32_t buf, int lane, uint32_t (&w)[kWords],
@@ -373,13 +373,13 @@ __device__ __forceinline__ void fp8_unit(const Fp8Params& p, int u, int& m, int&
 // whatever the stage holds next (its own vocabulary rows), which only feeds
 // lanes that no one reads.
 //
-// What bounds it. A short batch reads the weight once and is bound by that: 82.6
-// us at T=1 H=3584 V=152064, 6.6 TB/s; 26.4 us at T=64 H=4096 V=32000, 5.1 TB/s
+// What bounds it. A short batch reads the weight once and is bound by that: 82-84
+// us at T=1 H=3584 V=152064, 6.6 TB/s; 26.0 us at T=64 H=4096 V=32000, 5.2 TB/s
 // (one wave: its start and end show). A long one is bound by the promote groups:
 // a K block's 128 x 256 accumulator is read out of TMEM beside the MMAs, which
 // use TMEM as well (about 500 cycles, against 190 with no MMA running), scaled,
-// added and handed back, about 1100 cycles in all for 512 of MMAs. 999 us at
-// T=2048 H=3584 V=152064, 2.24 PFLOP/s (the same loop with one hand-over a tile
+// added and handed back, about 1100 cycles in all for 512 of MMAs. 982-999 us at
+// T=2048 H=3584 V=152064, 2.24-2.27 PFLOP/s (the same loop with one hand-over a tile
 // runs at 3.15, but sums unscaled blocks).
 // Tried and slower at T=2048 H=3584 V=38912 (253 us): CTA pairs sharing 256 x 256
 // tiles (276 us: half the weight traffic, but the hand-over crosses two CTAs);
@@ -666,7 +666,7 @@ cudaError_t fp8_setup() {
 
 // Columns of a tile when `sms` CTAs share the vocabulary m_tiles times over: as
 // few waves as 256-column tiles need, each tile just wide enough to fill them (one
-// 64-row tile of H=4096 V=32000, one wave of 152: 224 columns on 143 CTAs 26.6 us,
+// 64-row tile of H=4096 V=32000, one wave of 152: 224 columns on 143 CTAs 26.0 us,
 // 128 columns in two waves 32.1 us).
 int fp8_tile_n(int64_t V, int64_t m_tiles, int sms) {
   const int64_t units = m_tiles * ((V + kFMaxN - 1) / kFMaxN);

@@ -6,10 +6,12 @@
 // index. So a row is read once into a histogram of counts over the ordered
 // values (shared memory, integer adds), and all later work is on the
 // histogram: with m the largest z = x / t (fp32 division), a bin's weight is
-// exp(z - m), held as an integer in units of 2^-44, and its mass is count *
-// weight. Sums of integers are exact and have no order, so the result is the
-// same whatever adds first. Tokens are taken in descending logit, ties by
-// index:
+// exp(z - m) in fp32 (24 bits: expf's 2 units in the last place, one rounding, and
+// what the subtraction lost put back), cut to units of 2^-44, and its mass is
+// count * weight. Sums of these integers are exact and have no order, so the
+// result is the same whatever adds first; against exact weights a border between
+// two tokens is off by their relative error, below 2^-21. Tokens are taken in
+// descending logit, ties by index:
 //   top-k   the first k;
 //   top-p   the shortest prefix of those whose mass reaches p of their mass;
 //   min-p   those of weight >= min_p;
@@ -31,7 +33,9 @@
 // SM's shared memory, 32 random bins meeting 3.7 deep on a bank (four rows counting
 // at once take 83000 cycles, 0.85 of that pipe), and weighing, the shuffles and the
 // index search share it. Staggering the four rows of an SM, so that some weigh while
-// others count, gains nothing (1024 rows 153-158 us).
+// others count, gains nothing (1024 rows 153-158 us). The two shapes that share an
+// SM have 64 registers and spill (-Xptxas -v: <1, 512, 2> 96 bytes stored and 108
+// loaded, <1, 256, 4> 112 and 116); the others take 100 and do not.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
