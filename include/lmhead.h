@@ -510,6 +510,111 @@ int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logit
                   const float* row_min_p, const float* uniform, int32_t* out_token,
                   float* out_logprob, struct CUstream_st* stream);
 
+/* ------------------------------------------- around the quantised heads
+ *
+ * The steps of a server next to the fp8 head's: the norm before it, a 4-bit form of the
+ * head, and what is reported beside a token. Serving operators without a backward;
+ * a row's results do not depend, bit for bit, on the batch it arrives in.
+ */
+
+/*
+ * The last RMS norm before the head, with the residual's addition and an output that
+ * lmhead_logits_fp8 takes. For each row, with n = cols:
+ *   h = x + residual, rounded to bf16 (h = x without a residual)
+ *   y = h * weight / sqrt(sum h^2 / n + eps)
+ * and for each block of 128 columns (the last one is shorter), with
+ * a = max(max |y|, 2^-60):
+ *   scale = a / 448,   q = y * 448 / a, rounded to e4m3 once (nearest, ties to even)
+ * h is not rounded again and y not at all: a block of ordinary size has the q that exact
+ * arithmetic gives, and its scale 24 bits. A row that holds an infinity or a NaN has
+ * the values that the formula gives in fp32 (a block with a NaN gets it as its scale and
+ * NaN in every q).
+ *   x             bf16 [rows, cols], 16-byte aligned, rows ld_x apart (>= cols, a
+ *                 multiple of 8); cols % 16 == 0, at most 32768
+ *   residual      the same with ld_residual, or NULL
+ *   weight        bf16 [cols], 16-byte aligned
+ *   eps           finite, > 0
+ *   out_residual  receives h (rows ld_out_residual apart; may be residual or x itself,
+ *                 at the same distance), or NULL; only with a residual
+ *   q             e4m3 [rows, cols], contiguous, 16-byte aligned
+ *   scale         f32 [rows, ceil(cols / 128)]
+ * rows == 0 is a no-op.
+ */
+int lmhead_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16_t* weight,
+                       int64_t rows, int64_t cols, int64_t ld_x, int64_t ld_residual, float eps,
+                       uint16_t* out_residual, int64_t ld_out_residual, uint8_t* q, float* scale,
+                       struct CUstream_st* stream);
+
+/*
+ * Microscaled 4-bit floating point: 32 consecutive elements of a row share a power of
+ * two 2^(b - 127), held as the byte b, and an element is e2m1 (sign, two exponent bits,
+ * one fraction bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6). For each block with largest magnitude a:
+ *   b     the exponent that leaves a / 2^(b - 127) in [3.5, 7), at least 0; 255 (NaN)
+ *         where the block holds an infinity or a NaN
+ *   q     x / 2^(b - 127), rounded to e2m1 once (nearest, ties to even; at most 6)
+ * lmhead_dequantize_mxfp4 gives q * 2^(b - 127) in bf16, exactly (NaN for b = 255;
+ * past bf16's largest value an infinity).
+ *   x, out  bf16 [rows, cols], 16-byte aligned, rows ld elements apart (ld >= cols,
+ *           ld % 8 == 0); cols % 32 == 0
+ *   q       [rows, cols / 2] bytes, two elements each, the first in the low four bits;
+ *           contiguous, 16-byte aligned
+ *   scale   [ceil(rows / 128), ceil(cols / 128), 32, 16] bytes, 16-byte aligned: the byte
+ *           of (row, block) is at [row / 128][block / 4][row % 32][row / 32 % 4 * 4 +
+ *           block % 4] (the order in which the tensor cores read scales). The quantiser
+ *           writes 127 (the scale 1) in places past the rows and columns
+ * rows == 0 is a no-op.
+ */
+int lmhead_quantize_mxfp4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,
+                          uint8_t* scale, struct CUstream_st* stream);
+int lmhead_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t rows, int64_t cols,
+                            uint16_t* out, int64_t ld_out, struct CUstream_st* stream);
+
+/*
+ * bf16 logits of a 4-bit head, logits[t, v] = sum_h hidden[t, h] * weight[v, h] over the
+ * values that the two operands stand for: products and scales in the tensor cores, fp32
+ * sums over all of H, rounded to bf16 once.
+ *   hidden_q, hidden_scale  as lmhead_quantize_mxfp4 writes them for [T, H]
+ *   weight_q, weight_scale  the same for [V, H]; H % 32 == 0
+ *   logits        bf16 [T, V], rows ld_logits elements apart (ld_logits >= V),
+ *                 2-byte aligned; 16-byte aligned rows are written faster.
+ *                 Nothing between or after the rows is written
+ * T == 0 is a no-op.
+ */
+int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidden_scale,
+                        const uint8_t* weight_q, const uint8_t* weight_scale, int64_t T, int64_t H,
+                        int64_t V, uint16_t* logits, int64_t ld_logits,
+                        struct CUstream_st* stream);
+
+/*
+ * What a server reports of bf16 logits x: log-probs of given tokens, the entropy, and the
+ * likeliest alternatives. With z = x / temperature (0 counts as 1, as for the log-prob of
+ * lmhead_sample) and p = softmax(z):
+ *   out_logprob[t, i]      log p[tokens[t, i]]; 0 for a token outside [0, V)
+ *   out_entropy[t]         -sum p log p
+ *   out_top_token[t, j]    the j-th token in descending order of x, equal ones by index
+ *   out_top_logprob[t, j]  its log p
+ * One read of the logits, fp32 sums in an order fixed by V: agrees with
+ * logprob_from_logits_div within rounding (1e-5), not bit for bit.
+ * NaN and -inf logits are masked: they weigh nothing (in the entropy either), have
+ * log-prob -inf and are never listed; where fewer than n_top tokens are left the rest of
+ * the list is token -1, log-prob -inf. A row with nothing left has entropy 0 and -inf
+ * for every token of the vocabulary. Logits equal to the largest weigh the same even
+ * where z overflows.
+ *   logits       bf16 [T, V], rows ld_logits elements apart, 2-byte aligned (rows that
+ *                start on 16 bytes are read faster); T up to LMH_MAX_DIM / 8
+ *   temperature  finite, >= 0, or row_temperature f32 [T] on the device (NULL: none): a
+ *                row whose temperature is negative or not finite gets token -1 and NaN
+ *   tokens       int32 [T, n_tokens], n_tokens >= 0
+ *   n_top        0 to 128; it may exceed V
+ *   out_entropy  f32 [T] or NULL
+ * T == 0 is a no-op.
+ */
+int lmhead_top_logprobs(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logits,
+                        float temperature, const float* row_temperature, const int32_t* tokens,
+                        int64_t n_tokens, int64_t n_top, float* out_logprob, float* out_entropy,
+                        int32_t* out_top_token, float* out_top_logprob,
+                        struct CUstream_st* stream);
+
 /* ---------------------------------------------------------------- diagnostics */
 
 /* Message of the calling thread's last error ("" if none). */

@@ -83,6 +83,13 @@ SIGNATURES = {
     "lmhead_logits_fp8": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
     "lmhead_sample": ([_P, _I64, _I64, _I64, _F, _P, ctypes.c_int32, _P, _F, _P, _F, _P, _P, _P, _P,
                        _P], ctypes.c_int),
+    "lmhead_rmsnorm_fp8": ([_P, _P, _P, _I64, _I64, _I64, _I64, _F, _P, _I64, _P, _P, _P],
+                           ctypes.c_int),
+    "lmhead_quantize_mxfp4": ([_P, _I64, _I64, _I64, _P, _P, _P], ctypes.c_int),
+    "lmhead_dequantize_mxfp4": ([_P, _P, _I64, _I64, _P, _I64, _P], ctypes.c_int),
+    "lmhead_logits_mxfp4": ([_P, _P, _P, _P, _I64, _I64, _I64, _P, _I64, _P], ctypes.c_int),
+    "lmhead_top_logprobs": ([_P, _I64, _I64, _I64, _F, _P, _P, _I64, _I64, _P, _P, _P, _P, _P],
+                            ctypes.c_int),
 }
 
 _lib_handle: Optional[ctypes.CDLL] = None
@@ -704,6 +711,188 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
     if rc:
         _check("lmhead_sample", rc)
     return out_token, out_logprob
+
+
+def lmhead_rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None, out_scale=None,
+                       out_residual=None, stream=None):
+    """RMS norm of x (+ residual), block-quantised to e4m3 (see include/lmhead.h).
+
+    x and residual bf16 [rows, cols] (rows may be strided), weight bf16 [cols].
+    Returns (q float8_e4m3fn [rows, cols], scale f32 [rows, ceil(cols / 128)], the
+    bf16 sum x + residual or None), q and scale as lmhead_logits_fp8 takes them.
+    out_residual may be residual or x itself.
+    """
+    torch = _torch()
+    dev = x.device
+    bf16 = torch.bfloat16
+    ld = _need_rows(x, "x", bf16, dev)
+    rows, cols = x.shape
+    _need_out(weight, "weight", bf16, dev, (cols,))
+    ld_res = ld_out = 0
+    if residual is not None:
+        ld_res = _need_rows(residual, "residual", bf16, dev, (rows, cols))
+    elif out_residual is not None:
+        raise ValueError("out_residual needs a residual")
+    if out is not None:
+        _need_out(out, "out", torch.float8_e4m3fn, dev, (rows, cols))
+    kb = -(-cols // 128)
+    if out_scale is not None:
+        _need_out(out_scale, "out_scale", torch.float32, dev, (rows, kb))
+    if out_residual is not None:
+        ld_out = _need_rows(out_residual, "out_residual", bf16, dev, (rows, cols))
+    st, empty = _launch_on(x, "x", stream)
+    if out is None:
+        out = empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    if out_scale is None:
+        out_scale = empty((rows, kb), dtype=torch.float32, device=dev)
+    if residual is not None and out_residual is None:
+        out_residual = empty((rows, cols), dtype=bf16, device=dev)
+        ld_out = cols
+    rc = library().lmhead_rmsnorm_fp8(x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, cols,
+                                      ld, ld_res, eps, _ptr(out_residual), ld_out, out.data_ptr(),
+                                      out_scale.data_ptr(), st)
+    if rc:
+        _check("lmhead_rmsnorm_fp8", rc)
+    return out, out_scale, out_residual
+
+
+def _mxfp4_scale_shape(rows: int, cols: int):
+    return (-(-rows // 128), -(-cols // 128), 32, 16)
+
+
+def lmhead_quantize_mxfp4(x, *, out=None, out_scale=None, stream=None):
+    """Microscaled 4-bit quantisation of a bf16 matrix (see include/lmhead.h).
+
+    x bf16 [rows, cols] (rows may be strided), cols a multiple of 32. Returns (q
+    uint8 [rows, cols / 2], two e2m1 elements a byte, scale uint8 [ceil(rows / 128),
+    ceil(cols / 128), 32, 16]).
+    """
+    torch = _torch()
+    dev = x.device
+    ld = _need_rows(x, "x", torch.bfloat16, dev)
+    rows, cols = x.shape
+    shape = _mxfp4_scale_shape(rows, cols)
+    if out is not None:
+        _need_out(out, "out", torch.uint8, dev, (rows, cols // 2))
+    if out_scale is not None:
+        _need_out(out_scale, "out_scale", torch.uint8, dev, shape)
+    st, empty = _launch_on(x, "x", stream)
+    if out is None:
+        out = empty((rows, cols // 2), dtype=torch.uint8, device=dev)
+    if out_scale is None:
+        out_scale = empty(shape, dtype=torch.uint8, device=dev)
+    rc = library().lmhead_quantize_mxfp4(x.data_ptr(), rows, cols, ld, out.data_ptr(),
+                                         out_scale.data_ptr(), st)
+    if rc:
+        _check("lmhead_quantize_mxfp4", rc)
+    return out, out_scale
+
+
+def lmhead_dequantize_mxfp4(q, scale, *, out=None, stream=None):
+    """The bf16 values [rows, cols] that lmhead_quantize_mxfp4's output stands for."""
+    torch = _torch()
+    dev = q.device
+    _need(q, "q", torch.uint8, dev, 2)
+    rows, cols = q.shape[0], 2 * q.shape[1]
+    _need_out(scale, "scale", torch.uint8, dev, _mxfp4_scale_shape(rows, cols))
+    ld = cols
+    if out is not None:
+        ld = _need_rows(out, "out", torch.bfloat16, dev, (rows, cols))
+    st, empty = _launch_on(q, "q", stream)
+    if out is None:
+        out = empty((rows, cols), dtype=torch.bfloat16, device=dev)
+    rc = library().lmhead_dequantize_mxfp4(q.data_ptr(), scale.data_ptr(), rows, cols,
+                                           out.data_ptr(), ld, st)
+    if rc:
+        _check("lmhead_dequantize_mxfp4", rc)
+    return out
+
+
+def lmhead_logits_mxfp4(hidden_q, hidden_scale, weight_q, weight_scale, *, out_logits=None,
+                        stream=None):
+    """bf16 logits [T, V] of two microscaled 4-bit operands (see include/lmhead.h).
+
+    hidden_q [T, H / 2] with hidden_scale and weight_q [V, H / 2] with weight_scale,
+    as lmhead_quantize_mxfp4 returns them. out_logits may have strided rows.
+    """
+    torch = _torch()
+    dev = hidden_q.device
+    u8 = torch.uint8
+    _need(hidden_q, "hidden_q", u8, dev, 2)
+    _need(weight_q, "weight_q", u8, dev, 2)
+    T, half = hidden_q.shape
+    V = weight_q.shape[0]
+    if weight_q.shape[1] != half:
+        raise ValueError("shape mismatch between hidden_q and weight_q")
+    H = 2 * half
+    _need_out(hidden_scale, "hidden_scale", u8, dev, _mxfp4_scale_shape(T, H))
+    _need_out(weight_scale, "weight_scale", u8, dev, _mxfp4_scale_shape(V, H))
+    if out_logits is not None:
+        ld = _need_rows(out_logits, "out_logits", torch.bfloat16, dev, (T, V))
+    st, empty = _launch_on(hidden_q, "hidden_q", stream)
+    if out_logits is None:
+        out_logits = empty((T, V), dtype=torch.bfloat16, device=dev)
+        ld = V
+    rc = library().lmhead_logits_mxfp4(hidden_q.data_ptr(), hidden_scale.data_ptr(),
+                                       weight_q.data_ptr(), weight_scale.data_ptr(), T, H, V,
+                                       out_logits.data_ptr(), ld, st)
+    if rc:
+        _check("lmhead_logits_mxfp4", rc)
+    return out_logits
+
+
+def lmhead_top_logprobs(logits, tokens=None, temperature=1.0, *, top: int = 20, out_logprob=None,
+                        out_entropy=None, out_top_token=None, out_top_logprob=None,
+                        want_entropy: bool = True, stream=None):
+    """Log-probs of given tokens, the entropy, and the likeliest alternatives.
+
+    logits bf16 [T, V] (rows may be strided), tokens int32 [T] or [T, n] (or None),
+    temperature a number or f32 [T] (0 counts as 1), top the number of alternatives (0
+    to 128). Returns (logprob f32, shaped as tokens, or None; entropy f32 [T] or None;
+    top_token int32 [T, top]; top_logprob f32 [T, top]); see include/lmhead.h for masks.
+    """
+    torch = _torch()
+    dev = logits.device
+    f32, i32 = torch.float32, torch.int32
+    ld = _need_rows(logits, "logits", torch.bfloat16, dev)
+    T, V = logits.shape
+    n_tokens = 0
+    if tokens is not None:
+        if not isinstance(tokens, torch.Tensor) or tokens.dim() not in (1, 2):
+            raise ValueError("tokens must be a 1-D or 2-D tensor")
+        _need(tokens, "tokens", i32, dev, tokens.dim())
+        if tokens.shape[0] != T:
+            raise ValueError("tokens must have one row per row of logits")
+        n_tokens = 1 if tokens.dim() == 1 else tokens.shape[1]
+        if out_logprob is not None:
+            _need_out(out_logprob, "out_logprob", f32, dev, tuple(tokens.shape))
+    elif out_logprob is not None:
+        raise ValueError("out_logprob needs tokens")
+    t, row_t = _setting(temperature, "temperature", f32, dev, T)
+    top = int(top)
+    if not 0 <= top <= 128:
+        raise ValueError("top must be in [0, 128]")
+    if out_entropy is not None:
+        _need_out(out_entropy, "out_entropy", f32, dev, (T,))
+    if out_top_token is not None:
+        _need_out(out_top_token, "out_top_token", i32, dev, (T, top))
+    if out_top_logprob is not None:
+        _need_out(out_top_logprob, "out_top_logprob", f32, dev, (T, top))
+    st, empty = _launch_on(logits, "logits", stream)
+    if tokens is not None and out_logprob is None:
+        out_logprob = empty(tokens.shape, dtype=f32, device=dev)
+    if out_entropy is None and want_entropy:
+        out_entropy = empty((T,), dtype=f32, device=dev)
+    if out_top_token is None:
+        out_top_token = empty((T, top), dtype=i32, device=dev)
+    if out_top_logprob is None:
+        out_top_logprob = empty((T, top), dtype=f32, device=dev)
+    rc = library().lmhead_top_logprobs(logits.data_ptr(), T, V, ld, t, row_t, _ptr(tokens),
+                                       n_tokens, top, _ptr(out_logprob), _ptr(out_entropy),
+                                       out_top_token.data_ptr(), out_top_logprob.data_ptr(), st)
+    if rc:
+        _check("lmhead_top_logprobs", rc)
+    return out_logprob, out_entropy, out_top_token, out_top_logprob
 
 
 _LOGPROB_FN = None

@@ -21,7 +21,8 @@ CSRC = PKG_DIR / "csrc"
 INCLUDE = ROOT / "include"
 BUILD_DIR = ROOT / "_build"
 LIB_PATH = PKG_DIR / "liblmhead.so"
-SOURCES = ["api.cu", "gemm_tc.cu", "rowwise.cu", "noalloc.cu", "fp8.cu", "sample.cu"]
+SOURCES = ["api.cu", "gemm_tc.cu", "rowwise.cu", "noalloc.cu", "fp8.cu", "sample.cu", "norm.cu",
+           "mxfp4.cu", "top.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

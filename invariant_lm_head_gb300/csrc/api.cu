@@ -292,7 +292,8 @@ const char* const kKindNames[lmh::K_COUNT] = {
     "fused_fwd_gemm", "fwd_merge",   "dlogits_gemm",  "grad_hidden_gemm",  "grad_weight_gemm",
     "logits_rowwise", "engine_gemm", "selftest_wait", "logits_rowwise_div",
     "hidden_transpose", "sum_parts_bf16", "grad_hidden_sum",   "quantize_fp8",
-    "logits_fp8_gemm", "sample"};
+    "logits_fp8_gemm", "sample", "rmsnorm_fp8", "quantize_mxfp4", "dequantize_mxfp4",
+    "logits_mxfp4_gemm", "top_logprobs"};
 
 struct TimingRec {
   int kind;

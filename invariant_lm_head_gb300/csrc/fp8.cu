@@ -25,8 +25,10 @@
 
 #include <cuda_bf16.h>
 
+#include "fp8_block.cuh"
 #include "internal.h"
 #include "lmhead.h"
+#include "out_rows.cuh"
 #include "ptx.cuh"
 
 namespace lmh {
@@ -36,58 +38,20 @@ namespace {
 constexpr int kQBlock = 128;  // elements of a scale block along K (and along V)
 
 // ------------------------------------------------------------ quantisation
-// A block's quotient x * 448 / a in parts that stay clear of overflow and
-// underflow: with a = am * 2^e (1 <= am < 2), c = 448 * 2^-e and r = 1 / am
-// rounded to nearest, y = x * c is exact wherever q does not round to zero, and
-// y / am is corrected from y * r by its exact remainder (P. Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor",
-// IBM J. Res. Dev. 34(1), 1990). It is taken from -y and -r: a zero's remainder
-// is +0 either way, and +0 * -r is the zero whose addition keeps the quotient's
-// sign (-0 * 448 / a is -0).
-struct BlockScale {
-  float neg_c, am, neg_r, scale;
-};
-
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits16) {
+__device__ __forceinline__ BlockScale block_scale_of(uint32_t amax_bits16) {
   // amax_bits16: the largest |x| as bf16 bits (the order of magnitudes is the
   // order of their bits; a NaN is above inf)
   const uint32_t bits = amax_bits16 << 16;
-  BlockScale s;
-  if (bits >= 0x7f800000u) {  // inf or NaN in the block: every q becomes NaN
-    s.scale = __uint_as_float(bits);
-    s.neg_c = 0.f;
-    s.am = 1.f;
-    s.neg_r = __uint_as_float(0x7fffffffu);
-    return s;
-  }
-  const float a = fmaxf(__uint_as_float(bits), 0x1p-60f);
-  const uint32_t ab = __float_as_uint(a);
-  const int e = static_cast<int>(ab >> 23) - 127;
-  const float am = __uint_as_float((ab & 0x007fffffu) | 0x3f800000u);
-  s.neg_c = -448.f * __uint_as_float(static_cast<uint32_t>(127 - (e < 127 ? e : 126)) << 23);
-  if (e == 127) s.neg_c *= 0.5f;
-  s.am = am;
-  s.neg_r = -__frcp_rn(am);
-  s.scale = __fdiv_rn(a, 448.f);
-  return s;
+  if (bits >= 0x7f800000u) return block_scale_nan(__uint_as_float(bits));
+  return block_scale(fmaxf(__uint_as_float(bits), 0x1p-60f));
 }
 
 __device__ __forceinline__ uint32_t amax_u16x2(uint32_t m, uint32_t w) {
   return __vmaxu2(m, w & 0x7fff7fffu);
 }
 
-// Two quotients to a pair of e4m3 bytes (low half first).
 __device__ __forceinline__ uint32_t quantize2(uint32_t w, const BlockScale& s) {
-  const f32x2 x = f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-  const f32x2 neg_y = f2_mul(x, f2_pack(s.neg_c, s.neg_c));
-  const f32x2 neg_r = f2_pack(s.neg_r, s.neg_r);
-  const f32x2 q0 = f2_mul(neg_y, neg_r);
-  const f32x2 neg_rem = f2_fma(q0, f2_pack(s.am, s.am), neg_y);
-  float lo, hi;
-  f2_unpack(f2_fma(neg_rem, neg_r, q0), lo, hi);
-  uint16_t out;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out) : "f"(hi), "f"(lo));
-  return out;
+  return quantize2(f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)), s);
 }
 
 __device__ __forceinline__ uint2 quantize8(const uint4& v, const BlockScale& s) {
@@ -139,7 +103,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     m = max(m & 0xffffu, m >> 16);
 #pragma unroll
     for (int off = 4; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const BlockScale s = block_scale(m);
+    const BlockScale s = block_scale_of(m);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int64_t col = blk * kQBlock + h * 64 + sub * 8;
@@ -178,7 +142,7 @@ __global__ void __launch_bounds__(kQuantThreads)
     __syncthreads();  // the other parity's words are free: every thread has read them by now
 #pragma unroll
     for (int w = 0; w < kQuantThreads / 32; ++w) m = max(m, warp_max[parity][w]);
-    const BlockScale s = block_scale(m);
+    const BlockScale s = block_scale_of(m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int64_t row = row0 + 16 * i;
@@ -241,115 +205,6 @@ __device__ __forceinline__ void tc_mma_e4m3(uint32_t d_tmem, uint64_t a_desc, ui
 // 0 in bits 7 and 10), both K-major, [17,23) N >> 3, [24,29) M >> 4.
 __device__ __forceinline__ uint32_t idesc_e4m3_f32(uint32_t M, uint32_t N) {
   return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
-}
-
-__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t addr) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                             uint32_t d) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
-               : "memory");
-}
-// Predicated stores: divergent branches around single stores cost more than they.
-__device__ __forceinline__ void st_global_v4_if(uint16_t* at, uint4 v, bool on) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::
-          "l"(at),
-      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w), "r"(static_cast<int>(on))
-      : "memory");
-}
-__device__ __forceinline__ void st_global_u16_if(uint16_t* at, uint16_t v, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p st.global.b16 [%0], %1;\n\t}" ::"l"(at),
-               "h"(v), "r"(static_cast<int>(on))
-               : "memory");
-}
-
-// A warp's `rows` (of 32) rows of output, one in each lane as kWords pairs of bf16, to
-// rows at any 2-byte address (out + lane * ld), the first n elements of each. A lane
-// turns its row, as a ring, by its address's offset in 16 bytes, so that the ring's
-// 16-byte chunks are the row's aligned ones; sixteen rows at a time go through 4 KB of
-// shared memory, and half a warp writes a row: a chunk a lane, and the first chunk,
-// which holds the row's two ends, element by element. T=200 H=3600 V=32003 takes 43.3
-// us with it (V=32000, by TMA, 40.3); in boxes of 32 columns, as the 4-byte words that
-// they straddle, 53.1: those are 17 writes of parts of a 32-byte sector for 224 bytes.
-template <int kWords>
-__device__ __forceinline__ void store_rows(uint32_t buf, int lane, uint32_t (&w)[kWords],
-                                           uint16_t* out, int64_t ld, int rows, int n) {
-  constexpr int kChunks = kWords / 4;
-  static_assert(kWords % 4 == 0 && kChunks <= 16, "sixteen rows of 256 bytes");
-  {
-    const uint32_t off =
-        static_cast<uint32_t>(reinterpret_cast<uintptr_t>(out + static_cast<int64_t>(lane) * ld)) & 15u;
-    const uint32_t sel = off & 2u ? 0x5432u : 0x7654u;  // by an element
-    const uint32_t last = w[kWords - 1];
-#pragma unroll
-    for (int i = kWords - 1; i > 0; --i) w[i] = __byte_perm(w[i - 1], w[i], sel);
-    w[0] = __byte_perm(last, w[0], sel);
-#pragma unroll
-    for (int by = 1; by <= 2; ++by) {  // by a word, by two
-      const bool turn = off & (by == 1 ? 4u : 8u);
-      uint32_t end[2] = {w[kWords - by], w[kWords - 1]};
-#pragma unroll
-      for (int i = kWords - 1; i >= by; --i) w[i] = turn ? w[i - by] : w[i];
-#pragma unroll
-      for (int i = 0; i < by; ++i) w[i] = turn ? end[i] : w[i];
-    }
-  }
-  const int j = lane & 15;
-#pragma unroll 1
-  for (int first = 0; first < rows; first += 16) {
-    if ((lane & 16) == first) {
-#pragma unroll
-      for (int c = 0; c < kChunks; ++c)
-        st_shared_v4(buf + j * 256 + ((c ^ (j & 7)) << 4), w[4 * c], w[4 * c + 1], w[4 * c + 2],
-                     w[4 * c + 3]);
-    }
-    __syncwarp();
-    uint16_t* o = out + static_cast<int64_t>(first + (lane >> 4)) * ld;
-#pragma unroll 4
-    for (int i = 0; i < 8; ++i, o += 2 * ld) {
-      const int r = 2 * i + (lane >> 4);
-      const bool on = first + r < rows;
-      const int off = static_cast<int>(reinterpret_cast<uintptr_t>(o) & 15) >> 1;  // elements
-      const uint32_t row = buf + r * 256;
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (j < kChunks) v = ld_shared_v4(row + ((j ^ (r & 7)) << 4));
-      const int e = 8 * j - off;  // the chunk's first element
-      st_global_v4_if(o + e, v, on && j < kChunks && e >= 0 && e + 8 <= n);
-      // the first chunk, where it is not whole
-      const uint16_t x = ld_shared_u16(row + ((r & 7) << 4) + 2 * (j & 7));
-      const int ex = j >= off ? j - off : 2 * kWords + j - off;
-      st_global_u16_if(o + ex, x, on && j < 8 && (off != 0 || n < 8) && ex < n);
-      if (n < 2 * kWords) {  // the vocabulary's end: the chunk that it parts
-        const int c = (off + n) >> 3;
-        const int el = 8 * c + j - off;
-        if (c > 0 && c < kChunks && j < 8)
-          st_global_u16_if(o + el, ld_shared_u16(row + ((c ^ (r & 7)) << 4) + 2 * j), on && el < n);
-      }
-    }
-    __syncwarp();
-  }
-}
-// One row's 32 columns as bf16 into a 32 x 32 box with 64-byte swizzle (16-byte
-// chunk j of row r at j ^ ((r / 2) % 4)), as the TMA store reads it.
-__device__ __forceinline__ void stage_box_row(uint32_t buf, int r, const float* v) {
-  const uint32_t row = buf + static_cast<uint32_t>(r) * 64u;
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                     row + ((static_cast<uint32_t>(j) ^ ((r >> 1) & 3)) << 4)),
-                 "r"(bf16x2_of(v[8 * j], v[8 * j + 1])), "r"(bf16x2_of(v[8 * j + 2], v[8 * j + 3])),
-                 "r"(bf16x2_of(v[8 * j + 4], v[8 * j + 5])),
-                 "r"(bf16x2_of(v[8 * j + 6], v[8 * j + 7]))
-                 : "memory");
 }
 
 // Unit u -> (m tile, n tile): groups of group_m m tiles, vocabulary tiles

@@ -132,6 +132,11 @@ enum KernelKind : int {
   K_QUANTIZE_FP8,
   K_LOGITS_FP8,
   K_SAMPLE,
+  K_NORM_FP8,
+  K_QUANTIZE_MXFP4,
+  K_DEQUANTIZE_MXFP4,
+  K_LOGITS_MXFP4,
+  K_TOP,
   K_COUNT
 };
 

@@ -1,0 +1,660 @@
+// The 4-bit head (sm_103a): microscaled quantisation to e2m1 and bf16 logits from
+// two operands in that format.
+//
+// The format. 32 consecutive elements of a row share a power of two 2^(b - 127), held
+// as the byte b; an element is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives).
+// b leaves the block's largest magnitude in [3.5, 7): nothing is off by more than half
+// a step of its own binade, as 7 and above would be when cut to 6. (Relative error of
+// normal values 0.112; with the largest in (3, 6] 0.115, in [4, 8) 0.115.) The division
+// by a power of two is exact, so each element is rounded once.
+//
+// Scales lie in memory as the tensor cores read them: 128 rows x 4 blocks (128
+// columns) are 512 bytes, byte (row % 32) * 16 + (row / 32 % 4) * 4 + block % 4. A
+// tile's scales are then one contiguous copy, and 16 bytes a TMEM lane.
+//
+// Logits. logits[t][v] = sum_b 2^(hb - 127) 2^(wb - 127) sum_{k in b} hq[t][k] wq[v][k]
+// on the tensor cores with the scales applied there (tcgen05 kind::mxf4, K = 64 an
+// MMA), fp32 accumulators in TMEM over the whole K, one rounding to bf16.
+//
+// Batch invariance: a row's products and their order depend on H alone.
+#include <atomic>
+#include <cstdint>
+#include <cstdio>
+
+#include <cuda_bf16.h>
+
+#include "internal.h"
+#include "lmhead.h"
+#include "out_rows.cuh"
+#include "ptx.cuh"
+
+namespace lmh {
+
+namespace {
+
+constexpr int kXBlock = 32;     // elements of a scale
+constexpr int kXAtomRows = 128; // rows and
+constexpr int kXAtomCols = 128; // columns of 512 bytes of scales
+constexpr int kXAtomBytes = 512;
+constexpr uint32_t kXPad = 127; // the scale 1, in the atoms' unused places
+
+// ------------------------------------------------------------ quantisation
+// The byte of a block whose largest magnitude has these bf16 bits: its exponent,
+// rounded up from 1.75 on, less two; NaN (255) where the block holds an infinity or
+// a NaN.
+__device__ __forceinline__ uint32_t mx_scale(uint32_t amax_bits16) {
+  if (amax_bits16 >= 0x7f80u) return 255u;
+  const uint32_t e = (amax_bits16 + 0x20u) >> 7;
+  return e > 2u ? e - 2u : 0u;
+}
+
+// Eight bf16 values times 2^(127 - b) as eight e2m1 codes, the first in the lowest bits.
+__device__ __forceinline__ uint32_t mx_codes(const uint4& v, uint32_t b) {
+  const float inv = __uint_as_float(b == 255u ? 0u : (254u - b) << 23);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float y[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f2_unpack(f2_mul(f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)),
+                     f2_pack(inv, inv)),
+              y[2 * i], y[2 * i + 1]);
+  uint32_t out;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(out)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return out;
+}
+
+constexpr int kXThreads = 256;
+
+// A CTA takes 128 rows x 128 columns: 16 lanes a row (16 bytes each), eight rows a
+// thread, all loaded before the first is used. A block is four lanes; a row's four
+// scales meet in one word, and lane 0 of a row gathers the words of four rows, 32
+// apart, into the 16 bytes that they share.
+__global__ void __launch_bounds__(kXThreads)
+    quantize_mxfp4_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
+                          int64_t kb, int64_t n_tiles, uint8_t* __restrict__ q,
+                          uint8_t* __restrict__ scale) {
+  const int sub = threadIdx.x & 15, r16 = threadIdx.x >> 4;
+  for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
+    const int64_t rb = b / kb;
+    const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
+    const int64_t row0 = rb * kXAtomRows + r16;
+    uint4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + 16 * i;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row < rows && col < cols) v[i] = *reinterpret_cast<const uint4*>(x + row * ld + col);
+    }
+    uint32_t words[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + 16 * i;
+      const bool on = row < rows && col < cols;
+      uint32_t m = 0u;
+      m = __vmaxu2(m, v[i].x & 0x7fff7fffu);
+      m = __vmaxu2(m, v[i].y & 0x7fff7fffu);
+      m = __vmaxu2(m, v[i].z & 0x7fff7fffu);
+      m = __vmaxu2(m, v[i].w & 0x7fff7fffu);
+      m = max(m & 0xffffu, m >> 16);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      const uint32_t s = mx_scale(m);
+      if (on) *reinterpret_cast<uint32_t*>(q + (row * cols + col) / 2) = mx_codes(v[i], s);
+      uint32_t w = (on ? s : kXPad) << (8 * (sub >> 2));
+      w |= __shfl_xor_sync(0xffffffffu, w, 4);
+      w |= __shfl_xor_sync(0xffffffffu, w, 8);
+      words[i] = w;
+    }
+    if (sub == 0) {
+      uint4* o = reinterpret_cast<uint4*>(scale + b * kXAtomBytes) + r16;
+      o[0] = make_uint4(words[0], words[2], words[4], words[6]);
+      o[16] = make_uint4(words[1], words[3], words[5], words[7]);
+    }
+  }
+}
+
+// The scale of byte b in fp32.
+__device__ __forceinline__ float mx_value(uint32_t b) {
+  if (b == 0u) return 0x1p-127f;
+  return __uint_as_float(b == 255u ? 0x7fffffffu : b << 23);
+}
+
+// The same tiles back to bf16.
+__global__ void __launch_bounds__(kXThreads)
+    dequantize_mxfp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
+                            int64_t rows, int64_t cols, int64_t kb, int64_t n_tiles,
+                            uint16_t* __restrict__ out, int64_t ld) {
+  const int sub = threadIdx.x & 15, r16 = threadIdx.x >> 4;
+  for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
+    const int64_t rb = b / kb;
+    const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
+    const int64_t row0 = rb * kXAtomRows + r16;
+    if (col >= cols) continue;
+    uint32_t codes[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + 16 * i;
+      codes[i] = 0u;
+      if (row < rows) codes[i] = *reinterpret_cast<const uint32_t*>(q + (row * cols + col) / 2);
+    }
+    const uint4* s = reinterpret_cast<const uint4*>(scale + b * kXAtomBytes) + r16;
+    const uint4 sa = s[0], sb = s[16];
+    const uint32_t words[8] = {sa.x, sb.x, sa.y, sb.y, sa.z, sb.z, sa.w, sb.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t row = row0 + 16 * i;
+      if (row >= rows) continue;
+      const float f = mx_value((words[i] >> (8 * (sub >> 2))) & 0xffu);
+      uint32_t h[4], o[4];
+      asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+          "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+          : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+          : "r"(codes[i]));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+        o[j] = bf16x2_of(p.x * f, p.y * f);
+      }
+      *reinterpret_cast<uint4*>(out + row * ld + col) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+}
+
+// ------------------------------------------------------------ 4-bit logits
+constexpr int kXM = 128;              // token rows of one CTA's tile
+constexpr int kXN = 256;              // most vocabulary columns of a tile
+constexpr int kXK = 256;              // elements of a ring stage: 128 bytes a row
+constexpr int kXStageAtoms = kXK / kXAtomCols;
+constexpr int kXBox = 32;             // columns of an output box
+constexpr int kXMaxStages = 8;
+constexpr int kXEpiWarps = 4;
+constexpr int kXLogitsThreads = 64 + 32 * kXEpiWarps;  // warp 0 loads, warp 1 issues
+constexpr int kXStagingWarp = 4096;   // two 32 x 32 bf16 boxes
+constexpr int kXStagingBytes = kXEpiWarps * kXStagingWarp;
+constexpr int kXBarBytes = 512;
+constexpr int kXSmemBytes = 232448;
+constexpr int kXRingBytes = (kXSmemBytes - 1024 - kXBarBytes - kXStagingBytes) / 1024 * 1024;
+// TMEM's 512 columns: two accumulators, of which the second starts before the first
+// ends (256-column tiles: the columns [208, 256) are in both), and two sets of scales.
+constexpr uint32_t kXScaleCol = 464;  // where the scales begin
+constexpr uint32_t kXScaleSet = 24;   // a stage's: 2 x 4 columns for A, 2 x 8 for B
+static_assert(kXScaleCol + 2 * kXScaleSet <= 512, "TMEM columns");
+
+struct Mxfp4Params {
+  int T, V, KB;           // rows, vocabulary, ring stages of K
+  int k_atoms;            // 128-column atoms of K: ceil(H / 128)
+  int k_steps;            // MMAs of K: ceil(H / 64)
+  int tile_n;             // 128 or 256
+  int n_m, n_n, n_units;
+  int group_m;
+  int a_rows;             // rows of an A box (T <= 128: T rounded up to 8)
+  const uint8_t* hs;      // [ceil(T / 128)][k_atoms][512]
+  const uint8_t* ws;      // [ceil(V / 128)][k_atoms][512]
+  uint16_t* out;
+  int64_t ld;
+  int tma_out, v_tma;     // as for the fp8 logits
+  unsigned* status;
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e2m1 inputs with a scale for 32 of K each, K = 64.
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
+// 512 bytes of scales (32 rows of 16 bytes) into four TMEM columns, to the lanes of all
+// four warps. Runs in order with the MMAs that the same thread issues.
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+// Shared-memory descriptor of such an atom: no swizzle, 8 rows of 16 bytes together,
+// 128 bytes from one such group to the next.
+__device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
+  d |= static_cast<uint64_t>(128u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  return d;
+}
+
+// Instruction descriptor for kind::mxf4: A and B e2m1 (format 1 in bits 7 and 10), both
+// K-major, [17,23) N >> 3, bit 23 scales are powers of two, [24,29) M >> 4; `half`: which two
+// of an atom's four scales ([4,6) for B, [29,31) for A: 0 or 2).
+__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t half) {
+  return (half << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) |
+         (half << 29);
+}
+
+__device__ __forceinline__ void mx_unit(const Mxfp4Params& p, int u, int& m, int& n) {
+  const int per_group = p.group_m * p.n_n;
+  const int g = u / per_group;
+  const int first = g * p.group_m;
+  const int gm = min(p.group_m, p.n_m - first);
+  const int r = u - g * per_group;
+  n = r / gm;
+  m = first + (r - n * gm);
+}
+
+// Warp 0 loads, warp 1 copies the scales to TMEM and issues the MMAs, the others turn
+// finished tiles to bf16. Tokens are the MMA's rows, the vocabulary its columns.
+__global__ void __launch_bounds__(kXLogitsThreads, 1)
+    logits_mxfp4_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t base = smem_u32(smem);
+  const uint32_t staging = base + kXRingBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kXRingBytes + kXStagingBytes);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (kXMaxStages + s); };
+  const uint32_t tfull_bar = bar0 + 8u * (2 * kXMaxStages);
+  const uint32_t tfree_bar = bar0 + 8u * (2 * kXMaxStages + 1);
+  const uint32_t final_bar = bar0 + 8u * (2 * kXMaxStages + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kXMaxStages + 3);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  static_assert(8 * (2 * kXMaxStages + 3) + 8 <= kXBarBytes, "barrier area");
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * (kXK / 2);
+  const uint32_t b_bytes = static_cast<uint32_t>(p.tile_n) * (kXK / 2);
+  const uint32_t n_rb = static_cast<uint32_t>(p.tile_n / kXAtomRows);  // row blocks of B's scales
+  constexpr uint32_t kSetBytes = kXStageAtoms * kXAtomBytes;           // 128 rows of a stage
+  const uint32_t s_bytes = (1 + n_rb) * kSetBytes;
+  const uint32_t stage_bytes = a_bytes + b_bytes + s_bytes;
+  // the last stage's A operand may reach 128 rows on, past a short stage
+  const uint32_t n_st =
+      min(static_cast<uint32_t>(kXMaxStages),
+          (kXRingBytes - (kXM * kXK / 2 - min(stage_bytes, static_cast<uint32_t>(kXM * kXK / 2)))) /
+              stage_bytes);
+  // the second accumulator's first column, and the boxes that both hold
+  const uint32_t acc1 = p.tile_n == kXN ? kXScaleCol - kXN : kXN;
+  const int shared_boxes = p.tile_n == kXN ? 2 : 0;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kXMaxStages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(tfull_bar, 1);
+    mbar_init(tfree_bar, kXEpiWarps);
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (p.tma_out) tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0;
+      long long issued = 0;
+      bool ok = true;
+      const int last_rb = (p.V - 1) / kXAtomRows;
+      for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
+        int m, n;
+        mx_unit(p, u, m, n);
+        const int rb0 = n * static_cast<int>(n_rb);
+        const int rbs = min(static_cast<int>(n_rb), last_rb + 1 - rb0);  // that exist
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sA = base + stage * stage_bytes;
+          const uint32_t sS = sA + a_bytes + b_bytes;
+          const uint32_t bytes =
+              static_cast<uint32_t>(min(kXStageAtoms, p.k_atoms - kb * kXStageAtoms)) * kXAtomBytes;
+          mbar_arrive_expect_tx(full_bar(stage),
+                                a_bytes + b_bytes + static_cast<uint32_t>(1 + rbs) * bytes);
+          tma_load_2d(sA + a_bytes, &tmB, full_bar(stage), kb * (kXK / 2), n * p.tile_n);
+          tma_load_2d(sA, &tmA, full_bar(stage), kb * (kXK / 2), m * kXM);
+          const int64_t at = static_cast<int64_t>(kb) * kXStageAtoms;
+          bulk_load_1d(sS, p.hs + (static_cast<int64_t>(m) * p.k_atoms + at) * kXAtomBytes, bytes,
+                       full_bar(stage));
+          for (int i = 0; i < rbs; ++i)
+            bulk_load_1d(sS + (1 + i) * kSetBytes,
+                         p.ws + (static_cast<int64_t>(rb0 + i) * p.k_atoms + at) * kXAtomBytes,
+                         bytes, full_bar(stage));
+          ++issued;
+          if (++stage == n_st) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Wait (bounded) for the copies still in flight, so that none lands after the
+      // CTA exits: in every case, as another role may give up after the last was issued.
+      volatile int no_abort = 0;
+      for (long long i = issued > n_st ? issued - n_st : 0; i < issued; ++i)
+        mbar_wait(full_bar(static_cast<uint32_t>(i % n_st)),
+                  static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t stage = 0, phase = 0, set = 0, tile = 0;
+      bool ok = true;
+      for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x, ++tile) {
+        // the tile before has left the columns that both accumulators hold (and the one
+        // before that has left this one)
+        if (!mbar_wait(tfree_bar, (tile & 1u) ^ 1u, abort_flag, p.status)) break;
+        const uint32_t acc = tmem + ((tile & 1u) ? acc1 : 0u);
+        int steps = p.k_steps;
+        for (int kb = 0; kb < p.KB; ++kb) {
+          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sA = base + stage * stage_bytes;
+          const uint64_t ad = sw128_kmajor_desc(sA), bd = sw128_kmajor_desc(sA + a_bytes);
+          const uint64_t sd = scales_desc(sA + a_bytes + b_bytes);
+          const uint32_t sfa = tmem + kXScaleCol + set * kXScaleSet, sfb = sfa + 8;
+          const int now = min(steps, kXK / 64);
+#pragma unroll
+          for (int a = 0; a < kXStageAtoms; ++a) {
+            if (2 * a < now) {
+              tc_copy_scales(sfa + 4 * a, sd + a * (kXAtomBytes >> 4));
+              for (uint32_t i = 0; i < n_rb; ++i)
+                tc_copy_scales(sfb + 8 * a + 4 * i,
+                               sd + ((1 + i) * kSetBytes + a * kXAtomBytes) / 16);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < kXK / 64; ++k)  // 32 bytes on in each 128-byte row
+            if (k < now)
+              tc_mma_mxf4(acc, ad + 2 * k, bd + 2 * k,
+                          idesc_mxf4(kXM, static_cast<uint32_t>(p.tile_n), 2u * (k & 1)),
+                          sfa + 4 * (k >> 1), sfb + 8 * (k >> 1), (kb | k) != 0 ? 1u : 0u);
+          steps -= now;
+          tc_commit(empty_bar(stage));
+          set ^= 1u;
+          if (++stage == n_st) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (ok) tc_commit(tfull_bar);
+      }
+      // Every MMA of this thread ends before TMEM is released, also where a role gave up.
+      volatile int no_abort = 0;
+      tc_commit(final_bar);
+      mbar_wait(final_bar, 0, &no_abort, p.status);
+    }
+  } else {
+    const int ew = warp - 2;
+    const int lanes0 = 32 * (warp & 3);  // the TMEM lanes this warp may read
+    const uint32_t lane_addr = static_cast<uint32_t>(lanes0) << 16;
+    const uint32_t stg = staging + ew * kXStagingWarp;
+    const int boxes = p.tile_n / kXBox;
+    uint32_t tile = 0, obuf = 0;
+    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++tile) {
+      int m, n;
+      mx_unit(p, u, m, n);
+      const int row0 = m * kXM + lanes0;
+      const int row = row0 + lane;
+      const bool warp_on = row0 < p.T;
+      const int64_t col0 = static_cast<int64_t>(n) * p.tile_n;
+      const uint32_t src = tmem + lane_addr + ((tile & 1u) ? acc1 : 0u);
+      const bool ready = mbar_wait(tfull_bar, tile & 1u, abort_flag, p.status);
+      if (!__all_sync(0xffffffffu, ready)) break;
+      tc_fence_after();
+      // the shared columns first: the last boxes of the first accumulator, the first
+      // of the second
+      const int first = (tile & 1u) ? 0 : boxes - shared_boxes;
+      if (shared_boxes == 0 || !warp_on) {
+        // nothing to hold on to: the accumulators are apart (the tile before has left
+        // this one's by its order), or no row is stored
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tfree_bar);
+      }
+      if (!warp_on) continue;
+      for (int i = 0; i < boxes; ++i) {
+        const int b = first + i < boxes ? first + i : first + i - boxes;
+        const int64_t colb = col0 + b * kXBox;
+        float v[32];
+        tmem_ld32(src + b * kXBox, v);
+        if (shared_boxes > 0 && i == shared_boxes - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(tfree_bar);
+        }
+        if (colb >= p.V) continue;
+        const uint32_t obox = stg + obuf;
+        if (!p.tma_out) {
+          uint32_t words[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) words[j] = bf16x2_of(v[2 * j], v[2 * j + 1]);
+          const int64_t left = p.V - colb;
+          store_rows(stg, lane, words, p.out + static_cast<int64_t>(row0) * p.ld + colb, p.ld,
+                     min(32, p.T - row0), static_cast<int>(min(static_cast<int64_t>(kXBox), left)));
+          continue;
+        }
+        // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
+        obuf ^= kXStagingWarp / 2;
+        if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
+        __syncwarp();
+        stage_box_row(obox, lane, v);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (colb < p.v_tma) tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
+          bulk_commit_group();  // an empty one too: the buffers' turns are counted in groups
+        }
+        if (p.v_tma < p.V && p.v_tma < colb + kXBox && row < p.T) {
+          // the vocabulary's last columns (at most seven): a chunk that TMA would fill
+          // with zeros past the row's end
+          const int j = (p.v_tma - static_cast<int>(colb)) >> 3;
+          const uint4 c = ld_shared_v4(obox + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
+          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+          uint16_t* o = p.out + static_cast<int64_t>(row) * p.ld + p.v_tma;
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            st_global_u16_if(o + e, static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1))),
+                             p.v_tma + e < p.V);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();  // every output box of this warp has been written
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The kernel's shared-memory attribute belongs to the device: set by its first call.
+cudaError_t mxfp4_setup() {
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(logits_mxfp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kXSmemBytes);
+  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
+
+int launch_error(cudaError_t e, const char* what) {
+  char msg[256];
+  snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
+  return api_set_error(LMH_ERR_LAUNCH, msg);
+}
+
+// What the quantiser and its inverse ask of a matrix.
+int check_matrix(int64_t rows, int64_t cols, int64_t ld) {
+  if (rows < 0 || rows > LMH_MAX_DIM || cols < 1 || cols > LMH_MAX_DIM)
+    return api_set_error(LMH_ERR_INVALID_ARG, "rows or cols out of range");
+  if (ld < cols) return api_set_error(LMH_ERR_INVALID_ARG, "ld must be at least cols");
+  if (cols % kXBlock != 0 || ld % 8 != 0)
+    return api_set_error(LMH_ERR_ALIGNMENT, "cols must be a multiple of 32 and ld of 8");
+  return LMH_OK;
+}
+
+}  // namespace
+
+}  // namespace lmh
+
+extern "C" int lmhead_quantize_mxfp4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld,
+                                     uint8_t* q, uint8_t* scale, struct CUstream_st* stream) {
+  using namespace lmh;
+  int rc = check_matrix(rows, cols, ld);
+  if (rc != LMH_OK) return rc;
+  if (rows == 0) return api_set_error(LMH_OK, "");
+  if (!x || !q || !scale)
+    return api_set_error(LMH_ERR_INVALID_ARG, "x, q and scale are required");
+  if (misaligned(x, 16) || misaligned(q, 16) || misaligned(scale, 16))
+    return api_set_error(LMH_ERR_ALIGNMENT, "x, q and scale need 16-byte alignment");
+  int sms = 0;
+  unsigned* status = nullptr;
+  rc = api_device(&sms, &status);
+  if (rc != LMH_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t kb = ceil_div(cols, kXAtomCols);
+  const int64_t tiles = ceil_div(rows, kXAtomRows) * kb;
+  cudaError_t e;
+  {
+    KernelTimer timer(K_QUANTIZE_MXFP4, st);
+    const int grid = static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms);
+    quantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(x, rows, cols, ld, kb, tiles, q, scale);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+  }
+  if (e != cudaSuccess) return launch_error(e, "4-bit quantisation");
+  return api_set_error(LMH_OK, "");
+}
+
+extern "C" int lmhead_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int64_t rows,
+                                       int64_t cols, uint16_t* out, int64_t ld_out,
+                                       struct CUstream_st* stream) {
+  using namespace lmh;
+  int rc = check_matrix(rows, cols, ld_out);
+  if (rc != LMH_OK) return rc;
+  if (rows == 0) return api_set_error(LMH_OK, "");
+  if (!q || !scale || !out)
+    return api_set_error(LMH_ERR_INVALID_ARG, "q, scale and out are required");
+  if (misaligned(q, 16) || misaligned(scale, 16) || misaligned(out, 16))
+    return api_set_error(LMH_ERR_ALIGNMENT, "q, scale and out need 16-byte alignment");
+  int sms = 0;
+  unsigned* status = nullptr;
+  rc = api_device(&sms, &status);
+  if (rc != LMH_OK) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int64_t kb = ceil_div(cols, kXAtomCols);
+  const int64_t tiles = ceil_div(rows, kXAtomRows) * kb;
+  cudaError_t e;
+  {
+    KernelTimer timer(K_DEQUANTIZE_MXFP4, st);
+    const int grid = static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms);
+    dequantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(q, scale, rows, cols, kb, tiles, out,
+                                                        ld_out);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+  }
+  if (e != cudaSuccess) return launch_error(e, "4-bit dequantisation");
+  return api_set_error(LMH_OK, "");
+}
+
+extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidden_scale,
+                                   const uint8_t* weight_q, const uint8_t* weight_scale, int64_t T,
+                                   int64_t H, int64_t V, uint16_t* logits, int64_t ld_logits,
+                                   struct CUstream_st* stream) {
+  using namespace lmh;
+  if (T < 0 || T > LMH_MAX_DIM || V < 1 || V > LMH_MAX_DIM || H < 1 || H > LMH_MAX_DIM)
+    return api_set_error(LMH_ERR_INVALID_ARG, "T, H or V out of range");
+  if (H % kXBlock != 0) return api_set_error(LMH_ERR_ALIGNMENT, "H must be a multiple of 32");
+  if (ld_logits < V)
+    return api_set_error(LMH_ERR_INVALID_ARG, "ld_logits must be at least V");
+  if (ceil_div(T, kXM) * ceil_div(V, kXAtomRows) > (1LL << 30))
+    return api_set_error(LMH_ERR_INVALID_ARG, "T x V has too many tiles");
+  if (T == 0) return api_set_error(LMH_OK, "");
+  if (!hidden_q || !hidden_scale || !weight_q || !weight_scale || !logits)
+    return api_set_error(LMH_ERR_INVALID_ARG, "every pointer is required");
+  if (misaligned(hidden_q, 16) || misaligned(weight_q, 16) || misaligned(hidden_scale, 16) ||
+      misaligned(weight_scale, 16) || misaligned(logits, 2))
+    return api_set_error(LMH_ERR_ALIGNMENT,
+                         "the operands and scales need 16-byte, logits 2-byte alignment");
+  int sms = 0;
+  unsigned* status = nullptr;
+  int rc = api_device(&sms, &status);
+  if (rc != LMH_OK) return rc;
+  cudaError_t e = mxfp4_setup();
+  if (e != cudaSuccess) return launch_error(e, "4-bit logits");
+  const int64_t n_m = ceil_div(T, kXM);
+  Mxfp4Params p{};
+  p.tile_n = kXN;
+  const int64_t n_n = ceil_div(V, p.tile_n);
+  p.T = static_cast<int>(T);
+  p.V = static_cast<int>(V);
+  p.KB = static_cast<int>(ceil_div(H, kXK));
+  p.k_atoms = static_cast<int>(ceil_div(H, kXAtomCols));
+  p.k_steps = static_cast<int>(ceil_div(H, 64));
+  p.n_m = static_cast<int>(n_m);
+  p.n_n = static_cast<int>(n_n);
+  p.n_units = static_cast<int>(n_m * n_n);
+  p.group_m = 16;
+  p.a_rows = T < kXM ? static_cast<int>((T + 7) / 8 * 8) : kXM;
+  p.hs = hidden_scale;
+  p.ws = weight_scale;
+  p.out = logits;
+  p.ld = ld_logits;
+  p.v_tma = static_cast<int>(V / 8 * 8);
+  p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16) && p.v_tma > 0) ? 1 : 0;
+  p.status = status;
+  CUtensorMap ta, tb, tc{};
+  if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, p.v_tma, T, ld_logits * 2)) != LMH_OK)
+    return rc;
+  if ((rc = api_make_tmap_u8(&ta, hidden_q, H / 2, T, H / 2, kXK / 2, p.a_rows)) != LMH_OK)
+    return rc;
+  if ((rc = api_make_tmap_u8(&tb, weight_q, H / 2, V, H / 2, kXK / 2, p.tile_n)) != LMH_OK)
+    return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  {
+    KernelTimer timer(K_LOGITS_MXFP4, st);
+    const int grid = p.n_units < sms ? p.n_units : sms;
+    logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tc, p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) note_launch();
+  }
+  if (e != cudaSuccess) return launch_error(e, "4-bit logits");
+  return api_set_error(LMH_OK, "");
+}
