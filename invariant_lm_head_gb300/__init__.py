@@ -714,13 +714,13 @@ def lmhead_sample(logits, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p
 
 
 def lmhead_rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None, out_scale=None,
-                       out_residual=None, stream=None):
+                       out_residual=None, want_residual: bool = True, stream=None):
     """RMS norm of x (+ residual), block-quantised to e4m3 (see include/lmhead.h).
 
     x and residual bf16 [rows, cols] (rows may be strided), weight bf16 [cols].
     Returns (q float8_e4m3fn [rows, cols], scale f32 [rows, ceil(cols / 128)], the
     bf16 sum x + residual or None), q and scale as lmhead_logits_fp8 takes them.
-    out_residual may be residual or x itself.
+    out_residual may be residual or x itself; want_residual=False leaves the sum out.
     """
     torch = _torch()
     dev = x.device
@@ -745,7 +745,7 @@ def lmhead_rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None,
         out = empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev)
     if out_scale is None:
         out_scale = empty((rows, kb), dtype=torch.float32, device=dev)
-    if residual is not None and out_residual is None:
+    if residual is not None and out_residual is None and want_residual:
         out_residual = empty((rows, cols), dtype=bf16, device=dev)
         ld_out = cols
     rc = library().lmhead_rmsnorm_fp8(x.data_ptr(), _ptr(residual), weight.data_ptr(), rows, cols,

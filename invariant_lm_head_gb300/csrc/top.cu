@@ -138,7 +138,8 @@ __device__ __forceinline__ void fold32(OnlineStat& st, float& most, const uint4 
     m2 = __hmax2(m2, __hmax2(__hmax2(bf2(w[k].x), bf2(w[k].y)), __hmax2(bf2(w[k].z), bf2(w[k].w))));
   const float gmax = fmaxf(__low2float(m2), __high2float(m2));
   most = fmaxf(most, gmax);
-  const float mn = fmaxf(st.m, __fmul_rn(gmax, c));
+  // never -inf, from which a finite x * c would be infinitely far
+  const float mn = fmaxf(fmaxf(st.m, __fmul_rn(gmax, c)), -3.402823466e38f);
   const float d0 = fmaxf(__fsub_rn(st.m, mn), kPFloor);
   const float a = ex2(d0);
   f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
@@ -259,14 +260,19 @@ __device__ __noinline__ void list_by_bisection(TopShared& sh, const uint16_t* ro
   __syncthreads();
 }
 
-// The row's sums where y = x * c leaves fp32 or the largest logit is +inf: logits equal
-// to the largest weigh 1. One CTA, in an order fixed by V.
+// z - max z where y = x * c is too large to be subtracted from.
+__device__ __forceinline__ float far_shift(float x, float most, float t) {
+  return x == most ? 0.f : __fdiv_rn(__fsub_rn(x, most), t);
+}
+
+// The sums of such a row: logits equal to the largest weigh 1. One CTA, in an order
+// fixed by V.
 __device__ __noinline__ SliceStat sums_of_extremes(TopShared& sh, const uint16_t* row, int64_t V,
-                                                   float c, float most) {
+                                                   float t, float most) {
   float s = 0.f, u = 0.f;
   for (int64_t i = threadIdx.x; i < V; i += kPThreads) {
     const float x = __uint_as_float(static_cast<uint32_t>(row[i]) << 16);
-    const float d = x == most ? 0.f : fmaxf((x - most) * c, kPFloor);
+    const float d = fmaxf(__fmul_rn(far_shift(x, most, t), kLog2e), kPFloor);
     const float e = ex2(d);
     s += e;
     u += e * d;
@@ -417,16 +423,19 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
 
   SliceStat all = sh.slice[0];
   for (int k = 1; k < kC; ++k) merge_slice(all, sh.slice[k]);
-  // y left fp32, or the largest logit is +inf
-  const bool extreme = all.most > -INFINITY && !(fabsf(__fmul_rn(all.most, c)) <= 3.402823466e38f);
-  if (extreme) all = sums_of_extremes(sh, x, p.V, c, all.most);
+  // The largest y itself is shifted by its product's rounding, up to 2^-4 at 2^20; past
+  // that (or where the largest logit is +inf) the row is summed again.
+  const bool extreme = all.most > -INFINITY && !(fabsf(__fmul_rn(all.most, c)) <= 0x1p20f);
+  if (extreme) all = sums_of_extremes(sh, x, p.V, t, all.most);
   const bool nothing = !(all.most > -INFINITY);
   const float l2s = log2f(all.s);
   const float bad = __int_as_float(0x7fffffff);
   auto logprob = [&](float v) -> float {
     if (!valid_t) return bad;
     if (nothing || !(v > -INFINITY)) return -INFINITY;  // a masked one
-    const float d = !extreme ? __fmaf_rn(v, c, -all.m) : v == all.most ? 0.f : (v - all.most) * c;
+    const float d = __fmaf_rn(v, c, -all.m);
+    if (extreme || d == -INFINITY)  // in base e what base 2 may not hold
+      return __fsub_rn(far_shift(v, all.most, t), __fmul_rn(kLn2, l2s));
     return __fmul_rn(kLn2, __fsub_rn(d, l2s));
   };
   if (threadIdx.x == 0 && p.out_entropy)

@@ -8,6 +8,12 @@ log-prob's and its logits' do not depend on the batch its row arrives in.
     token, logprob = head.sample(hidden, uniform, 0.7, top_p=0.95)
     head.refresh(weight)                        # after a training step
 
+With the model's last norm in it (lmhead_rmsnorm_fp8, in place of the quantisation), the
+head takes the last layer's output and the residual stream:
+
+    head = FP8Head(weight, norm_weight, norm_eps=1e-6)
+    token, logprob = head.sample(hidden, uniform, residual=residual)
+
 Every call runs on the current stream and can be captured into a CUDA graph
 (after a first call outside of one). The head holds one byte per weight
 element, and four per 128 x 128 block.
@@ -17,12 +23,15 @@ from __future__ import annotations
 
 import invariant_lm_head_gb300 as lmh
 
+from .quantized_head import QuantizedHead
 
-class FP8Head:
+
+class FP8Head(QuantizedHead):
     """A head whose weight [V, H] is held in e4m3 with one scale per 128 x 128 block."""
 
-    def __init__(self, weight):
+    def __init__(self, weight, norm_weight=None, norm_eps: float = 1e-6):
         self.weight_q, self.weight_scale = lmh.lmhead_quantize_fp8(weight, 128)
+        self.norm_weight, self.norm_eps = norm_weight, norm_eps
 
     @property
     def vocab_size(self) -> int:
@@ -36,26 +45,17 @@ class FP8Head:
         """Quantise a new weight of the same shape in place (graphs stay valid)."""
         lmh.lmhead_quantize_fp8(weight, 128, out=self.weight_q, out_scale=self.weight_scale)
 
-    def logits(self, hidden, *, out_logits=None):
-        """bf16 logits [T, V] of hidden bf16 [T, H] (rows may be strided)."""
-        hidden_q, hidden_scale = lmh.lmhead_quantize_fp8(hidden)
+    def logits(self, hidden, *, residual=None, out_logits=None):
+        """bf16 logits [T, V] of hidden bf16 [T, H] (rows may be strided).
+
+        A head with a norm takes hidden states before it, and adds residual (or None).
+        """
+        if self.norm_weight is not None:
+            hidden_q, hidden_scale, _ = lmh.lmhead_rmsnorm_fp8(
+                hidden, self.norm_weight, residual, eps=self.norm_eps, want_residual=False)
+        elif residual is not None:
+            raise ValueError("residual needs a head with a norm")
+        else:
+            hidden_q, hidden_scale = lmh.lmhead_quantize_fp8(hidden)
         return lmh.lmhead_logits_fp8(hidden_q, hidden_scale, self.weight_q, self.weight_scale,
                                      out_logits=out_logits)
-
-    def sample(self, hidden, uniform, temperature=1.0, *, top_k=0, top_p=1.0, min_p=0.0,
-               mask=None, out_logits=None):
-        """(token int32 [T], logprob f32 [T]) of hidden bf16 [T, H].
-
-        uniform f32 [T] in [0, 1]; the settings are those of lmhead_sample. mask
-        (bool [T, V] or [V]) marks tokens that must not be drawn; they drop out of
-        the log-prob's distribution too. out_logits receives the (masked) logits.
-        """
-        if out_logits is None and self.vocab_size % 8:
-            # rows of their own that start on 16 bytes, for wide stores and loads
-            V = self.vocab_size
-            out_logits = hidden.new_empty((hidden.shape[0], -(-V // 8) * 8))[:, :V]
-        logits = self.logits(hidden, out_logits=out_logits)
-        if mask is not None:
-            logits.masked_fill_(mask, float("-inf"))
-        return lmh.lmhead_sample(logits, uniform, temperature, top_k=top_k, top_p=top_p,
-                                 min_p=min_p)
