@@ -799,6 +799,22 @@ int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_
                    CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
+int api_make_tmap_scales(CUtensorMap* map, const void* base, uint64_t words, uint64_t rows,
+                         uint32_t box_words, uint32_t box_rows) {
+  cuuint64_t dims[2] = {words, rows};
+  cuuint64_t strides[1] = {words * 4};
+  cuuint32_t box[2] = {box_words, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims,
+                              strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(LMH_ERR_LAUNCH, "cuTensorMapEncodeTiled (scales) failed (%d) for %llu x %llu", (int)r,
+                (unsigned long long)words, (unsigned long long)rows);
+  return LMH_OK;
+}
+
 int api_make_out_tmap_bf16(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows,
                            uint64_t row_bytes) {
   return make_out_tmap(map, base, cols, rows, row_bytes, false);

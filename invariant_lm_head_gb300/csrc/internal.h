@@ -172,6 +172,9 @@ int api_make_tmap(CUtensorMap* map, const void* base, uint64_t inner, uint64_t o
 // The same for 8-bit elements (fp8 operands), 128-byte swizzle.
 int api_make_tmap_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                      uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// 32-bit words without a swizzle (the 4-bit operands' scales, 128 words an atom).
+int api_make_tmap_scales(CUtensorMap* map, const void* base, uint64_t words, uint64_t rows,
+                         uint32_t box_words, uint32_t box_rows);
 // A bf16 output in 32 x 32 boxes with 64-byte swizzle (one epilogue warp's).
 int api_make_out_tmap_bf16(CUtensorMap* map, void* base, uint64_t cols, uint64_t rows,
                            uint64_t row_bytes);

@@ -169,11 +169,15 @@ __global__ void __launch_bounds__(kXThreads)
 }
 
 // ------------------------------------------------------------ 4-bit logits
-constexpr int kXM = 128;              // token rows of one CTA's tile
-constexpr int kXN = 256;              // most vocabulary columns of a tile
+// A CTA alone takes a tile of 128 x 256, a pair of CTAs (cta_group::2) one of 256 x 256:
+// each holds its 128 rows of A and half of B, so an MMA reads 8 KB of each SM's shared
+// memory instead of 12, and L2 delivers 35 KB a stage and CTA instead of 51.
+constexpr int kXM = 128;              // token rows of a CTA
+constexpr int kXN = 256;              // vocabulary columns of a tile
 constexpr int kXK = 256;              // elements of a ring stage: 128 bytes a row
-constexpr int kXStageAtoms = kXK / kXAtomCols;
+constexpr int kXSteps = kXK / 64;     // MMAs of a stage
 constexpr int kXBox = 32;             // columns of an output box
+constexpr int kXBoxes = kXN / kXBox;
 constexpr int kXMaxStages = 8;
 constexpr int kXEpiWarps = 4;
 constexpr int kXLogitsThreads = 64 + 32 * kXEpiWarps;  // warp 0 loads, warp 1 issues
@@ -182,22 +186,24 @@ constexpr int kXStagingBytes = kXEpiWarps * kXStagingWarp;
 constexpr int kXBarBytes = 512;
 constexpr int kXSmemBytes = 232448;
 constexpr int kXRingBytes = (kXSmemBytes - 1024 - kXBarBytes - kXStagingBytes) / 1024 * 1024;
+constexpr int kXStageAtoms = kXK / kXAtomCols;             // atoms of a stage's scales: 2
+constexpr int kXSetBytes = kXStageAtoms * kXAtomBytes;     // a stage's scales of 128 rows
+constexpr int kXScaleBytes = (1 + kXN / kXAtomRows) * kXSetBytes;  // A's, then B's
 // TMEM's 512 columns: two accumulators, of which the second starts before the first
-// ends (256-column tiles: the columns [208, 256) are in both), and two sets of scales.
+// ends (the columns [208, 256) are in both), and two stages' scales.
 constexpr uint32_t kXScaleCol = 464;  // where the scales begin
 constexpr uint32_t kXScaleSet = 24;   // a stage's: 2 x 4 columns for A, 2 x 8 for B
+constexpr uint32_t kXAcc1 = kXScaleCol - kXN;  // the second accumulator's first column
+constexpr int kXShared = 2;           // output boxes that touch the shared columns
 static_assert(kXScaleCol + 2 * kXScaleSet <= 512, "TMEM columns");
+static_assert(kXN - kXAcc1 <= kXShared * kXBox, "shared columns");
 
 struct Mxfp4Params {
   int T, V, KB;           // rows, vocabulary, ring stages of K
-  int k_atoms;            // 128-column atoms of K: ceil(H / 128)
   int k_steps;            // MMAs of K: ceil(H / 64)
-  int tile_n;             // 128 or 256
-  int n_m, n_n, n_units;
+  int n_m, n_n, n_units;  // tiles (of 128 or 256 rows)
   int group_m;
   int a_rows;             // rows of an A box (T <= 128: T rounded up to 8)
-  const uint8_t* hs;      // [ceil(T / 128)][k_atoms][512]
-  const uint8_t* ws;      // [ceil(V / 128)][k_atoms][512]
   uint16_t* out;
   int64_t ld;
   int tma_out, v_tma;     // as for the fp8 logits
@@ -205,22 +211,39 @@ struct Mxfp4Params {
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e2m1 inputs with a scale for 32 of K each, K = 64.
+template <bool kPair>
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
                                             uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], "
-      "p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
-      : "memory");
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+        "[%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
 }
 
 // 512 bytes of scales (32 rows of 16 bytes) into four TMEM columns, to the lanes of all
-// four warps. Runs in order with the MMAs that the same thread issues.
+// four warps; a pair's form does so in each CTA from its own shared memory. Runs in
+// order with the MMAs that the same thread issues.
+template <bool kPair>
 __device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+  if constexpr (kPair)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
 }
 
 // Shared-memory descriptor of such an atom: no swizzle, 8 rows of 16 bytes together,
@@ -236,7 +259,7 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t smem_addr) {
 // Instruction descriptor for kind::mxf4: A and B e2m1 (format 1 in bits 7 and 10), both
 // K-major, [17,23) N >> 3, bit 23 scales are powers of two, [24,29) M >> 4; `half`: which two
 // of an atom's four scales ([4,6) for B, [29,31) for A: 0 or 2).
-__device__ __forceinline__ uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t half) {
+__device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N, uint32_t half) {
   return (half << 4) | (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24) |
          (half << 29);
 }
@@ -251,12 +274,13 @@ __device__ __forceinline__ void mx_unit(const Mxfp4Params& p, int u, int& m, int
   m = first + (r - n * gm);
 }
 
-// Warp 0 loads, warp 1 copies the scales to TMEM and issues the MMAs, the others turn
-// finished tiles to bf16. Tokens are the MMA's rows, the vocabulary its columns.
-__global__ void __launch_bounds__(kXLogitsThreads, 1)
-    logits_mxfp4_kernel(const __grid_constant__ CUtensorMap tmA,
-                        const __grid_constant__ CUtensorMap tmB,
-                        const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
+// Warp 0 loads, warp 1 copies the scales to TMEM and issues the MMAs (CTA 0 of a pair for
+// both), the others turn finished tiles to bf16. Tokens are the MMA's rows, the
+// vocabulary its columns.
+template <bool kPair>
+__device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
+                                                  const CUtensorMap& tmSA, const CUtensorMap& tmSB,
+                                                  const CUtensorMap& tmC, const Mxfp4Params& p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -271,86 +295,110 @@ __global__ void __launch_bounds__(kXLogitsThreads, 1)
   const uint32_t final_bar = bar0 + 8u * (2 * kXMaxStages + 2);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * kXMaxStages + 3);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  static_assert(8 * (2 * kXMaxStages + 3) + 8 <= kXBarBytes, "barrier area");
+  // pair: the number of stages that CTA 1 loaded, told to CTA 0 at the end
+  volatile uint32_t* peer_issued = tmem_slot + 2;
+  static_assert(8 * (2 * kXMaxStages + 3) + 12 <= kXBarBytes, "barrier area");
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+  const int first_unit = kPair ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int unit_stride = kPair ? static_cast<int>(cluster_nid_x()) : static_cast<int>(gridDim.x);
   const uint32_t a_bytes = static_cast<uint32_t>(p.a_rows) * (kXK / 2);
-  const uint32_t b_bytes = static_cast<uint32_t>(p.tile_n) * (kXK / 2);
-  const uint32_t n_rb = static_cast<uint32_t>(p.tile_n / kXAtomRows);  // row blocks of B's scales
-  constexpr uint32_t kSetBytes = kXStageAtoms * kXAtomBytes;           // 128 rows of a stage
-  const uint32_t s_bytes = (1 + n_rb) * kSetBytes;
-  const uint32_t stage_bytes = a_bytes + b_bytes + s_bytes;
+  constexpr uint32_t kBBytes = (kPair ? kXN / 2 : kXN) * (kXK / 2);
+  const uint32_t stage_bytes = a_bytes + kBBytes + kXScaleBytes;
   // the last stage's A operand may reach 128 rows on, past a short stage
   const uint32_t n_st =
       min(static_cast<uint32_t>(kXMaxStages),
           (kXRingBytes - (kXM * kXK / 2 - min(stage_bytes, static_cast<uint32_t>(kXM * kXK / 2)))) /
               stage_bytes);
-  // the second accumulator's first column, and the boxes that both hold
-  const uint32_t acc1 = p.tile_n == kXN ? kXScaleCol - kXN : kXN;
-  const int shared_boxes = p.tile_n == kXN ? 2 : 0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kXMaxStages; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(s), 1);  // a pair's CTA 0: one arrive, both CTAs' bytes
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(tfull_bar, 1);
-    mbar_init(tfree_bar, kXEpiWarps);
+    mbar_init(tfree_bar, (kPair ? 2 : 1) * kXEpiWarps);  // a pair's: CTA 0's
     mbar_init(final_bar, 1);
     *abort_flag = 0;
+    *peer_issued = 0;
     fence_barrier_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
     if (p.tma_out) tma_prefetch_desc(&tmC);
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    if constexpr (kPair) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) {
+    __syncwarp();
+    cluster_sync();  // the peer's barriers are initialised before any arrive on them
+  } else {
+    __syncthreads();
+  }
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  long long issued = 0;  // stages loaded by this CTA
 
+  // Warps 0 and 1 run their loops as whole warps and act by one elected lane: with the
+  // loops in one lane's branch the issue of a stage's 11 instructions took 1450 cycles
+  // (673 us at T=2048 H=3584 V=152064 for 438).
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t stage = 0, phase = 0;
-      long long issued = 0;
-      bool ok = true;
-      const int last_rb = (p.V - 1) / kXAtomRows;
-      for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x) {
-        int m, n;
-        mx_unit(p, u, m, n);
-        const int rb0 = n * static_cast<int>(n_rb);
-        const int rbs = min(static_cast<int>(n_rb), last_rb + 1 - rb0);  // that exist
-        for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status)) {
-            ok = false;
-            break;
-          }
-          const uint32_t sA = base + stage * stage_bytes;
-          const uint32_t sS = sA + a_bytes + b_bytes;
-          const uint32_t bytes =
-              static_cast<uint32_t>(min(kXStageAtoms, p.k_atoms - kb * kXStageAtoms)) * kXAtomBytes;
-          mbar_arrive_expect_tx(full_bar(stage),
-                                a_bytes + b_bytes + static_cast<uint32_t>(1 + rbs) * bytes);
-          tma_load_2d(sA + a_bytes, &tmB, full_bar(stage), kb * (kXK / 2), n * p.tile_n);
-          tma_load_2d(sA, &tmA, full_bar(stage), kb * (kXK / 2), m * kXM);
-          const int64_t at = static_cast<int64_t>(kb) * kXStageAtoms;
-          bulk_load_1d(sS, p.hs + (static_cast<int64_t>(m) * p.k_atoms + at) * kXAtomBytes, bytes,
-                       full_bar(stage));
-          for (int i = 0; i < rbs; ++i)
-            bulk_load_1d(sS + (1 + i) * kSetBytes,
-                         p.ws + (static_cast<int64_t>(rb0 + i) * p.k_atoms + at) * kXAtomBytes,
-                         bytes, full_bar(stage));
-          ++issued;
-          if (++stage == n_st) {
-            stage = 0;
-            phase ^= 1u;
+    const bool one = elect_one();
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int u = first_unit; u < p.n_units && ok; u += unit_stride) {
+      int m, n;
+      mx_unit(p, u, m, n);
+      const int row_blk = kPair ? 2 * m + static_cast<int>(rank) : m;
+      const int b_row = n * kXN + (kPair ? static_cast<int>(rank) * (kXN / 2) : 0);
+      for (int kb = 0; kb < p.KB; ++kb) {
+        if (!__all_sync(0xffffffffu, mbar_wait(empty_bar(stage), phase ^ 1u, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        const uint32_t sA = base + stage * stage_bytes;
+        const uint32_t sS = sA + a_bytes + kBBytes;
+        if (one) {
+          if (rank == 0)
+            mbar_arrive_expect_tx(full_bar(stage), (kPair ? 2u : 1u) * stage_bytes);
+          if constexpr (kPair) {
+            const uint32_t bar = mapa_shared(full_bar(stage), 0);
+            tma_load_2d_pair(sA + a_bytes, &tmB, bar, kb * (kXK / 2), b_row);
+            tma_load_2d_pair(sA, &tmA, bar, kb * (kXK / 2), row_blk * kXM);
+            tma_load_2d_pair(sS, &tmSA, bar, kb * (kXSetBytes / 4), row_blk);
+            tma_load_2d_pair(sS + kXSetBytes, &tmSB, bar, kb * (kXSetBytes / 4),
+                             n * (kXN / kXAtomRows));
+          } else {
+            tma_load_2d(sA + a_bytes, &tmB, full_bar(stage), kb * (kXK / 2), b_row);
+            tma_load_2d(sA, &tmA, full_bar(stage), kb * (kXK / 2), row_blk * kXM);
+            tma_load_2d(sS, &tmSA, full_bar(stage), kb * (kXSetBytes / 4), row_blk);
+            tma_load_2d(sS + kXSetBytes, &tmSB, full_bar(stage), kb * (kXSetBytes / 4),
+                        n * (kXN / kXAtomRows));
           }
         }
+        ++issued;
+        if (++stage == n_st) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
+    }
+    if constexpr (kPair) {
+      if (rank != 0 && one)  // CTA 0 waits for this CTA's copies too, at the end
+        st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_issued)), 0),
+                              static_cast<uint32_t>(issued));
+    } else {
       // Wait (bounded) for the copies still in flight, so that none lands after the
       // CTA exits: in every case, as another role may give up after the last was issued.
       volatile int no_abort = 0;
@@ -359,111 +407,114 @@ __global__ void __launch_bounds__(kXLogitsThreads, 1)
                   static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    const bool one = elect_one();
+    volatile int no_abort = 0;
+    if (rank == 0) {
+      constexpr uint32_t kM = kPair ? 2 * kXM : kXM;
+      const uint64_t a0 = sw128_kmajor_desc(base), b0 = sw128_kmajor_desc(base + a_bytes);
+      const uint64_t s0 = scales_desc(base + a_bytes + kBBytes);
       uint32_t stage = 0, phase = 0, set = 0, tile = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < p.n_units && ok; u += gridDim.x, ++tile) {
+      auto commit = [&](uint32_t bar) {
+        if (one) {
+          if constexpr (kPair)
+            tc_commit_pair(bar, 0x3);
+          else
+            tc_commit(bar);
+        }
+      };
+      for (int u = first_unit; u < p.n_units && ok; u += unit_stride, ++tile) {
         // the tile before has left the columns that both accumulators hold (and the one
         // before that has left this one)
-        if (!mbar_wait(tfree_bar, (tile & 1u) ^ 1u, abort_flag, p.status)) break;
-        const uint32_t acc = tmem + ((tile & 1u) ? acc1 : 0u);
-        int steps = p.k_steps;
+        if (!__all_sync(0xffffffffu, mbar_wait<kPair>(tfree_bar, (tile & 1u) ^ 1u, abort_flag,
+                                                      p.status)))
+          break;
+        const uint32_t acc = tmem + ((tile & 1u) ? kXAcc1 : 0u);
         for (int kb = 0; kb < p.KB; ++kb) {
-          if (!mbar_wait(full_bar(stage), phase, abort_flag, p.status)) {
+          if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, p.status))) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sA = base + stage * stage_bytes;
-          const uint64_t ad = sw128_kmajor_desc(sA), bd = sw128_kmajor_desc(sA + a_bytes);
-          const uint64_t sd = scales_desc(sA + a_bytes + b_bytes);
+          const uint32_t off = (stage * stage_bytes) >> 4;
+          const uint64_t ad = a0 + off, bd = b0 + off, sd = s0 + off;
           const uint32_t sfa = tmem + kXScaleCol + set * kXScaleSet, sfb = sfa + 8;
-          const int now = min(steps, kXK / 64);
+          const int now = p.k_steps - kb * kXSteps;  // MMAs up to the end of K
+          if (one) {
 #pragma unroll
-          for (int a = 0; a < kXStageAtoms; ++a) {
-            if (2 * a < now) {
-              tc_copy_scales(sfa + 4 * a, sd + a * (kXAtomBytes >> 4));
-              for (uint32_t i = 0; i < n_rb; ++i)
-                tc_copy_scales(sfb + 8 * a + 4 * i,
-                               sd + ((1 + i) * kSetBytes + a * kXAtomBytes) / 16);
+            for (int a = 0; a < kXStageAtoms; ++a) {  // past K's end too: zeros
+              tc_copy_scales<kPair>(sfa + 4 * a, sd + a * (kXAtomBytes >> 4));
+#pragma unroll
+              for (int i = 0; i < kXN / kXAtomRows; ++i)
+                tc_copy_scales<kPair>(sfb + 8 * a + 4 * i,
+                                      sd + ((1 + i) * kXSetBytes + a * kXAtomBytes) / 16);
             }
-          }
 #pragma unroll
-          for (int k = 0; k < kXK / 64; ++k)  // 32 bytes on in each 128-byte row
-            if (k < now)
-              tc_mma_mxf4(acc, ad + 2 * k, bd + 2 * k,
-                          idesc_mxf4(kXM, static_cast<uint32_t>(p.tile_n), 2u * (k & 1)),
-                          sfa + 4 * (k >> 1), sfb + 8 * (k >> 1), (kb | k) != 0 ? 1u : 0u);
-          steps -= now;
-          tc_commit(empty_bar(stage));
+            for (int k = 0; k < kXSteps; ++k)  // 32 bytes on in each 128-byte row
+              if (k == 0 || k < now)
+                tc_mma_mxf4<kPair>(acc, ad + 2 * k, bd + 2 * k, idesc_mxf4(kM, kXN, 2u * (k & 1)),
+                                   sfa + 4 * (k >> 1), sfb + 8 * (k >> 1),
+                                   k > 0 || kb > 0 ? 1u : 0u);
+          }
+          commit(empty_bar(stage));
+          if (kb == p.KB - 1) commit(tfull_bar);
           set ^= 1u;
           if (++stage == n_st) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (ok) tc_commit(tfull_bar);
       }
-      // Every MMA of this thread ends before TMEM is released, also where a role gave up.
-      volatile int no_abort = 0;
-      tc_commit(final_bar);
-      mbar_wait(final_bar, 0, &no_abort, p.status);
+      // Every MMA ends before TMEM is released, also where a role gave up.
+      commit(final_bar);
     }
+    mbar_wait(final_bar, 0, &no_abort, p.status);
   } else {
     const int ew = warp - 2;
     const int lanes0 = 32 * (warp & 3);  // the TMEM lanes this warp may read
     const uint32_t lane_addr = static_cast<uint32_t>(lanes0) << 16;
     const uint32_t stg = staging + ew * kXStagingWarp;
-    const int boxes = p.tile_n / kXBox;
     uint32_t tile = 0, obuf = 0;
-    for (int u = blockIdx.x; u < p.n_units; u += gridDim.x, ++tile) {
+    for (int u = first_unit; u < p.n_units; u += unit_stride, ++tile) {
       int m, n;
       mx_unit(p, u, m, n);
-      const int row0 = m * kXM + lanes0;
+      const int row0 = (kPair ? 2 * m + static_cast<int>(rank) : m) * kXM + lanes0;
       const int row = row0 + lane;
       const bool warp_on = row0 < p.T;
-      const int64_t col0 = static_cast<int64_t>(n) * p.tile_n;
-      const uint32_t src = tmem + lane_addr + ((tile & 1u) ? acc1 : 0u);
-      const bool ready = mbar_wait(tfull_bar, tile & 1u, abort_flag, p.status);
+      const int64_t col0 = static_cast<int64_t>(n) * kXN;
+      const uint32_t src = tmem + lane_addr + ((tile & 1u) ? kXAcc1 : 0u);
+      const bool ready = mbar_wait<kPair>(tfull_bar, tile & 1u, abort_flag, p.status);
       if (!__all_sync(0xffffffffu, ready)) break;
       tc_fence_after();
-      // the shared columns first: the last boxes of the first accumulator, the first
-      // of the second
-      const int first = (tile & 1u) ? 0 : boxes - shared_boxes;
-      if (shared_boxes == 0 || !warp_on) {
-        // nothing to hold on to: the accumulators are apart (the tile before has left
-        // this one's by its order), or no row is stored
+      auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tfree_bar);
-      }
-      if (!warp_on) continue;
-      for (int i = 0; i < boxes; ++i) {
-        const int b = first + i < boxes ? first + i : first + i - boxes;
-        const int64_t colb = col0 + b * kXBox;
-        float v[32];
-        tmem_ld32(src + b * kXBox, v);
-        if (shared_boxes > 0 && i == shared_boxes - 1) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(tfree_bar);
+        if (lane == 0) {
+          if constexpr (kPair)
+            mbar_arrive_remote(mapa_shared(tfree_bar, 0));
+          else
+            mbar_arrive(tfree_bar);
         }
-        if (colb >= p.V) continue;
-        const uint32_t obox = stg + obuf;
+      };
+      auto store = [&](int b, const uint32_t (&d)[32]) {
+        const int64_t colb = col0 + b * kXBox;
+        if (colb >= p.V) return;
         if (!p.tma_out) {
           uint32_t words[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) words[j] = bf16x2_of(v[2 * j], v[2 * j + 1]);
+          for (int j = 0; j < 16; ++j)
+            words[j] = bf16x2_of(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
           const int64_t left = p.V - colb;
           store_rows(stg, lane, words, p.out + static_cast<int64_t>(row0) * p.ld + colb, p.ld,
                      min(32, p.T - row0), static_cast<int>(min(static_cast<int64_t>(kXBox), left)));
-          continue;
+          return;
         }
         // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
+        const uint32_t obox = stg + obuf;
         obuf ^= kXStagingWarp / 2;
         if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
         __syncwarp();
-        stage_box_row(obox, lane, v);
+        stage_box_row(obox, lane, reinterpret_cast<const float*>(d));
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -482,32 +533,115 @@ __global__ void __launch_bounds__(kXLogitsThreads, 1)
             st_global_u16_if(o + e, static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1))),
                              p.v_tma + e < p.V);
         }
+      };
+      if (!warp_on) {  // no row of this warp's is stored
+        release();
+        continue;
+      }
+      // the shared columns first (the last boxes of the first accumulator, the first of
+      // the second): the next tile's MMAs wait for no more than these reads
+      const int first = (tile & 1u) ? 0 : kXBoxes - kXShared;
+      uint32_t d0[32], d1[32];
+      tmem_ld32_issue(src + first * kXBox, d0);
+      tmem_ld32_issue(src + (first + 1) * kXBox, d1);
+      tmem_ld_wait(d0);
+      tmem_ld_wait(d1);
+      release();
+      store(first, d0);
+      store(first + 1, d1);
+#pragma unroll 1
+      for (int i = kXShared; i < kXBoxes; ++i) {
+        const int b = (first + i) & (kXBoxes - 1);
+        tmem_ld32_issue(src + b * kXBox, d0);
+        tmem_ld_wait(d0);
+        store(b, d0);
       }
     }
     if (lane == 0) bulk_wait_group<0>();  // every output box of this warp has been written
   }
 
   tc_fence_before();
-  __syncthreads();
+  if constexpr (kPair) {
+    // Neither CTA leaves (or frees TMEM) while the other may still touch its barriers,
+    // shared memory or TMEM. In between CTA 0 waits (bounded) for every stage still in
+    // flight in either CTA: the stages before the last n_st of the CTA further ahead were
+    // consumed by MMAs. A stage that one CTA did not load gets that CTA's share settled
+    // here (CTA 0's arrive, or CTA 1's bytes as done).
+    __syncwarp();
+    cluster_sync();
+    if (rank == 0 && warp == 0 && lane == 0) {
+      const long long n0 = issued, n1 = static_cast<long long>(*peer_issued);
+      const long long hi = n0 > n1 ? n0 : n1;
+      volatile int no_abort = 0;
+      for (long long i = hi > n_st ? hi - n_st : 0; i < hi; ++i) {
+        const uint32_t s = static_cast<uint32_t>(i % n_st);
+        if (i < n0 && i >= n1)
+          mbar_complete_tx(full_bar(s), stage_bytes);
+        else if (i >= n0 && i < n1)
+          mbar_arrive_expect_tx(full_bar(s), stage_bytes);
+        mbar_wait(full_bar(s), static_cast<uint32_t>((i / n_st) & 1), &no_abort, p.status);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    if constexpr (kPair)
+      tmem_dealloc_pair(tmem, 512);
+    else
+      tmem_dealloc(tmem, 512);
   }
 }
 
-// The kernel's shared-memory attribute belongs to the device: set by its first call.
-cudaError_t mxfp4_setup() {
-  static std::atomic<bool> done[64];
+__global__ void __launch_bounds__(kXLogitsThreads, 1)
+    logits_mxfp4_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB,
+                        const __grid_constant__ CUtensorMap tmSA,
+                        const __grid_constant__ CUtensorMap tmSB,
+                        const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
+  logits_mxfp4_body<false>(tmA, tmB, tmSA, tmSB, tmC, p);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXLogitsThreads, 1)
+    logits_mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                             const __grid_constant__ CUtensorMap tmB,
+                             const __grid_constant__ CUtensorMap tmSA,
+                             const __grid_constant__ CUtensorMap tmSB,
+                             const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
+  logits_mxfp4_body<true>(tmA, tmB, tmSA, tmSB, tmC, p);
+}
+
+// The kernels' shared-memory attribute belongs to the device: set by its first call. *pairs:
+// the CTA pairs that the device holds at once.
+cudaError_t mxfp4_setup(int sms, int* pairs) {
+  static std::atomic<int> done[64];  // pairs + 1
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
-  e = cudaFuncSetAttribute(logits_mxfp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kXSmemBytes);
-  if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
-  return e;
+  int n = done[dev].load(std::memory_order_acquire);
+  if (n == 0) {
+    if ((e = cudaFuncSetAttribute(logits_mxfp4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  kXSmemBytes)) != cudaSuccess ||
+        (e = cudaFuncSetAttribute(logits_mxfp4_pair_kernel,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kXSmemBytes)) !=
+            cudaSuccess)
+      return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1));
+    cfg.blockDim = dim3(kXLogitsThreads);
+    cfg.dynamicSmemBytes = kXSmemBytes;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, logits_mxfp4_pair_kernel, &cfg)) != cudaSuccess)
+      return e;
+    n = (n < sms / 2 ? n : sms / 2) + 1;
+    done[dev].store(n, std::memory_order_release);
+  }
+  *pairs = n - 1;
+  return cudaSuccess;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -617,41 +751,49 @@ extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidde
   unsigned* status = nullptr;
   int rc = api_device(&sms, &status);
   if (rc != LMH_OK) return rc;
-  cudaError_t e = mxfp4_setup();
+  int pairs = 0;
+  cudaError_t e = mxfp4_setup(sms, &pairs);
   if (e != cudaSuccess) return launch_error(e, "4-bit logits");
-  const int64_t n_m = ceil_div(T, kXM);
+  // two row blocks or more go to pairs of CTAs
+  const bool pair = T > kXM && pairs > 0;
+  const int64_t n_m = ceil_div(T, pair ? 2 * kXM : kXM), n_n = ceil_div(V, kXN);
+  const int64_t k_words = ceil_div(H, kXAtomCols) * (kXAtomBytes / 4);
   Mxfp4Params p{};
-  p.tile_n = kXN;
-  const int64_t n_n = ceil_div(V, p.tile_n);
   p.T = static_cast<int>(T);
   p.V = static_cast<int>(V);
   p.KB = static_cast<int>(ceil_div(H, kXK));
-  p.k_atoms = static_cast<int>(ceil_div(H, kXAtomCols));
   p.k_steps = static_cast<int>(ceil_div(H, 64));
   p.n_m = static_cast<int>(n_m);
   p.n_n = static_cast<int>(n_n);
   p.n_units = static_cast<int>(n_m * n_n);
-  p.group_m = 16;
+  p.group_m = pair ? 8 : 16;
   p.a_rows = T < kXM ? static_cast<int>((T + 7) / 8 * 8) : kXM;
-  p.hs = hidden_scale;
-  p.ws = weight_scale;
   p.out = logits;
   p.ld = ld_logits;
   p.v_tma = static_cast<int>(V / 8 * 8);
   p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16) && p.v_tma > 0) ? 1 : 0;
   p.status = status;
-  CUtensorMap ta, tb, tc{};
+  CUtensorMap ta, tb, tsa, tsb, tc{};
   if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, p.v_tma, T, ld_logits * 2)) != LMH_OK)
     return rc;
-  if ((rc = api_make_tmap_u8(&ta, hidden_q, H / 2, T, H / 2, kXK / 2, p.a_rows)) != LMH_OK)
-    return rc;
-  if ((rc = api_make_tmap_u8(&tb, weight_q, H / 2, V, H / 2, kXK / 2, p.tile_n)) != LMH_OK)
+  if ((rc = api_make_tmap_u8(&ta, hidden_q, H / 2, T, H / 2, kXK / 2, p.a_rows)) != LMH_OK ||
+      (rc = api_make_tmap_u8(&tb, weight_q, H / 2, V, H / 2, kXK / 2, pair ? kXN / 2 : kXN)) !=
+          LMH_OK ||
+      (rc = api_make_tmap_scales(&tsa, hidden_scale, k_words, ceil_div(T, kXAtomRows),
+                                 kXSetBytes / 4, 1)) != LMH_OK ||
+      (rc = api_make_tmap_scales(&tsb, weight_scale, k_words, ceil_div(V, kXAtomRows),
+                                 kXSetBytes / 4, kXN / kXAtomRows)) != LMH_OK)
     return rc;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   {
     KernelTimer timer(K_LOGITS_MXFP4, st);
-    const int grid = p.n_units < sms ? p.n_units : sms;
-    logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tc, p);
+    if (pair) {
+      const int grid = 2 * (p.n_units < pairs ? p.n_units : pairs);
+      logits_mxfp4_pair_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, tc, p);
+    } else {
+      const int grid = p.n_units < sms ? p.n_units : sms;
+      logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, tc, p);
+    }
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
   }
