@@ -14,10 +14,12 @@
 // more tokens reach it than the list holds (equal logits), the n-th largest value is
 // found by bisection over the 16-bit keys, counting over the row.
 //
-// A row is taken by a cluster of CTAs whose number depends on V alone, each with its
-// slice; the first CTA merges their sums in order, and their lists.
+// A row is eight slices, and every thread of a CTA has its share of each. A cluster of 1
+// to 8 CTAs takes the row, as many as a short batch leaves SMs for; a thread's sums are
+// merged over the slices as a binary tree, the same one for any number of CTAs, and then
+// over the threads.
 //
-// Batch invariance: the split and the order of every sum depend on V alone.
+// Batch invariance: the slices and the order of every sum depend on V alone.
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -39,8 +41,11 @@ typedef unsigned long long u64;
 constexpr int kPThreads = 256;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPMaxTop = 128;   // most alternatives
-constexpr int kPMaxC = 4;       // most CTAs of a row
-constexpr int kPList = 1024;    // tokens of a CTA's list
+constexpr int kPSlices = 8;     // of a row; the most CTAs that share one
+constexpr int kPList = 512;     // tokens of a CTA's list
+constexpr int kPGroup = 4;      // vectors that a thread folds at once
+constexpr int kPDepth = 3;      // groups on their way to a thread
+constexpr int kPMinSlice = kPGroup * kPThreads;  // vectors of a slice, where the row has them
 static_assert(kPMaxTop <= kPThreads, "a thread's largest value for each alternative");
 constexpr float kPFloor = -200.f;  // 2^-200 is 0: what masked and far values are cut to
 
@@ -51,27 +56,30 @@ struct TopParams {
   const float* row_t;
   const int32_t* tokens;
   int n_tokens, n_top;
+  int64_t per;  // vectors of a slice: whole runs of 32
   float* out_logprob;
   float* out_entropy;
   int32_t* top_token;
   float* top_logprob;
 };
 
-// A CTA's sums, and the largest logit of its slice (-inf: all masked).
-struct SliceStat {
+// A slice's sums and its largest logit (-inf: all masked); stored whole by 16 bytes.
+struct alignas(16) SliceStat {
   float m, s, u, most;
 };
 
+template <int kC>
 struct TopShared {
   u64 list[kPList];
-  u64 merged[kPMaxC * kPMaxTop];  // CTA 0: every CTA's best, in order; 0 where it has none
-  SliceStat slice[kPMaxC];        // CTA 0
-  SliceStat warp[kPWarps];
-  uint16_t key[kPThreads];
-  uint16_t hit[kPThreads];
-  uint32_t count[kPWarps];
-  uint32_t bar;                   // the key that alternatives reach
+  u64 merged[kC][kPMaxTop];          // CTA 0: every CTA's best, in order,
+  int n_merged[kC];                  // and how many they are
   int n_hit, n_list;
+  SliceStat peer[kC > 1 ? kC - 1 : 1][kPThreads];  // CTA 0: the other CTAs' threads' sums
+  SliceStat warp[kPWarps];
+  uint16_t key[kPSlices / kC][kPThreads];  // a thread's largest value in each slice
+  uint16_t hit[kPThreads * kPSlices / kC];
+  uint32_t count[kPWarps];
+  uint32_t bar;                      // the key that alternatives reach
 };
 
 // 16 bits in the order of the values: 0 for a masked logit, and equal zeros.
@@ -91,6 +99,24 @@ __device__ __forceinline__ u64 entry_of(uint32_t key, int64_t index) {
 
 constexpr uint32_t kMasked2 = 0xff80ff80u;  // two -inf
 
+// 8 values at `off` bytes (even, below 16) into two aligned vectors.
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, uint32_t off) {
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8u) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4u) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  if (off & 2u) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Vector v (elements [8 v, 8 v + 8)) of a row at any address, -inf past its end. A row
 // that does not start on 16 bytes is read in the aligned 16 bytes that hold the vector,
 // but for its two ends, so that nothing outside the row is.
@@ -99,23 +125,8 @@ __device__ __forceinline__ uint4 load_vector(const uint16_t* row, int64_t V, int
   const uint16_t* at = row + 8 * v;
   if (kAligned && 8 * v + 8 <= V) return *reinterpret_cast<const uint4*>(at);
   if (!kAligned && v > 0 && 8 * v + 16 <= V) {
-    const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 15);
     const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(at) & ~uintptr_t{15});
-    const uint4 a = g[0], b = g[1];
-    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    if (off & 8u) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-    }
-    if (off & 4u) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-    }
-    if (off & 2u) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    return shifted(g[0], g[1], static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at) & 15));
   }
   uint32_t w[4] = {kMasked2, kMasked2, kMasked2, kMasked2};
 #pragma unroll
@@ -130,11 +141,12 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// Folds 32 values into the state; `most` keeps the largest value.
-__device__ __forceinline__ void fold32(OnlineStat& st, float& most, const uint4 (&w)[4], float c) {
+// Folds kV vectors into the state; `most` keeps the largest value.
+template <int kV>
+__device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w, float c) {
   __nv_bfloat162 m2 = bf2(kMasked2);  // a NaN is passed over
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
+  for (int k = 0; k < kV; ++k)
     m2 = __hmax2(m2, __hmax2(__hmax2(bf2(w[k].x), bf2(w[k].y)), __hmax2(bf2(w[k].z), bf2(w[k].w))));
   const float gmax = fmaxf(__low2float(m2), __high2float(m2));
   most = fmaxf(most, gmax);
@@ -145,7 +157,7 @@ __device__ __forceinline__ void fold32(OnlineStat& st, float& most, const uint4 
   f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
   const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-mn, -mn);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < kV; ++k) {
     const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -194,8 +206,8 @@ __device__ __noinline__ uint32_t count_from(const uint16_t* row, int64_t V, int6
 
 // The slice's first n tokens into sh.list, exactly n: those above the n-th largest key,
 // and of those that have it the first by index. At least n tokens are not masked.
-template <bool kAligned>
-__device__ __noinline__ void list_by_bisection(TopShared& sh, const uint16_t* row, int64_t V,
+template <bool kAligned, class Shared>
+__device__ __noinline__ void list_by_bisection(Shared& sh, const uint16_t* row, int64_t V,
                                                int64_t v0, int64_t v1, int n) {
   uint32_t lo = 1, hi = 0x10000u;  // count(lo) >= n > count(hi)
   while (hi - lo > 1) {
@@ -267,7 +279,8 @@ __device__ __forceinline__ float far_shift(float x, float most, float t) {
 
 // The sums of such a row: logits equal to the largest weigh 1. One CTA, in an order
 // fixed by V.
-__device__ __noinline__ SliceStat sums_of_extremes(TopShared& sh, const uint16_t* row, int64_t V,
+template <class Shared>
+__device__ __noinline__ SliceStat sums_of_extremes(Shared& sh, const uint16_t* row, int64_t V,
                                                    float t, float most) {
   float s = 0.f, u = 0.f;
   for (int64_t i = threadIdx.x; i < V; i += kPThreads) {
@@ -292,22 +305,92 @@ __device__ __noinline__ SliceStat sums_of_extremes(TopShared& sh, const uint16_t
   return r;
 }
 
+// Not the .aligned forms: a warp need not be whole where it comes out of a branch.
+__device__ __forceinline__ void row_arrive() {
+  asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+}
+__device__ __forceinline__ void row_wait() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 template <int kC>
 __device__ __forceinline__ uint32_t first_cta(const void* here) {
   return kC > 1 ? mapa_shared(smem_u32(here), 0u) : smem_u32(here);
 }
 
+// 16 bytes of a thread's own on their way to shared memory.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kN>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
+}
+
+// How the vectors of a row reach a thread: each copies its own, kPDepth groups of up to
+// four ahead, into shared memory that no other thread touches. A row that does not start
+// on 16 bytes takes two aligned vectors for each.
+template <bool kAligned>
+struct Ring {
+  static constexpr int kCopies = kAligned ? 1 : 2;
+  static constexpr int kBytes = kPDepth * kPGroup * kCopies * kPThreads * 16;
+  const uint16_t* row;
+  int64_t V;
+  uint32_t at;  // this thread's first slot
+  __device__ __forceinline__ uint32_t slot(int depth, int k, int copy) const {
+    return at + static_cast<uint32_t>(((depth * kPGroup + k) * kCopies + copy) * kPThreads * 16);
+  }
+  // A vector whose copies would reach outside the row: read element by element.
+  __device__ __forceinline__ bool edge(int64_t v) const {
+    return kAligned ? 8 * v + 8 > V : v == 0 || 8 * v + 16 > V;
+  }
+  __device__ __forceinline__ void fetch(int depth, int k, int64_t v) const {
+    if (edge(v)) {
+      const uint4 w = load_vector<kAligned>(row, V, v);
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(depth, k, 0)), "r"(w.x),
+                   "r"(w.y), "r"(w.z), "r"(w.w)
+                   : "memory");
+      return;
+    }
+    const uint16_t* from = row + 8 * v;
+    if constexpr (!kAligned)
+      from = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t{15});
+#pragma unroll
+    for (int c = 0; c < kCopies; ++c) copy16_async(slot(depth, k, c), from + 8 * c);
+  }
+  __device__ __forceinline__ uint4 take(int depth, int k, int64_t v) const {
+    const uint4 a = ld_shared_v4(slot(depth, k, 0));
+    if constexpr (kAligned) return a;
+    if (edge(v)) return a;
+    return shifted(a, ld_shared_v4(slot(depth, k, 1)),
+                   static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15));
+  }
+};
+
+// Place `groups` groups on, through slices of `per` vectors.
+struct Place {
+  int slice, group;
+  __device__ __forceinline__ void next(int groups) {
+    if (++group == groups) {
+      group = 0;
+      ++slice;
+    }
+  }
+};
+
 template <int kC, bool kAligned>
-__global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopParams p) {
-  __shared__ __align__(16) TopShared sh;
+__global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopParams p) {
+  extern __shared__ __align__(16) uint8_t ring_smem[];
+  __shared__ __align__(16) TopShared<kC> sh;
+  constexpr int kMine = kPSlices / kC;  // slices of this CTA
   const int64_t row = blockIdx.x / kC;
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const uint16_t* x = p.logits + row * p.ld;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // this CTA's vectors: whole runs of 32, but for the row's end
-  const int64_t n_vec = (p.V + 7) / 8;
-  const int64_t per = ((n_vec + kC - 1) / kC + 31) / 32 * 32;
-  const int64_t v0 = min(n_vec, per * rank), v1 = min(n_vec, v0 + per);
+  const int64_t n_vec = (p.V + 7) / 8, per = p.per;
+  const int groups = static_cast<int>((per + kPGroup * kPThreads - 1) / (kPGroup * kPThreads));
+  const int64_t first = per * (rank * kMine);  // this CTA's vectors
 
   float t = p.row_t ? p.row_t[row] : p.temperature;
   if (t == 0.f) t = 1.f;
@@ -315,20 +398,183 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   if (!valid_t) t = 1.f;
   const float c = __fdiv_rn(kLog2e, t);
   if (threadIdx.x == 0) sh.n_hit = sh.n_list = 0;
+  if (kC > 1) row_arrive();  // this CTA has begun: see the wait below
 
+  const Ring<kAligned> ring{x, p.V, smem_u32(ring_smem) + threadIdx.x * 16};
+  auto fetch = [&](const Place& at, int depth) {
+    const int64_t end = min(n_vec, first + per * (at.slice + 1));
+    const int64_t v = first + per * at.slice + at.group * (kPGroup * kPThreads) + threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < kPGroup; ++k)
+      if (at.slice < kMine && v + k * kPThreads < end) ring.fetch(depth, k, v + k * kPThreads);
+    copies_commit();  // an empty one too: the groups are counted
+  };
+  Place ahead{0, 0};
+#pragma unroll
+  for (int d = 0; d < kPDepth - 1; ++d, ahead.next(groups)) fetch(ahead, d);
+
+  // The slices' sums as a binary tree: pairs, fours, all eight.
+  const SliceStat none{-INFINITY, 0.f, 0.f, -INFINITY};
+  SliceStat one = none, two = none, four = none, mine = none;
   OnlineStat st = stat_empty();
   float most = -INFINITY;
-  for (int64_t v = v0 + threadIdx.x; v < v1; v += 4 * kPThreads) {
-    uint4 w[4];
+  int depth = 0;
+#pragma unroll 1
+  for (Place at{0, 0}; at.slice < kMine;) {
+    fetch(ahead, depth == 0 ? kPDepth - 1 : depth - 1);
+    ahead.next(groups);
+    copies_wait<kPDepth - 1>();
+    const int64_t end = min(n_vec, first + per * (at.slice + 1));
+    const int64_t v0 = first + per * at.slice + at.group * (kPGroup * kPThreads);
+    const int64_t v = v0 + threadIdx.x;
+    uint4 w[kPGroup];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kPGroup; ++k) {
       w[k] = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
-      if (v + k * kPThreads < v1) w[k] = load_vector<kAligned>(x, p.V, v + k * kPThreads);
+      if (v + k * kPThreads < end) w[k] = ring.take(depth, k, v + k * kPThreads);
     }
-    fold32(st, most, w, c);
+    if (end - v0 > 3 * kPThreads)
+      fold<4>(st, most, w, c);
+    else if (end - v0 > 2 * kPThreads)
+      fold<3>(st, most, w, c);
+    else if (end - v0 > kPThreads)
+      fold<2>(st, most, w, c);
+    else if (end - v0 > 0)
+      fold<1>(st, most, w, c);
+    if (++depth == kPDepth) depth = 0;
+    const int i = at.slice;
+    at.next(groups);
+    if (at.group != 0) continue;
+    // the slice's end
+    sh.key[i][threadIdx.x] = static_cast<uint16_t>(order_key(__float_as_uint(most) >> 16));
+    mine = SliceStat{st.m, st.s, st.u, most};
+    st = stat_empty();
+    most = -INFINITY;
+    if (!(i & 1)) {
+      one = mine;
+      continue;
+    }
+    merge_slice(one, mine);
+    mine = one;
+    if (!(i & 2)) {
+      two = mine;
+      continue;
+    }
+    merge_slice(two, mine);
+    mine = two;
+    if (!(i & 4)) {
+      four = mine;
+      continue;
+    }
+    merge_slice(four, mine);
+    mine = four;
   }
-  sh.key[threadIdx.x] = static_cast<uint16_t>(order_key(__float_as_uint(most) >> 16));
-  SliceStat mine{st.m, st.s, st.u, most};
+  // The first CTA's shared memory may be written once it runs; a CTA without a slice of
+  // its own is here before that.
+  if (kC > 1) row_wait();
+  if (kC > 1 && rank > 0) {
+    const uint32_t at = first_cta<kC>(&sh.peer[rank > 0 ? rank - 1 : 0][threadIdx.x]);
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(mine.m),
+                 "f"(mine.s), "f"(mine.u), "f"(mine.most)
+                 : "memory");
+  }
+  __syncthreads();
+
+  const int n = p.n_top;
+  if (warp == 0 && n > 0) {
+    // the n-th largest of the threads' keys (1 where fewer are not masked), two bits at
+    // a time: the counts that reach three thresholds, in one word's three parts
+    uint32_t k[kPThreads / 32];
+#pragma unroll
+    for (int i = 0; i < kPThreads / 32; ++i) {
+      k[i] = sh.key[0][lane + 32 * i];
+#pragma unroll
+      for (int j = 1; j < kMine; ++j) k[i] = max(k[i], static_cast<uint32_t>(sh.key[j][lane + 32 * i]));
+    }
+    uint32_t bar = 0;
+#pragma unroll 1
+    for (int sft = 14; sft >= 0; sft -= 2) {
+      uint32_t reach = 0;
+#pragma unroll
+      for (int i = 0; i < kPThreads / 32; ++i)
+#pragma unroll
+        for (uint32_t q = 1; q <= 3; ++q)
+          reach += k[i] >= (bar | (q << sft)) ? 1u << (10 * (q - 1)) : 0u;
+      reach = __reduce_add_sync(0xffffffffu, reach);
+      const uint32_t want = static_cast<uint32_t>(n);
+      const uint32_t q = ((reach & 1023u) >= want) + ((reach >> 10 & 1023u) >= want) +
+                         ((reach >> 20) >= want);
+      bar |= q << sft;
+    }
+    if (lane == 0) sh.bar = max(bar, 1u);
+  }
+  __syncthreads();
+
+  if (n > 0) {
+    const uint32_t bar = sh.bar;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (sh.key[i][threadIdx.x] >= bar)
+        sh.hit[atomicAdd(&sh.n_hit, 1)] = static_cast<uint16_t>(i * kPThreads + threadIdx.x);
+    __syncthreads();
+    const int share = static_cast<int>((per + kPThreads - 1) / kPThreads);
+    const int64_t looks = static_cast<int64_t>(sh.n_hit) * share;
+    for (int64_t i = threadIdx.x; i < looks; i += kPThreads) {
+      const int h = static_cast<int>(static_cast<uint64_t>(i) / static_cast<uint32_t>(share));
+      const int j = static_cast<int>(i - static_cast<int64_t>(h) * share);
+      const int who = sh.hit[h];
+      const int64_t from = first + per * (who / kPThreads);
+      const int64_t v = from + who % kPThreads + static_cast<int64_t>(j) * kPThreads;
+      if (v >= min(n_vec, from + per)) continue;
+      const uint4 w = load_vector<kAligned>(x, p.V, v);
+      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+      const __nv_bfloat162 m2 = __hmax2(__hmax2(bf2(w.x), bf2(w.y)), __hmax2(bf2(w.z), bf2(w.w)));
+      const float m = fmaxf(__low2float(m2), __high2float(m2));
+      if (order_key(__float_as_uint(m) >> 16) < bar) continue;
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t word = e < 4 ? (e < 2 ? ws[0] : ws[1]) : (e < 6 ? ws[2] : ws[3]);
+        const uint32_t k = order_key(word >> (16 * (e & 1)) & 0xffffu);
+        if (k >= bar) {
+          const int at = atomicAdd(&sh.n_list, 1);
+          if (at < kPList) sh.list[at] = entry_of(k, 8 * v + e);
+        }
+      }
+    }
+    __syncthreads();
+    if (sh.n_list > kPList)
+      list_by_bisection<kAligned>(sh, x, p.V, min(n_vec, first), min(n_vec, first + per * kMine), n);
+    const int found = sh.n_list;
+    // the first n of them, in order, to the first CTA
+    const uint32_t to = first_cta<kC>(&sh.merged[rank][0]);
+    for (int i = threadIdx.x; i < found; i += kPThreads) {
+      const u64 me = sh.list[i];
+      int r = 0;
+#pragma unroll 4
+      for (int j = 0; j < found; ++j) r += sh.list[j] > me;
+      if (r < n)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8u * r), "l"(me) : "memory");
+    }
+    if (threadIdx.x == 0)
+      st_shared_cluster_u32(first_cta<kC>(&sh.n_merged[rank]), static_cast<uint32_t>(min(found, n)));
+  }
+  if constexpr (kC > 1) {
+    __syncwarp();
+    row_arrive();
+    row_wait();
+    if (rank != 0) return;
+    // the rest of the tree: pairs of CTAs, pairs of pairs
+    SliceStat part[kC];
+    part[0] = mine;
+#pragma unroll
+    for (int k = 1; k < kC; ++k) part[k] = sh.peer[k - 1][threadIdx.x];
+#pragma unroll
+    for (int by = 1; by < kC; by *= 2)
+#pragma unroll
+      for (int k = 0; k < kC; k += 2 * by) merge_slice(part[k], part[k + by]);
+    mine = part[0];
+  }
+  // then the threads: within each warp, and the warps as a tree
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     SliceStat o;
@@ -340,93 +586,22 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   }
   if (lane == 0) sh.warp[warp] = mine;
   __syncthreads();
+  SliceStat part[kPWarps];
+#pragma unroll
+  for (int w = 0; w < kPWarps; ++w) part[w] = sh.warp[w];
+#pragma unroll
+  for (int by = 1; by < kPWarps; by *= 2)
+#pragma unroll
+    for (int w = 0; w < kPWarps; w += 2 * by) merge_slice(part[w], part[w + by]);
+  SliceStat all = part[0];
 
-  const int n = p.n_top;
-  if (warp == 1 && lane == 0) {
-    SliceStat r = sh.warp[0];
-    for (int w = 1; w < kPWarps; ++w) merge_slice(r, sh.warp[w]);
-    const uint32_t at = first_cta<kC>(&sh.slice[rank]);
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(r.m), "f"(r.s),
-                 "f"(r.u), "f"(r.most)
-                 : "memory");
-  }
-  if (warp == 0 && n > 0) {
-    // the n-th largest of the threads' keys, by bisection (1 where fewer are not masked)
-    uint32_t k[kPThreads / 32];
-#pragma unroll
-    for (int i = 0; i < kPThreads / 32; ++i) k[i] = sh.key[lane + 32 * i];
-    uint32_t bar = 0;
-#pragma unroll 1
-    for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1) {
-      uint32_t reach = 0;
-#pragma unroll
-      for (int i = 0; i < kPThreads / 32; ++i) reach += k[i] >= (bar | bit);
-      if (__reduce_add_sync(0xffffffffu, reach) >= static_cast<uint32_t>(n)) bar |= bit;
-    }
-    bar = max(bar, 1u);
-    int base = 0;
-#pragma unroll
-    for (int i = 0; i < kPThreads / 32; ++i) {
-      const uint32_t on = __ballot_sync(0xffffffffu, k[i] >= bar);
-      if (k[i] >= bar)
-        sh.hit[base + __popc(on & ((1u << lane) - 1u))] = static_cast<uint16_t>(lane + 32 * i);
-      base += __popc(on);
-    }
-    if (lane == 0) {
-      sh.bar = bar;
-      sh.n_hit = base;
-    }
-  }
-  __syncthreads();
-
-  if (n > 0) {
-    const uint32_t bar = sh.bar;
-    const int64_t share = (v1 - v0 + kPThreads - 1) / kPThreads;
-    const int64_t looks = share * sh.n_hit;
-    for (int64_t i = threadIdx.x; i < looks; i += kPThreads) {
-      const int64_t v = v0 + sh.hit[i / share] + (i % share) * kPThreads;
-      if (v >= v1) continue;
-      const uint4 w = load_vector<kAligned>(x, p.V, v);
-      const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t k = order_key(ws[e / 2] >> (16 * (e & 1)) & 0xffffu);
-        if (k >= bar) {
-          const int at = atomicAdd(&sh.n_list, 1);
-          if (at < kPList) sh.list[at] = entry_of(k, 8 * v + e);
-        }
-      }
-    }
-    __syncthreads();
-    if (sh.n_list > kPList) list_by_bisection<kAligned>(sh, x, p.V, v0, v1, n);
-    const int found = sh.n_list;
-    // the first n of them, in order, to the first CTA
-    const uint32_t to = first_cta<kC>(&sh.merged[rank * kPMaxTop]);
-    for (int i = threadIdx.x; i < found; i += kPThreads) {
-      const u64 me = sh.list[i];
-      int r = 0;
-      for (int j = 0; j < found; ++j) r += sh.list[j] > me;
-      if (r < n)
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8u * r), "l"(me) : "memory");
-    }
-    for (int i = found + threadIdx.x; i < n; i += kPThreads)
-      asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(to + 8u * i), "l"(u64{0}) : "memory");
-  }
-  if (kC > 1) {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-    if (rank != 0) return;
-  } else {
-    __syncthreads();
-  }
-
-  SliceStat all = sh.slice[0];
-  for (int k = 1; k < kC; ++k) merge_slice(all, sh.slice[k]);
   // The largest y itself is shifted by its product's rounding, up to 2^-4 at 2^20; past
   // that (or where the largest logit is +inf) the row is summed again.
   const bool extreme = all.most > -INFINITY && !(fabsf(__fmul_rn(all.most, c)) <= 0x1p20f);
-  if (extreme) all = sums_of_extremes(sh, x, p.V, t, all.most);
+  if (extreme) {
+    __syncthreads();
+    all = sums_of_extremes(sh, x, p.V, t, all.most);
+  }
   const bool nothing = !(all.most > -INFINITY);
   const float l2s = log2f(all.s);
   const float bad = __int_as_float(0x7fffffff);
@@ -438,33 +613,52 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
       return __fsub_rn(far_shift(v, all.most, t), __fmul_rn(kLn2, l2s));
     return __fmul_rn(kLn2, __fsub_rn(d, l2s));
   };
-  if (threadIdx.x == 0 && p.out_entropy)
+  // the last threads take the tokens, the first ones the lists
+  const int back = kPThreads - 1 - static_cast<int>(threadIdx.x);
+  if (back == 0 && p.out_entropy)
     p.out_entropy[row] = !valid_t ? bad
                          : nothing ? 0.f
                                    : __fmul_rn(kLn2, __fsub_rn(l2s, __fdiv_rn(all.u, all.s)));
-  for (int i = threadIdx.x; i < p.n_tokens; i += kPThreads) {
+  for (int i = back; i < p.n_tokens; i += kPThreads) {
     const int32_t id = p.tokens[row * p.n_tokens + i];
     float lp = valid_t ? 0.f : bad;
     if (id >= 0 && id < p.V) lp = logprob(__uint_as_float(static_cast<uint32_t>(x[id]) << 16));
     p.out_logprob[row * p.n_tokens + i] = lp;
   }
-  for (int i = threadIdx.x; i < kC * n; i += kPThreads) {
-    const u64 me = sh.merged[i / n * kPMaxTop + i % n];
-    int r = 0, total = 0;
-    for (int k = 0; k < kC; ++k) {
-      for (int j = 0; j < n; ++j) {
-        const u64 o = sh.merged[k * kPMaxTop + j];
-        r += o > me;
-        total += o != 0;
-      }
-    }
-    if (me != 0 && r < n && valid_t) {
-      p.top_token[row * n + r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(me));
-      p.top_logprob[row * n + r] = logprob(value_of_key(static_cast<uint32_t>(me >> 32)));
-    }
-    if (i < n && (i >= total || !valid_t)) {
+  if (n == 0) return;
+  int total = 0;
+#pragma unroll
+  for (int k = 0; k < kC; ++k) total += sh.n_merged[k];
+  if (!valid_t) total = 0;
+  for (int i = threadIdx.x; i < n; i += kPThreads) {  // places that no token takes
+    if (i >= total) {
       p.top_token[row * n + i] = -1;
       p.top_logprob[row * n + i] = valid_t ? -INFINITY : bad;
+    }
+  }
+  for (int i = threadIdx.x; i < kC * kPMaxTop; i += kPThreads) {
+    const int own = i / kPMaxTop, place = i % kPMaxTop;  // a list and the place in it
+    if (!valid_t || place >= sh.n_merged[own]) continue;
+    const u64 me = sh.merged[own][place];
+    int r = place;  // and how many of each other list come before
+    if constexpr (kC > 1) {
+      int lo[kC], len[kC];
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        lo[k] = 0;
+        len[k] = k == own ? 0 : sh.n_merged[k];
+      }
+      for (int step = kPMaxTop; step > 0; step >>= 1) {
+#pragma unroll
+        for (int k = 0; k < kC; ++k)
+          if (lo[k] + step <= len[k] && sh.merged[k][lo[k] + step - 1] > me) lo[k] += step;
+      }
+#pragma unroll
+      for (int k = 0; k < kC; ++k) r += lo[k];
+    }
+    if (r < n) {
+      p.top_token[row * n + r] = static_cast<int32_t>(0xffffffffu - static_cast<uint32_t>(me));
+      p.top_logprob[row * n + r] = logprob(value_of_key(static_cast<uint32_t>(me >> 32)));
     }
   }
 }
@@ -473,9 +667,27 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 template <int kC, bool kAligned>
 cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
+  // The kernel's shared-memory attribute belongs to the device: set by its first call.
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(top_logprobs_kernel<kC, kAligned>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<kAligned>::kBytes);
+    if (e != cudaSuccess) return e;
+    done[dev].store(true, std::memory_order_release);
+  }
+  if constexpr (kC == 1) {
+    top_logprobs_kernel<kC, kAligned>
+        <<<static_cast<unsigned>(p.T), kPThreads, Ring<kAligned>::kBytes, st>>>(p);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
   cfg.blockDim = dim3(kPThreads);
+  cfg.dynamicSmemBytes = Ring<kAligned>::kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -487,11 +699,19 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, top_logprobs_kernel<kC, kAligned>, p);
 }
 
+// CTAs of a row: as many as leave each an SM's share of the batch, and no more than
+// there are slices with something in them.
 template <bool kAligned>
-cudaError_t launch_by_vocabulary(const TopParams& p, cudaStream_t st) {
-  if (p.V > 65536) return launch_top<4, kAligned>(p, st);
-  if (p.V > 16384) return launch_top<2, kAligned>(p, st);
-  return launch_top<1, kAligned>(p, st);
+cudaError_t launch_by_rows(const TopParams& p, int sms, cudaStream_t st) {
+  int most = p.T * 8 <= 2 * sms ? 8 : p.T * 4 <= 2 * sms ? 4 : p.T * 2 <= 4 * sms ? 2 : 1;
+  const int64_t used = ((p.V + 7) / 8 + p.per - 1) / p.per;
+  while (most > 1 && most / 2 >= used) most /= 2;
+  switch (most) {
+    case 8: return launch_top<8, kAligned>(p, st);
+    case 4: return launch_top<4, kAligned>(p, st);
+    case 2: return launch_top<2, kAligned>(p, st);
+    default: return launch_top<1, kAligned>(p, st);
+  }
 }
 
 }  // namespace
@@ -535,6 +755,8 @@ extern "C" int lmhead_top_logprobs(const uint16_t* logits, int64_t T, int64_t V,
   p.temperature = temperature;
   p.row_t = row_temperature;
   p.tokens = tokens;
+  p.per = ((V + 7) / 8 + kPSlices - 1) / kPSlices;
+  p.per = (p.per > kPMinSlice ? p.per + 31 : kPMinSlice) / 32 * 32;
   p.n_tokens = static_cast<int>(n_tokens);
   p.n_top = static_cast<int>(n_top);
   p.out_logprob = out_logprob;
@@ -547,7 +769,7 @@ extern "C" int lmhead_top_logprobs(const uint16_t* logits, int64_t T, int64_t V,
     KernelTimer timer(K_TOP, st);
     // rows that all start on 16 bytes
     const bool aligned = !misaligned(logits, 16) && (ld_logits % 8 == 0 || T == 1);
-    e = aligned ? launch_by_vocabulary<true>(p, st) : launch_by_vocabulary<false>(p, st);
+    e = aligned ? launch_by_rows<true>(p, sms, st) : launch_by_rows<false>(p, sms, st);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) {
