@@ -56,7 +56,7 @@ struct TopParams {
   const float* row_t;
   const int32_t* tokens;
   int n_tokens, n_top;
-  int64_t per;  // vectors of a slice: whole runs of 32
+  int per;  // vectors of a slice: whole runs of 32
   float* out_logprob;
   float* out_entropy;
   int32_t* top_token;
@@ -76,6 +76,7 @@ struct TopShared {
   int n_hit, n_list;
   SliceStat peer[kC > 1 ? kC - 1 : 1][kPThreads];  // CTA 0: the other CTAs' threads' sums
   SliceStat warp[kPWarps];
+  float2 top[kPWarps];               // the warps' largest y and logit
   uint16_t key[kPSlices / kC][kPThreads];  // a thread's largest value in each slice
   uint16_t hit[kPThreads * kPSlices / kC];
   uint32_t count[kPWarps];
@@ -141,14 +142,30 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// Folds kV vectors into the state; `most` keeps the largest value.
+// One pair of values into the packed sums: e = 2^d, and e * d.
+__device__ __forceinline__ void add_pair(float da, float db, f32x2& s2, f32x2& u2) {
+  const f32x2 e2 = f2_pack(ex2(da), ex2(db));
+  s2 = f2_add(s2, e2);
+  u2 = f2_fma(e2, f2_pack(da, db), u2);
+}
+
+// Folds kV vectors into the state; `most` keeps the largest value. Where a value is
+// masked, or so far below that its shift leaves fp32, the shifts are cut to kPFloor.
 template <int kV>
 __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w, float c) {
-  __nv_bfloat162 m2 = bf2(kMasked2);  // a NaN is passed over
+  __nv_bfloat162 hi = bf2(w[0].x), lo = hi;  // the largest passes over a NaN, the smallest keeps it
 #pragma unroll
-  for (int k = 0; k < kV; ++k)
-    m2 = __hmax2(m2, __hmax2(__hmax2(bf2(w[k].x), bf2(w[k].y)), __hmax2(bf2(w[k].z), bf2(w[k].w))));
-  const float gmax = fmaxf(__low2float(m2), __high2float(m2));
+  for (int k = 0; k < kV; ++k) {
+    const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      hi = __hmax2(hi, bf2(ws[q]));
+      lo = __hmin2_nan(lo, bf2(ws[q]));
+    }
+  }
+  // a NaN of two NaN is a masked value
+  const float gmax = fmaxf(fmaxf(__low2float(hi), __high2float(hi)), -INFINITY);
+  const float l0 = __low2float(lo), l1 = __high2float(lo);
   most = fmaxf(most, gmax);
   // never -inf, from which a finite x * c would be infinitely far
   const float mn = fmaxf(fmaxf(st.m, __fmul_rn(gmax, c)), -3.402823466e38f);
@@ -156,18 +173,27 @@ __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w
   const float a = ex2(d0);
   f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
   const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-mn, -mn);
+  if (__fmaf_rn(l0, c, -mn) > -1e30f && __fmaf_rn(l1, c, -mn) > -1e30f) {
 #pragma unroll
-  for (int k = 0; k < kV; ++k) {
-    const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    for (int k = 0; k < kV; ++k) {
+      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      float da, db;
-      f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
-      da = fmaxf(da, kPFloor);  // a NaN (a masked value) too
-      db = fmaxf(db, kPFloor);
-      const f32x2 e2 = f2_pack(ex2(da), ex2(db));
-      s2 = f2_add(s2, e2);
-      u2 = f2_fma(e2, f2_pack(da, db), u2);
+      for (int q = 0; q < 4; ++q) {
+        float da, db;
+        f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
+        add_pair(da, db, s2, u2);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kV; ++k) {
+      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float da, db;
+        f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
+        add_pair(fmaxf(da, kPFloor), fmaxf(db, kPFloor), s2, u2);  // a NaN too
+      }
     }
   }
   float s0, s1, u0, u1;
@@ -178,10 +204,24 @@ __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w
   st.m = mn;
 }
 
-__device__ __forceinline__ void merge_slice(SliceStat& a, const SliceStat& b) {
-  OnlineStat x{a.m, a.s, a.u, 0.f};
-  stat_merge(x, OnlineStat{b.m, b.s, b.u, 0.f});
-  a = SliceStat{x.m, x.s, x.u, fmaxf(a.most, b.most)};
+// Scales a slice's sums to the maximum m (its own or a larger one); an empty slice's
+// stay zero.
+__device__ __forceinline__ void rescale(SliceStat& a, float m) {
+  const float d = fmaxf(__fsub_rn(a.m, m), kPFloor);
+  const float e = ex2(d);
+  a.u = __fmul_rn(e, __fmaf_rn(a.s, d, a.u));
+  a.s = __fmul_rn(a.s, e);
+  a.m = m;
+}
+
+// a <- a (+) b. An empty side leaves the other's bits.
+__device__ __forceinline__ void merge_slice(SliceStat& a, SliceStat b) {
+  const float m = fmaxf(a.m, b.m);
+  rescale(a, m);
+  rescale(b, m);
+  a.s = __fadd_rn(a.s, b.s);
+  a.u = __fadd_rn(a.u, b.u);
+  a.most = fmaxf(a.most, b.most);
 }
 
 // How many values of the slice have a key of at least k, in every thread.
@@ -368,17 +408,6 @@ struct Ring {
   }
 };
 
-// Place `groups` groups on, through slices of `per` vectors.
-struct Place {
-  int slice, group;
-  __device__ __forceinline__ void next(int groups) {
-    if (++group == groups) {
-      group = 0;
-      ++slice;
-    }
-  }
-};
-
 template <int kC, bool kAligned>
 __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopParams p) {
   extern __shared__ __align__(16) uint8_t ring_smem[];
@@ -388,9 +417,13 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
   const int rank = kC > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const uint16_t* x = p.logits + row * p.ld;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t n_vec = (p.V + 7) / 8, per = p.per;
-  const int groups = static_cast<int>((per + kPGroup * kPThreads - 1) / (kPGroup * kPThreads));
-  const int64_t first = per * (rank * kMine);  // this CTA's vectors
+  // This CTA's slices [0, slices) with something in them, of `per` vectors but the last;
+  // vectors are counted from the first slice's first.
+  constexpr int kStep = kPGroup * kPThreads;
+  const int n_vec = static_cast<int>((p.V + 7) / 8), per = p.per;
+  const int first = static_cast<int>(min(static_cast<int64_t>(n_vec), static_cast<int64_t>(per) * (rank * kMine)));
+  const int n_mine = static_cast<int>(min(static_cast<int64_t>(n_vec - first), static_cast<int64_t>(per) * kMine));
+  const int slices = (n_mine + per - 1) / per;
 
   float t = p.row_t ? p.row_t[row] : p.temperature;
   if (t == 0.f) t = 1.f;
@@ -401,71 +434,84 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
   if (kC > 1) row_arrive();  // this CTA has begun: see the wait below
 
   const Ring<kAligned> ring{x, p.V, smem_u32(ring_smem) + threadIdx.x * 16};
-  auto fetch = [&](const Place& at, int depth) {
-    const int64_t end = min(n_vec, first + per * (at.slice + 1));
-    const int64_t v = first + per * at.slice + at.group * (kPGroup * kPThreads) + threadIdx.x;
+  int ahead = 0, ahead_end = min(per, n_mine);  // the next group to fetch, its slice's end
+  auto fetch = [&](int depth) {
+    const int v = ahead + static_cast<int>(threadIdx.x);
 #pragma unroll
     for (int k = 0; k < kPGroup; ++k)
-      if (at.slice < kMine && v + k * kPThreads < end) ring.fetch(depth, k, v + k * kPThreads);
+      if (v + k * kPThreads < ahead_end)
+        ring.fetch(depth, k, static_cast<int64_t>(first) + v + k * kPThreads);
     copies_commit();  // an empty one too: the groups are counted
+    ahead += kStep;
+    if (ahead >= ahead_end) {
+      ahead = ahead_end;
+      ahead_end = min(ahead_end + per, n_mine);
+    }
   };
-  Place ahead{0, 0};
 #pragma unroll
-  for (int d = 0; d < kPDepth - 1; ++d, ahead.next(groups)) fetch(ahead, d);
+  for (int d = 0; d < kPDepth - 1; ++d) fetch(d);
 
-  // The slices' sums as a binary tree: pairs, fours, all eight.
+  // The slices' sums as a binary tree: pairs, fours, all eight. What is missing at the
+  // end is empty, and leaves the rest as it is.
   const SliceStat none{-INFINITY, 0.f, 0.f, -INFINITY};
   SliceStat one = none, two = none, four = none, mine = none;
-  OnlineStat st = stat_empty();
-  float most = -INFINITY;
-  int depth = 0;
+  uint32_t top_key = 0;  // of this thread's values
+  int depth = 0, v0 = 0;
 #pragma unroll 1
-  for (Place at{0, 0}; at.slice < kMine;) {
-    fetch(ahead, depth == 0 ? kPDepth - 1 : depth - 1);
-    ahead.next(groups);
-    copies_wait<kPDepth - 1>();
-    const int64_t end = min(n_vec, first + per * (at.slice + 1));
-    const int64_t v0 = first + per * at.slice + at.group * (kPGroup * kPThreads);
-    const int64_t v = v0 + threadIdx.x;
-    uint4 w[kPGroup];
+  for (int i = 0; i < slices; ++i) {
+    const int end = min((i + 1) * per, n_mine);
+    OnlineStat st = stat_empty();
+    float most = -INFINITY;
+#pragma unroll 1
+    for (; v0 < end; v0 += kStep) {
+      fetch(depth == 0 ? kPDepth - 1 : depth - 1);
+      copies_wait<kPDepth - 1>();
+      const int v = v0 + static_cast<int>(threadIdx.x);
+      uint4 w[kPGroup];
 #pragma unroll
-    for (int k = 0; k < kPGroup; ++k) {
-      w[k] = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
-      if (v + k * kPThreads < end) w[k] = ring.take(depth, k, v + k * kPThreads);
+      for (int k = 0; k < kPGroup; ++k) {
+        w[k] = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
+        if (v + k * kPThreads < end)
+          w[k] = ring.take(depth, k, static_cast<int64_t>(first) + v + k * kPThreads);
+      }
+      if (end - v0 > 3 * kPThreads)
+        fold<4>(st, most, w, c);
+      else if (end - v0 > 2 * kPThreads)
+        fold<3>(st, most, w, c);
+      else if (end - v0 > kPThreads)
+        fold<2>(st, most, w, c);
+      else
+        fold<1>(st, most, w, c);
+      if (++depth == kPDepth) depth = 0;
     }
-    if (end - v0 > 3 * kPThreads)
-      fold<4>(st, most, w, c);
-    else if (end - v0 > 2 * kPThreads)
-      fold<3>(st, most, w, c);
-    else if (end - v0 > kPThreads)
-      fold<2>(st, most, w, c);
-    else if (end - v0 > 0)
-      fold<1>(st, most, w, c);
-    if (++depth == kPDepth) depth = 0;
-    const int i = at.slice;
-    at.next(groups);
-    if (at.group != 0) continue;
-    // the slice's end
-    sh.key[i][threadIdx.x] = static_cast<uint16_t>(order_key(__float_as_uint(most) >> 16));
+    v0 = end;
+    const uint32_t key = order_key(__float_as_uint(most) >> 16);
+    sh.key[i][threadIdx.x] = static_cast<uint16_t>(key);
+    top_key = max(top_key, key);
     mine = SliceStat{st.m, st.s, st.u, most};
-    st = stat_empty();
-    most = -INFINITY;
     if (!(i & 1)) {
       one = mine;
-      continue;
+    } else {
+      merge_slice(one, mine);
+      if (!(i & 2)) {
+        two = one;
+      } else {
+        merge_slice(two, one);
+        if (!(i & 4)) {
+          four = two;
+        } else {
+          merge_slice(four, two);
+        }
+      }
     }
-    merge_slice(one, mine);
-    mine = one;
-    if (!(i & 2)) {
-      two = mine;
-      continue;
-    }
+  }
+  mine = none;
+  if (slices & 1) mine = one;
+  if (slices & 2) {
     merge_slice(two, mine);
     mine = two;
-    if (!(i & 4)) {
-      four = mine;
-      continue;
-    }
+  }
+  if (slices >= 4) {
     merge_slice(four, mine);
     mine = four;
   }
@@ -481,69 +527,47 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
   __syncthreads();
 
   const int n = p.n_top;
-  if (warp == 0 && n > 0) {
-    // the n-th largest of the threads' keys (1 where fewer are not masked), two bits at
-    // a time: the counts that reach three thresholds, in one word's three parts
-    uint32_t k[kPThreads / 32];
-#pragma unroll
-    for (int i = 0; i < kPThreads / 32; ++i) {
-      k[i] = sh.key[0][lane + 32 * i];
-#pragma unroll
-      for (int j = 1; j < kMine; ++j) k[i] = max(k[i], static_cast<uint32_t>(sh.key[j][lane + 32 * i]));
-    }
+  if (n > 0) {
+    // the n-th largest of the threads' keys (1 where fewer are not masked), bit by bit
     uint32_t bar = 0;
 #pragma unroll 1
-    for (int sft = 14; sft >= 0; sft -= 2) {
-      uint32_t reach = 0;
-#pragma unroll
-      for (int i = 0; i < kPThreads / 32; ++i)
-#pragma unroll
-        for (uint32_t q = 1; q <= 3; ++q)
-          reach += k[i] >= (bar | (q << sft)) ? 1u << (10 * (q - 1)) : 0u;
-      reach = __reduce_add_sync(0xffffffffu, reach);
-      const uint32_t want = static_cast<uint32_t>(n);
-      const uint32_t q = ((reach & 1023u) >= want) + ((reach >> 10 & 1023u) >= want) +
-                         ((reach >> 20) >= want);
-      bar |= q << sft;
+    for (uint32_t bit = 0x8000u; bit > 0; bit >>= 1)
+      if (__syncthreads_count(top_key >= (bar | bit)) >= n) bar |= bit;
+    bar = max(bar, 1u);
+    if (top_key >= bar) {
+      for (int i = 0; i < slices; ++i)
+        if (sh.key[i][threadIdx.x] >= bar)
+          sh.hit[atomicAdd(&sh.n_hit, 1)] = static_cast<uint16_t>(i * kPThreads + threadIdx.x);
     }
-    if (lane == 0) sh.bar = max(bar, 1u);
-  }
-  __syncthreads();
-
-  if (n > 0) {
-    const uint32_t bar = sh.bar;
-#pragma unroll
-    for (int i = 0; i < kMine; ++i)
-      if (sh.key[i][threadIdx.x] >= bar)
-        sh.hit[atomicAdd(&sh.n_hit, 1)] = static_cast<uint16_t>(i * kPThreads + threadIdx.x);
     __syncthreads();
-    const int share = static_cast<int>((per + kPThreads - 1) / kPThreads);
-    const int64_t looks = static_cast<int64_t>(sh.n_hit) * share;
-    for (int64_t i = threadIdx.x; i < looks; i += kPThreads) {
-      const int h = static_cast<int>(static_cast<uint64_t>(i) / static_cast<uint32_t>(share));
-      const int j = static_cast<int>(i - static_cast<int64_t>(h) * share);
+    const uint32_t share = static_cast<uint32_t>((per + kPThreads - 1) / kPThreads);
+    const uint32_t looks = static_cast<uint32_t>(sh.n_hit) * share;
+    for (uint32_t i = threadIdx.x; i < looks; i += kPThreads) {
+      const uint32_t h = i / share, j = i - h * share;
       const int who = sh.hit[h];
-      const int64_t from = first + per * (who / kPThreads);
-      const int64_t v = from + who % kPThreads + static_cast<int64_t>(j) * kPThreads;
-      if (v >= min(n_vec, from + per)) continue;
+      const int from = who / kPThreads * per;
+      const int at_v = from + who % kPThreads + static_cast<int>(j) * kPThreads;
+      if (at_v >= min(from + per, n_mine)) continue;
+      const int64_t v = static_cast<int64_t>(first) + at_v;
       const uint4 w = load_vector<kAligned>(x, p.V, v);
       const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-      const __nv_bfloat162 m2 = __hmax2(__hmax2(bf2(w.x), bf2(w.y)), __hmax2(bf2(w.z), bf2(w.w)));
-      const float m = fmaxf(__low2float(m2), __high2float(m2));
-      if (order_key(__float_as_uint(m) >> 16) < bar) continue;
-#pragma unroll 1
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t word = e < 4 ? (e < 2 ? ws[0] : ws[1]) : (e < 6 ? ws[2] : ws[3]);
-        const uint32_t k = order_key(word >> (16 * (e & 1)) & 0xffffu);
-        if (k >= bar) {
-          const int at = atomicAdd(&sh.n_list, 1);
-          if (at < kPList) sh.list[at] = entry_of(k, 8 * v + e);
+      uint32_t reach = 0;  // a bit for each value that does
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        reach |= (order_key(ws[e / 2] >> (16 * (e & 1)) & 0xffffu) >= bar ? 1u : 0u) << e;
+      if (reach == 0) continue;
+      int at = atomicAdd(&sh.n_list, __popc(reach));
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (reach >> e & 1u) {
+          if (at < kPList)
+            sh.list[at] = entry_of(order_key(ws[e / 2] >> (16 * (e & 1)) & 0xffffu), 8 * v + e);
+          ++at;
         }
-      }
     }
     __syncthreads();
     if (sh.n_list > kPList)
-      list_by_bisection<kAligned>(sh, x, p.V, min(n_vec, first), min(n_vec, first + per * kMine), n);
+      list_by_bisection<kAligned>(sh, x, p.V, first, first + n_mine, n);
     const int found = sh.n_list;
     // the first n of them, in order, to the first CTA
     const uint32_t to = first_cta<kC>(&sh.merged[rank][0]);
@@ -574,26 +598,34 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
       for (int k = 0; k < kC; k += 2 * by) merge_slice(part[k], part[k + by]);
     mine = part[0];
   }
-  // then the threads: within each warp, and the warps as a tree
+  // then the threads, all scaled to the row's maximum: within each warp, and the warps in order
+  float m = mine.m, most = mine.most;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
-    SliceStat o;
-    o.m = __shfl_down_sync(0xffffffffu, mine.m, off);
-    o.s = __shfl_down_sync(0xffffffffu, mine.s, off);
-    o.u = __shfl_down_sync(0xffffffffu, mine.u, off);
-    o.most = __shfl_down_sync(0xffffffffu, mine.most, off);
-    if (lane + off < 32) merge_slice(mine, o);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  }
+  if (lane == 0) sh.top[warp] = make_float2(m, most);
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kPWarps; ++w) {
+    m = fmaxf(m, sh.top[w].x);
+    most = fmaxf(most, sh.top[w].y);
+  }
+  rescale(mine, m);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    mine.s = __fadd_rn(mine.s, __shfl_xor_sync(0xffffffffu, mine.s, off));
+    mine.u = __fadd_rn(mine.u, __shfl_xor_sync(0xffffffffu, mine.u, off));
   }
   if (lane == 0) sh.warp[warp] = mine;
   __syncthreads();
-  SliceStat part[kPWarps];
+  SliceStat all{m, 0.f, 0.f, most};
 #pragma unroll
-  for (int w = 0; w < kPWarps; ++w) part[w] = sh.warp[w];
-#pragma unroll
-  for (int by = 1; by < kPWarps; by *= 2)
-#pragma unroll
-    for (int w = 0; w < kPWarps; w += 2 * by) merge_slice(part[w], part[w + by]);
-  SliceStat all = part[0];
+  for (int w = 0; w < kPWarps; ++w) {
+    all.s = __fadd_rn(all.s, sh.warp[w].s);
+    all.u = __fadd_rn(all.u, sh.warp[w].u);
+  }
 
   // The largest y itself is shifted by its product's rounding, up to 2^-4 at 2^20; past
   // that (or where the largest logit is +inf) the row is summed again.
@@ -636,8 +668,10 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
       p.top_logprob[row * n + i] = valid_t ? -INFINITY : bad;
     }
   }
-  for (int i = threadIdx.x; i < kC * kPMaxTop; i += kPThreads) {
-    const int own = i / kPMaxTop, place = i % kPMaxTop;  // a list and the place in it
+  int half = 1;  // steps of a search in a list of up to n
+  while (2 * half <= n) half *= 2;
+  for (int i = threadIdx.x; i < kC * n; i += kPThreads) {
+    const int own = kC == 1 ? 0 : i / n, place = i - own * n;  // a list and the place in it
     if (!valid_t || place >= sh.n_merged[own]) continue;
     const u64 me = sh.merged[own][place];
     int r = place;  // and how many of each other list come before
@@ -648,10 +682,14 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
         lo[k] = 0;
         len[k] = k == own ? 0 : sh.n_merged[k];
       }
-      for (int step = kPMaxTop; step > 0; step >>= 1) {
+#pragma unroll 1
+      for (int step = half; step > 0; step >>= 1) {
+        u64 other[kC];
+#pragma unroll
+        for (int k = 0; k < kC; ++k) other[k] = sh.merged[k][min(lo[k] + step, kPMaxTop) - 1];
 #pragma unroll
         for (int k = 0; k < kC; ++k)
-          if (lo[k] + step <= len[k] && sh.merged[k][lo[k] + step - 1] > me) lo[k] += step;
+          if (lo[k] + step <= len[k] && other[k] > me) lo[k] += step;
       }
 #pragma unroll
       for (int k = 0; k < kC; ++k) r += lo[k];
@@ -704,7 +742,7 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
 template <bool kAligned>
 cudaError_t launch_by_rows(const TopParams& p, int sms, cudaStream_t st) {
   int most = p.T * 8 <= 2 * sms ? 8 : p.T * 4 <= 2 * sms ? 4 : p.T * 2 <= 4 * sms ? 2 : 1;
-  const int64_t used = ((p.V + 7) / 8 + p.per - 1) / p.per;
+  const int64_t used = ((p.V + 7) / 8 + p.per - 1) / p.per;  // slices
   while (most > 1 && most / 2 >= used) most /= 2;
   switch (most) {
     case 8: return launch_top<8, kAligned>(p, st);
@@ -755,8 +793,8 @@ extern "C" int lmhead_top_logprobs(const uint16_t* logits, int64_t T, int64_t V,
   p.temperature = temperature;
   p.row_t = row_temperature;
   p.tokens = tokens;
-  p.per = ((V + 7) / 8 + kPSlices - 1) / kPSlices;
-  p.per = (p.per > kPMinSlice ? p.per + 31 : kPMinSlice) / 32 * 32;
+  const int64_t per = ((V + 7) / 8 + kPSlices - 1) / kPSlices;
+  p.per = static_cast<int>((per > kPMinSlice ? per + 31 : kPMinSlice) / 32 * 32);
   p.n_tokens = static_cast<int>(n_tokens);
   p.n_top = static_cast<int>(n_top);
   p.out_logprob = out_logprob;
