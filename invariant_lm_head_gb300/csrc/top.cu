@@ -44,7 +44,7 @@ constexpr int kPMaxTop = 128;   // most alternatives
 constexpr int kPSlices = 8;     // of a row; the most CTAs that share one
 constexpr int kPList = 512;     // tokens of a CTA's list
 constexpr int kPGroup = 4;      // vectors that a thread folds at once
-constexpr int kPDepth = 3;      // groups on their way to a thread
+constexpr int kPDepth = 2;      // groups on their way to a thread
 constexpr int kPMinSlice = kPGroup * kPThreads;  // vectors of a slice, where the row has them
 static_assert(kPMaxTop <= kPThreads, "a thread's largest value for each alternative");
 constexpr float kPFloor = -200.f;  // 2^-200 is 0: what masked and far values are cut to
@@ -74,7 +74,6 @@ struct TopShared {
   u64 merged[kC][kPMaxTop];          // CTA 0: every CTA's best, in order,
   int n_merged[kC];                  // and how many they are
   int n_hit, n_list;
-  SliceStat peer[kC > 1 ? kC - 1 : 1][kPThreads];  // CTA 0: the other CTAs' threads' sums
   SliceStat warp[kPWarps];
   float2 top[kPWarps];               // the warps' largest y and logit
   uint16_t key[kPSlices / kC][kPThreads];  // a thread's largest value in each slice
@@ -370,7 +369,8 @@ __device__ __forceinline__ void copies_wait() {
 
 // How the vectors of a row reach a thread: each copies its own, kPDepth groups of up to
 // four ahead, into shared memory that no other thread touches. A row that does not start
-// on 16 bytes takes two aligned vectors for each.
+// on 16 bytes takes two aligned vectors for each. Vectors outside [lo, hi), whose copies
+// would reach outside the row, are read element by element.
 template <bool kAligned>
 struct Ring {
   static constexpr int kCopies = kAligned ? 1 : 2;
@@ -378,39 +378,62 @@ struct Ring {
   const uint16_t* row;
   int64_t V;
   uint32_t at;  // this thread's first slot
+  int first;    // the CTA's first vector, from which v below counts
+  int lo, hi;
+  const uint16_t* from;  // this thread's place in the first group, down to 16 bytes
+  __device__ __forceinline__ Ring(const uint16_t* row, int64_t V, uint32_t smem, int first)
+      : row(row), V(V), at(smem + threadIdx.x * 16), first(first) {
+    lo = kAligned ? 0 : 1 - first;
+    hi = static_cast<int>(kAligned ? V / 8 : V / 8 - 1) - first;
+    from = row + 8 * (static_cast<int64_t>(first) + threadIdx.x);
+    if constexpr (!kAligned)
+      from = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t{15});
+  }
   __device__ __forceinline__ uint32_t slot(int depth, int k, int copy) const {
     return at + static_cast<uint32_t>(((depth * kPGroup + k) * kCopies + copy) * kPThreads * 16);
   }
-  // A vector whose copies would reach outside the row: read element by element.
-  __device__ __forceinline__ bool edge(int64_t v) const {
-    return kAligned ? 8 * v + 8 > V : v == 0 || 8 * v + 16 > V;
-  }
-  __device__ __forceinline__ void fetch(int depth, int k, int64_t v) const {
-    if (edge(v)) {
-      const uint4 w = load_vector<kAligned>(row, V, v);
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(depth, k, 0)), "r"(w.x),
-                   "r"(w.y), "r"(w.z), "r"(w.w)
-                   : "memory");
-      return;
-    }
-    const uint16_t* from = row + 8 * v;
-    if constexpr (!kAligned)
-      from = reinterpret_cast<const uint16_t*>(reinterpret_cast<uintptr_t>(from) & ~uintptr_t{15});
+  // The group of vectors v0 + t + 256 k below end.
+  __device__ __forceinline__ void fetch(int depth, int v0, int end) const {
+    const uint16_t* src = from + 8 * static_cast<int64_t>(v0);
+    if (v0 >= lo && v0 + kPGroup * kPThreads <= min(end, hi)) {
 #pragma unroll
-    for (int c = 0; c < kCopies; ++c) copy16_async(slot(depth, k, c), from + 8 * c);
+      for (int k = 0; k < kPGroup; ++k)
+#pragma unroll
+        for (int c = 0; c < kCopies; ++c)
+          copy16_async(slot(depth, k, c), src + 8 * (k * kPThreads + c));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPGroup; ++k) {
+        const int v = v0 + static_cast<int>(threadIdx.x) + k * kPThreads;
+        if (v >= end) continue;
+        if (v >= lo && v < hi) {
+#pragma unroll
+          for (int c = 0; c < kCopies; ++c)
+            copy16_async(slot(depth, k, c), src + 8 * (k * kPThreads + c));
+        } else {
+          const uint4 w = load_vector<kAligned>(row, V, static_cast<int64_t>(first) + v);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(slot(depth, k, 0)),
+                       "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w)
+                       : "memory");
+        }
+      }
+    }
+    copies_commit();  // an empty one too: the groups are counted
   }
-  __device__ __forceinline__ uint4 take(int depth, int k, int64_t v) const {
+  __device__ __forceinline__ uint4 take(int depth, int k, int v) const {
     const uint4 a = ld_shared_v4(slot(depth, k, 0));
     if constexpr (kAligned) return a;
-    if (edge(v)) return a;
+    if (v < lo || v >= hi) return a;
     return shifted(a, ld_shared_v4(slot(depth, k, 1)),
                    static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15));
   }
 };
 
 template <int kC, bool kAligned>
-__global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopParams p) {
+__global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopParams p) {
   extern __shared__ __align__(16) uint8_t ring_smem[];
+  // CTA 0: the other CTAs' threads' sums, behind the ring
+  SliceStat* peer = reinterpret_cast<SliceStat*>(ring_smem + Ring<kAligned>::kBytes);
   __shared__ __align__(16) TopShared<kC> sh;
   constexpr int kMine = kPSlices / kC;  // slices of this CTA
   const int64_t row = blockIdx.x / kC;
@@ -433,15 +456,10 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
   if (threadIdx.x == 0) sh.n_hit = sh.n_list = 0;
   if (kC > 1) row_arrive();  // this CTA has begun: see the wait below
 
-  const Ring<kAligned> ring{x, p.V, smem_u32(ring_smem) + threadIdx.x * 16};
+  const Ring<kAligned> ring(x, p.V, smem_u32(ring_smem), first);
   int ahead = 0, ahead_end = min(per, n_mine);  // the next group to fetch, its slice's end
   auto fetch = [&](int depth) {
-    const int v = ahead + static_cast<int>(threadIdx.x);
-#pragma unroll
-    for (int k = 0; k < kPGroup; ++k)
-      if (v + k * kPThreads < ahead_end)
-        ring.fetch(depth, k, static_cast<int64_t>(first) + v + k * kPThreads);
-    copies_commit();  // an empty one too: the groups are counted
+    ring.fetch(depth, ahead, ahead_end);
     ahead += kStep;
     if (ahead >= ahead_end) {
       ahead = ahead_end;
@@ -468,11 +486,15 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
       copies_wait<kPDepth - 1>();
       const int v = v0 + static_cast<int>(threadIdx.x);
       uint4 w[kPGroup];
+      if (v0 + kStep <= end) {
 #pragma unroll
-      for (int k = 0; k < kPGroup; ++k) {
-        w[k] = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
-        if (v + k * kPThreads < end)
-          w[k] = ring.take(depth, k, static_cast<int64_t>(first) + v + k * kPThreads);
+        for (int k = 0; k < kPGroup; ++k) w[k] = ring.take(depth, k, v + k * kPThreads);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kPGroup; ++k) {
+          w[k] = make_uint4(kMasked2, kMasked2, kMasked2, kMasked2);
+          if (v + k * kPThreads < end) w[k] = ring.take(depth, k, v + k * kPThreads);
+        }
       }
       if (end - v0 > 3 * kPThreads)
         fold<4>(st, most, w, c);
@@ -519,7 +541,7 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
   // its own is here before that.
   if (kC > 1) row_wait();
   if (kC > 1 && rank > 0) {
-    const uint32_t at = first_cta<kC>(&sh.peer[rank > 0 ? rank - 1 : 0][threadIdx.x]);
+    const uint32_t at = first_cta<kC>(peer + (rank - 1) * kPThreads + threadIdx.x);
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(mine.m),
                  "f"(mine.s), "f"(mine.u), "f"(mine.most)
                  : "memory");
@@ -591,7 +613,7 @@ __global__ void __launch_bounds__(kPThreads, 3) top_logprobs_kernel(const TopPar
     SliceStat part[kC];
     part[0] = mine;
 #pragma unroll
-    for (int k = 1; k < kC; ++k) part[k] = sh.peer[k - 1][threadIdx.x];
+    for (int k = 1; k < kC; ++k) part[k] = peer[(k - 1) * kPThreads + threadIdx.x];
 #pragma unroll
     for (int by = 1; by < kC; by *= 2)
 #pragma unroll
@@ -705,6 +727,8 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 template <int kC, bool kAligned>
 cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
+  constexpr int kBytes =
+      Ring<kAligned>::kBytes + (kC - 1) * kPThreads * static_cast<int>(sizeof(SliceStat));
   // The kernel's shared-memory attribute belongs to the device: set by its first call.
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -713,19 +737,19 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(top_logprobs_kernel<kC, kAligned>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<kAligned>::kBytes);
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
     if (e != cudaSuccess) return e;
     done[dev].store(true, std::memory_order_release);
   }
   if constexpr (kC == 1) {
     top_logprobs_kernel<kC, kAligned>
-        <<<static_cast<unsigned>(p.T), kPThreads, Ring<kAligned>::kBytes, st>>>(p);
+        <<<static_cast<unsigned>(p.T), kPThreads, kBytes, st>>>(p);
     return cudaGetLastError();
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
   cfg.blockDim = dim3(kPThreads);
-  cfg.dynamicSmemBytes = Ring<kAligned>::kBytes;
+  cfg.dynamicSmemBytes = kBytes;
   cfg.stream = st;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
