@@ -14,8 +14,8 @@
 // more tokens reach it than the list holds (equal logits), the n-th largest value is
 // found by bisection over the 16-bit keys, counting over the row.
 //
-// A row is eight slices, and every thread of a CTA has its share of each. A cluster of 1
-// to 8 CTAs takes the row, as many as a short batch leaves SMs for; a thread's sums are
+// A row is four slices, and every thread of a CTA has its share of each. A cluster of 1
+// to 4 CTAs takes the row, as many as a short batch leaves SMs for; a thread's sums are
 // merged over the slices as a binary tree, the same one for any number of CTAs, and then
 // over the threads.
 //
@@ -24,6 +24,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -41,7 +42,7 @@ typedef unsigned long long u64;
 constexpr int kPThreads = 256;
 constexpr int kPWarps = kPThreads / 32;
 constexpr int kPMaxTop = 128;   // most alternatives
-constexpr int kPSlices = 8;     // of a row; the most CTAs that share one
+constexpr int kPSlices = 4;     // of a row; the most CTAs that share one
 constexpr int kPList = 512;     // tokens of a CTA's list
 constexpr int kPGroup = 4;      // vectors that a thread folds at once
 constexpr int kPDepth = 2;      // groups on their way to a thread
@@ -141,38 +142,29 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// One pair of values into the packed sums: e = 2^d, and e * d.
-__device__ __forceinline__ void add_pair(float da, float db, f32x2& s2, f32x2& u2) {
-  const f32x2 e2 = f2_pack(ex2(da), ex2(db));
-  s2 = f2_add(s2, e2);
-  u2 = f2_fma(e2, f2_pack(da, db), u2);
-}
-
-// Folds kV vectors into the state; `most` keeps the largest value. Where a value is
-// masked, or so far below that its shift leaves fp32, the shifts are cut to kPFloor.
+// Folds kV vectors into the state; `most` keeps the largest value. A masked value, or one
+// so far below the maximum that its shift leaves fp32, makes the plain sum of e * d a
+// NaN; the shifts are then cut to kPFloor.
 template <int kV>
 __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w, float c) {
-  __nv_bfloat162 hi = bf2(w[0].x), lo = hi;  // the largest passes over a NaN, the smallest keeps it
+  __nv_bfloat162 hi = bf2(w[0].x);  // passes over a NaN
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
     const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      hi = __hmax2(hi, bf2(ws[q]));
-      lo = __hmin2_nan(lo, bf2(ws[q]));
-    }
+    for (int q = 0; q < 4; ++q) hi = __hmax2(hi, bf2(ws[q]));
   }
-  // a NaN of two NaN is a masked value
+  // (the largest of two NaN is one: a masked value)
   const float gmax = fmaxf(fmaxf(__low2float(hi), __high2float(hi)), -INFINITY);
-  const float l0 = __low2float(lo), l1 = __high2float(lo);
   most = fmaxf(most, gmax);
   // never -inf, from which a finite x * c would be infinitely far
   const float mn = fmaxf(fmaxf(st.m, __fmul_rn(gmax, c)), -3.402823466e38f);
   const float d0 = fmaxf(__fsub_rn(st.m, mn), kPFloor);
   const float a = ex2(d0);
-  f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
   const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-mn, -mn);
-  if (__fmaf_rn(l0, c, -mn) > -1e30f && __fmaf_rn(l1, c, -mn) > -1e30f) {
+  float s, u;
+  auto sums = [&](auto cut) {
+    f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
 #pragma unroll
     for (int k = 0; k < kV; ++k) {
       const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
@@ -180,26 +172,25 @@ __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w
       for (int q = 0; q < 4; ++q) {
         float da, db;
         f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
-        add_pair(da, db, s2, u2);
+        if (decltype(cut)::value) {
+          da = fmaxf(da, kPFloor);  // a NaN too
+          db = fmaxf(db, kPFloor);
+        }
+        const f32x2 e2 = f2_pack(ex2(da), ex2(db));
+        s2 = f2_add(s2, e2);
+        u2 = f2_fma(e2, f2_pack(da, db), u2);
       }
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float da, db;
-        f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
-        add_pair(fmaxf(da, kPFloor), fmaxf(db, kPFloor), s2, u2);  // a NaN too
-      }
-    }
-  }
-  float s0, s1, u0, u1;
-  f2_unpack(s2, s0, s1);
-  f2_unpack(u2, u0, u1);
-  st.u = __fadd_rn(__fmul_rn(a, __fmaf_rn(st.s, d0, st.u)), __fadd_rn(u0, u1));
-  st.s = __fadd_rn(__fmul_rn(st.s, a), __fadd_rn(s0, s1));
+    float lo, up;
+    f2_unpack(s2, lo, up);
+    s = __fadd_rn(lo, up);
+    f2_unpack(u2, lo, up);
+    u = __fadd_rn(lo, up);
+  };
+  sums(std::false_type{});
+  if (!(fabsf(u) <= 3.402823466e38f)) sums(std::true_type{});
+  st.u = __fadd_rn(__fmul_rn(a, __fmaf_rn(st.s, d0, st.u)), u);
+  st.s = __fadd_rn(__fmul_rn(st.s, a), s);
   st.m = mn;
 }
 
@@ -469,10 +460,10 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
 #pragma unroll
   for (int d = 0; d < kPDepth - 1; ++d) fetch(d);
 
-  // The slices' sums as a binary tree: pairs, fours, all eight. What is missing at the
-  // end is empty, and leaves the rest as it is.
+  // The slices' sums as a binary tree: pairs, then all four. What is missing at the end
+  // is empty, and leaves the rest as it is.
   const SliceStat none{-INFINITY, 0.f, 0.f, -INFINITY};
-  SliceStat one = none, two = none, four = none, mine = none;
+  SliceStat one = none, two = none, mine = none;
   uint32_t top_key = 0;  // of this thread's values
   int depth = 0, v0 = 0;
 #pragma unroll 1
@@ -515,27 +506,16 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
       one = mine;
     } else {
       merge_slice(one, mine);
-      if (!(i & 2)) {
+      if (i == 1)
         two = one;
-      } else {
+      else
         merge_slice(two, one);
-        if (!(i & 4)) {
-          four = two;
-        } else {
-          merge_slice(four, two);
-        }
-      }
     }
   }
-  mine = none;
-  if (slices & 1) mine = one;
-  if (slices & 2) {
+  mine = slices & 1 ? one : none;
+  if (slices >= 2) {
     merge_slice(two, mine);
     mine = two;
-  }
-  if (slices >= 4) {
-    merge_slice(four, mine);
-    mine = four;
   }
   // The first CTA's shared memory may be written once it runs; a CTA without a slice of
   // its own is here before that.
@@ -765,11 +745,10 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
 // there are slices with something in them.
 template <bool kAligned>
 cudaError_t launch_by_rows(const TopParams& p, int sms, cudaStream_t st) {
-  int most = p.T * 8 <= 2 * sms ? 8 : p.T * 4 <= 2 * sms ? 4 : p.T * 2 <= 4 * sms ? 2 : 1;
+  int most = p.T * 4 <= 2 * sms ? 4 : p.T * 2 <= 2 * sms ? 2 : 1;
   const int64_t used = ((p.V + 7) / 8 + p.per - 1) / p.per;  // slices
   while (most > 1 && most / 2 >= used) most /= 2;
   switch (most) {
-    case 8: return launch_top<8, kAligned>(p, st);
     case 4: return launch_top<4, kAligned>(p, st);
     case 2: return launch_top<2, kAligned>(p, st);
     default: return launch_top<1, kAligned>(p, st);
