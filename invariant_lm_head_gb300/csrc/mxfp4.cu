@@ -70,53 +70,50 @@ __device__ __forceinline__ uint32_t mx_codes(const uint4& v, uint32_t b) {
   return out;
 }
 
-constexpr int kXThreads = 256;
+constexpr int kXThreads = 512;
+constexpr int kXGridPerSm = 12;  // (152064 x 3584: 3 an SM 223 us, 6 216, 12 212, a tile each 236)
+constexpr int kXRows = kXAtomRows / (kXThreads / 16);  // rows of a thread: 4, 32 apart
+static_assert(kXRows == 4, "the four rows that share 16 bytes of scales");
 
-// A CTA takes 128 rows x 128 columns: 16 lanes a row (16 bytes each), eight rows a
-// thread, all loaded before the first is used. A block is four lanes; a row's four
-// scales meet in one word, and lane 0 of a row gathers the words of four rows, 32
-// apart, into the 16 bytes that they share.
-__global__ void __launch_bounds__(kXThreads)
+// A CTA takes 128 rows x 128 columns: 16 lanes a row (16 bytes each), four rows a thread,
+// all loaded before the first is used. A block is four lanes; a row's four scales meet
+// in one word, and the words of a thread's four rows are the 16 bytes that they share.
+__global__ void __launch_bounds__(kXThreads, 3)
     quantize_mxfp4_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
                           int64_t kb, int64_t n_tiles, uint8_t* __restrict__ q,
                           uint8_t* __restrict__ scale) {
-  const int sub = threadIdx.x & 15, r16 = threadIdx.x >> 4;
+  const int sub = threadIdx.x & 15, r32 = threadIdx.x >> 4;
   for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
     const int64_t rb = b / kb;
     const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
-    const int64_t row0 = rb * kXAtomRows + r16;
-    uint4 v[8];
+    const int64_t row0 = rb * kXAtomRows + r32;
+    // of this thread's rows, how many there are
+    const int n = col < cols ? static_cast<int>(min(int64_t{kXRows}, (rows - row0 + 31) >> 5)) : 0;
+    const uint16_t* src = x + row0 * ld + col;
+    uint4 v[kXRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + 16 * i;
+    for (int i = 0; i < kXRows; ++i) {
       v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (row < rows && col < cols) v[i] = *reinterpret_cast<const uint4*>(x + row * ld + col);
+      if (i < n) v[i] = *reinterpret_cast<const uint4*>(src + i * 32 * ld);
     }
-    uint32_t words[8];
+    uint8_t* dst = q + (row0 * cols + col) / 2;
+    uint32_t words[kXRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + 16 * i;
-      const bool on = row < rows && col < cols;
-      uint32_t m = 0u;
-      m = __vmaxu2(m, v[i].x & 0x7fff7fffu);
-      m = __vmaxu2(m, v[i].y & 0x7fff7fffu);
-      m = __vmaxu2(m, v[i].z & 0x7fff7fffu);
-      m = __vmaxu2(m, v[i].w & 0x7fff7fffu);
+    for (int i = 0; i < kXRows; ++i) {
+      uint32_t m = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                            __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
       m = max(m & 0xffffu, m >> 16);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       const uint32_t s = mx_scale(m);
-      if (on) *reinterpret_cast<uint32_t*>(q + (row * cols + col) / 2) = mx_codes(v[i], s);
-      uint32_t w = (on ? s : kXPad) << (8 * (sub >> 2));
+      if (i < n) *reinterpret_cast<uint32_t*>(dst + i * 16 * cols) = mx_codes(v[i], s);
+      uint32_t w = (i < n ? s : kXPad) << (8 * (sub >> 2));
       w |= __shfl_xor_sync(0xffffffffu, w, 4);
-      w |= __shfl_xor_sync(0xffffffffu, w, 8);
-      words[i] = w;
+      words[i] = w | __shfl_xor_sync(0xffffffffu, w, 8);
     }
-    if (sub == 0) {
-      uint4* o = reinterpret_cast<uint4*>(scale + b * kXAtomBytes) + r16;
-      o[0] = make_uint4(words[0], words[2], words[4], words[6]);
-      o[16] = make_uint4(words[1], words[3], words[5], words[7]);
-    }
+    if (sub == 0)
+      reinterpret_cast<uint4*>(scale + b * kXAtomBytes)[r32] =
+          make_uint4(words[0], words[1], words[2], words[3]);
   }
 }
 
@@ -127,30 +124,28 @@ __device__ __forceinline__ float mx_value(uint32_t b) {
 }
 
 // The same tiles back to bf16.
-__global__ void __launch_bounds__(kXThreads)
+__global__ void __launch_bounds__(kXThreads, 3)
     dequantize_mxfp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                             int64_t rows, int64_t cols, int64_t kb, int64_t n_tiles,
                             uint16_t* __restrict__ out, int64_t ld) {
-  const int sub = threadIdx.x & 15, r16 = threadIdx.x >> 4;
+  const int sub = threadIdx.x & 15, r32 = threadIdx.x >> 4;
   for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
     const int64_t rb = b / kb;
     const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
-    const int64_t row0 = rb * kXAtomRows + r16;
-    if (col >= cols) continue;
-    uint32_t codes[8];
+    const int64_t row0 = rb * kXAtomRows + r32;
+    const int n = col < cols ? static_cast<int>(min(int64_t{kXRows}, (rows - row0 + 31) >> 5)) : 0;
+    const uint8_t* src = q + (row0 * cols + col) / 2;
+    uint32_t codes[kXRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + 16 * i;
+    for (int i = 0; i < kXRows; ++i) {
       codes[i] = 0u;
-      if (row < rows) codes[i] = *reinterpret_cast<const uint32_t*>(q + (row * cols + col) / 2);
+      if (i < n) codes[i] = *reinterpret_cast<const uint32_t*>(src + i * 16 * cols);
     }
-    const uint4* s = reinterpret_cast<const uint4*>(scale + b * kXAtomBytes) + r16;
-    const uint4 sa = s[0], sb = s[16];
-    const uint32_t words[8] = {sa.x, sb.x, sa.y, sb.y, sa.z, sb.z, sa.w, sb.w};
+    const uint4 s = reinterpret_cast<const uint4*>(scale + b * kXAtomBytes)[r32];
+    const uint32_t words[kXRows] = {s.x, s.y, s.z, s.w};
+    uint16_t* dst = out + row0 * ld + col;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int64_t row = row0 + 16 * i;
-      if (row >= rows) continue;
+    for (int i = 0; i < kXRows; ++i) {
       const float f = mx_value((words[i] >> (8 * (sub >> 2))) & 0xffu);
       uint32_t h[4], o[4];
       asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
@@ -163,7 +158,7 @@ __global__ void __launch_bounds__(kXThreads)
         const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
         o[j] = bf16x2_of(p.x * f, p.y * f);
       }
-      *reinterpret_cast<uint4*>(out + row * ld + col) = make_uint4(o[0], o[1], o[2], o[3]);
+      if (i < n) *reinterpret_cast<uint4*>(dst + i * 32 * ld) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -688,7 +683,7 @@ extern "C" int lmhead_quantize_mxfp4(const uint16_t* x, int64_t rows, int64_t co
   cudaError_t e;
   {
     KernelTimer timer(K_QUANTIZE_MXFP4, st);
-    const int grid = static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms);
+    const int grid = static_cast<int>(tiles < kXGridPerSm * sms ? tiles : kXGridPerSm * sms);
     quantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(x, rows, cols, ld, kb, tiles, q, scale);
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
@@ -718,7 +713,7 @@ extern "C" int lmhead_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, i
   cudaError_t e;
   {
     KernelTimer timer(K_DEQUANTIZE_MXFP4, st);
-    const int grid = static_cast<int>(tiles < 8 * sms ? tiles : 8 * sms);
+    const int grid = static_cast<int>(tiles < kXGridPerSm * sms ? tiles : kXGridPerSm * sms);
     dequantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(q, scale, rows, cols, kb, tiles, out,
                                                         ld_out);
     e = cudaGetLastError();

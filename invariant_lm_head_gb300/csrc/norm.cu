@@ -16,6 +16,7 @@
 // range, infinities, NaN) take y itself, rounded.
 //
 // Batch invariance: the order of a row's sum depends on H alone.
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 
@@ -33,6 +34,7 @@ namespace {
 
 constexpr int kNBlock = 128;   // columns of a scale
 constexpr int kNLanes = 8;     // lanes of a block, 16 elements each
+constexpr int kNMaxSmem = 131072;  // 32768 columns one row at a time, 16384 two
 constexpr int kNMaxCols = 32768;  // four units of each of 512 threads
 
 struct NormParams {
@@ -68,9 +70,11 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 
 // One row a CTA at a time. Thread t holds, for unit i < kU, 16 elements of block
 // (t + i * blockDim.x) / 8: two runs of 8 (16 bytes), 64 columns apart, so that a block's
-// scale is worked out by 8 lanes.
-template <int kU>
+// scale is worked out by 8 lanes. Each thread copies its own share of the CTA's next kD
+// - 1 rows to shared memory while it works on one.
+template <int kU, int kD>
 __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const NormParams p) {
+  extern __shared__ __align__(16) uint8_t ahead[];
   __shared__ float part[3][32];
   const int sub = threadIdx.x & (kNLanes - 1);
   int col[kU];
@@ -79,6 +83,29 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
   for (int i = 0; i < kU; ++i) {
     const int blk = (threadIdx.x + i * blockDim.x) / kNLanes;
     col[i] = blk < p.kb ? blk * kNBlock + sub * 8 : p.cols;
+  }
+  const uint32_t slots = smem_u32(ahead) + threadIdx.x * 16;
+  auto slot = [&](int d, int which, int i, int h) {
+    return slots + static_cast<uint32_t>((((d * 2 + which) * kU + i) * 2 + h) * blockDim.x * 16);
+  };
+  auto fetch = [&](int64_t row, int d) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < kU; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (col[i] + 64 * h < p.cols) {
+            copy16_async(slot(d, 0, i, h), p.x + row * p.ld_x + col[i] + 64 * h);
+            if (p.residual)
+              copy16_async(slot(d, 1, i, h), p.residual + row * p.ld_res + col[i] + 64 * h);
+          }
+    }
+    copies_commit();  // an empty one too: the groups are counted
+  };
+#pragma unroll
+  for (int d = 0; d < kD - 1; ++d) fetch(blockIdx.x + static_cast<int64_t>(d) * gridDim.x, d);
+#pragma unroll
+  for (int i = 0; i < kU; ++i) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       w[i][h] = make_uint4(0u, 0u, 0u, 0u);
@@ -86,42 +113,31 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
         w[i][h] = *reinterpret_cast<const uint4*>(p.weight + col[i] + 64 * h);
     }
   }
-  int parity = 0;
+  int parity = 0, depth = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+    fetch(row + static_cast<int64_t>(kD - 1) * gridDim.x, depth == 0 ? kD - 1 : depth - 1);
+    copies_wait<kD - 1>();
     uint4 v[kU][2];
 #pragma unroll
     for (int i = 0; i < kU; ++i) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         v[i][h] = make_uint4(0u, 0u, 0u, 0u);
-        if (col[i] + 64 * h < p.cols)
-          v[i][h] = *reinterpret_cast<const uint4*>(p.x + row * p.ld_x + col[i] + 64 * h);
-      }
-    }
-    if (p.residual) {
-      uint4 r[kU][2];
-#pragma unroll
-      for (int i = 0; i < kU; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          r[i][h] = make_uint4(0u, 0u, 0u, 0u);
-          if (col[i] + 64 * h < p.cols)
-            r[i][h] = *reinterpret_cast<const uint4*>(p.residual + row * p.ld_res + col[i] + 64 * h);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kU; ++i) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          v[i][h].x = add_bf16x2(v[i][h].x, r[i][h].x);
-          v[i][h].y = add_bf16x2(v[i][h].y, r[i][h].y);
-          v[i][h].z = add_bf16x2(v[i][h].z, r[i][h].z);
-          v[i][h].w = add_bf16x2(v[i][h].w, r[i][h].w);
-          if (p.out_residual && col[i] + 64 * h < p.cols)
-            *reinterpret_cast<uint4*>(p.out_residual + row * p.ld_out + col[i] + 64 * h) = v[i][h];
+        if (col[i] + 64 * h < p.cols) {
+          v[i][h] = ld_shared_v4(slot(depth, 0, i, h));
+          if (p.residual) {
+            const uint4 r = ld_shared_v4(slot(depth, 1, i, h));
+            v[i][h].x = add_bf16x2(v[i][h].x, r.x);
+            v[i][h].y = add_bf16x2(v[i][h].y, r.y);
+            v[i][h].z = add_bf16x2(v[i][h].z, r.z);
+            v[i][h].w = add_bf16x2(v[i][h].w, r.w);
+            if (p.out_residual)
+              *reinterpret_cast<uint4*>(p.out_residual + row * p.ld_out + col[i] + 64 * h) = v[i][h];
+          }
         }
       }
     }
+    if (++depth == kD) depth = 0;
     auto squares = [&](float factor) {
       f32x2 s2 = f2_pack(0.f, 0.f);
 #pragma unroll
@@ -216,15 +232,32 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
 // Units of 16 elements of a thread, by the row's length alone: the sum's order follows.
-template <int kU>
+template <int kU, int kD>
 cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   const int units = p.kb * kNLanes;
-  const int threads = ((units + kU - 1) / kU + 31) / 32 * 32;
-  int per_sm = 2048 / threads;
-  if (per_sm > 16) per_sm = 16;
-  const int64_t most = static_cast<int64_t>(sms) * per_sm;
+  const int warps = ((units + kU - 1) / kU + 31) / 32, threads = 32 * warps;
+  const int bytes = kD * 2 * kU * 2 * threads * 16;
+  // CTAs that an SM holds, by the CTA's warps, and the kernel's shared-memory attribute:
+  // the device's, looked up by its first call of that length.
+  static std::atomic<int> per_sm[64][17];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n = per_sm[dev][warps].load(std::memory_order_acquire);
+  if (n == 0) {
+    if ((e = cudaFuncSetAttribute(norm_fp8_kernel<kU, kD>,
+                                  cudaFuncAttributeMaxDynamicSharedMemorySize, kNMaxSmem)) !=
+            cudaSuccess ||
+        (e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_fp8_kernel<kU, kD>, threads,
+                                                           bytes)) != cudaSuccess)
+      return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    per_sm[dev][warps].store(n, std::memory_order_release);
+  }
+  const int64_t most = static_cast<int64_t>(sms) * n;  // a persistent grid
   const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
-  norm_fp8_kernel<kU><<<grid, threads, 0, st>>>(p);
+  norm_fp8_kernel<kU, kD><<<grid, threads, bytes, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -278,12 +311,15 @@ extern "C" int lmhead_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual,
   cudaError_t e;
   {
     KernelTimer timer(K_NORM_FP8, st);
+    // rows ahead as shared memory allows
     if (cols <= 4096)
-      e = launch_norm<1>(p, sms, st);
+      e = launch_norm<1, 3>(p, sms, st);
+    else if (cols <= 8192)
+      e = launch_norm<2, 3>(p, sms, st);
     else if (cols <= 16384)
-      e = launch_norm<2>(p, sms, st);
+      e = launch_norm<2, 2>(p, sms, st);
     else
-      e = launch_norm<4>(p, sms, st);
+      e = launch_norm<4, 1>(p, sms, st);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) {

@@ -348,16 +348,6 @@ __device__ __forceinline__ uint32_t first_cta(const void* here) {
   return kC > 1 ? mapa_shared(smem_u32(here), 0u) : smem_u32(here);
 }
 
-// 16 bytes of a thread's own on their way to shared memory.
-__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void copies_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kN) : "memory");
-}
-
 // How the vectors of a row reach a thread: each copies its own, kPDepth groups of up to
 // four ahead, into shared memory that no other thread touches. A row that does not start
 // on 16 bytes takes two aligned vectors for each. Vectors outside [lo, hi), whose copies
