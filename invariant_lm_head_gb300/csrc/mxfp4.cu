@@ -176,7 +176,7 @@ constexpr int kXBoxes = kXN / kXBox;
 constexpr int kXMaxStages = 8;
 constexpr int kXEpiWarps = 4;
 constexpr int kXLogitsThreads = 64 + 32 * kXEpiWarps;  // warp 0 loads, warp 1 issues
-constexpr int kXStagingWarp = 4096;   // two 32 x 32 bf16 boxes
+constexpr int kXStagingWarp = 4096;   // of rows at any address
 constexpr int kXStagingBytes = kXEpiWarps * kXStagingWarp;
 constexpr int kXBarBytes = 512;
 constexpr int kXSmemBytes = 232448;
@@ -201,7 +201,7 @@ struct Mxfp4Params {
   int a_rows;             // rows of an A box (T <= 128: T rounded up to 8)
   uint16_t* out;
   int64_t ld;
-  int tma_out, v_tma;     // as for the fp8 logits
+  int wide;               // rows on 32 (2) or 16 (1) bytes: stored in such parts
   unsigned* status;
 };
 
@@ -269,13 +269,47 @@ __device__ __forceinline__ void mx_unit(const Mxfp4Params& p, int u, int& m, int
   m = first + (r - n * gm);
 }
 
+// 32 finished columns of this lane's row, the first n - col of them, in parts of 32 or 16
+// bytes. Straight from the registers: a box in shared memory on the way to a TMA store
+// costs the loads and the MMAs, which share its bandwidth, more than 64-byte pieces of
+// rows cost L2.
+__device__ __forceinline__ void store_box(uint16_t* row, int col, int n, const uint32_t (&d)[32],
+                                          int wide) {
+  uint32_t w[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    w[j] = bf16x2_of(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+  uint16_t* o = row + col;
+  const int left = n - col;
+  if (left >= kXBox && wide == 2) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(o + 16 * j),
+                   "r"(w[8 * j]), "r"(w[8 * j + 1]), "r"(w[8 * j + 2]), "r"(w[8 * j + 3]),
+                   "r"(w[8 * j + 4]), "r"(w[8 * j + 5]), "r"(w[8 * j + 6]), "r"(w[8 * j + 7])
+                   : "memory");
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (8 * j + 8 <= left) {
+      *reinterpret_cast<uint4*>(o + 8 * j) =
+          make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+    } else {  // the vocabulary's end
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (8 * j + e < left) o[8 * j + e] = static_cast<uint16_t>(w[4 * j + e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
 // Warp 0 loads, warp 1 copies the scales to TMEM and issues the MMAs (CTA 0 of a pair for
 // both), the others turn finished tiles to bf16. Tokens are the MMA's rows, the
 // vocabulary its columns.
 template <bool kPair>
 __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const CUtensorMap& tmB,
                                                   const CUtensorMap& tmSA, const CUtensorMap& tmSB,
-                                                  const CUtensorMap& tmC, const Mxfp4Params& p) {
+                                                  const Mxfp4Params& p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -323,7 +357,6 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmSA);
     tma_prefetch_desc(&tmSB);
-    if (p.tma_out) tma_prefetch_desc(&tmC);
   }
   if (warp == 1) {
     if constexpr (kPair) {
@@ -469,7 +502,7 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
     const int lanes0 = 32 * (warp & 3);  // the TMEM lanes this warp may read
     const uint32_t lane_addr = static_cast<uint32_t>(lanes0) << 16;
     const uint32_t stg = staging + ew * kXStagingWarp;
-    uint32_t tile = 0, obuf = 0;
+    uint32_t tile = 0;
     for (int u = first_unit; u < p.n_units; u += unit_stride, ++tile) {
       int m, n;
       mx_unit(p, u, m, n);
@@ -491,68 +524,55 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
             mbar_arrive(tfree_bar);
         }
       };
-      auto store = [&](int b, const uint32_t (&d)[32]) {
-        const int64_t colb = col0 + b * kXBox;
-        if (colb >= p.V) return;
-        if (!p.tma_out) {
-          uint32_t words[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j)
-            words[j] = bf16x2_of(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
-          const int64_t left = p.V - colb;
-          store_rows(stg, lane, words, p.out + static_cast<int64_t>(row0) * p.ld + colb, p.ld,
-                     min(32, p.T - row0), static_cast<int>(min(static_cast<int64_t>(kXBox), left)));
-          return;
-        }
-        // a warp's 32 rows leave in boxes of 32 columns, through two buffers in turn
-        const uint32_t obox = stg + obuf;
-        obuf ^= kXStagingWarp / 2;
-        if (lane == 0) bulk_wait_group_read<1>();  // the box before the last has left
-        __syncwarp();
-        stage_box_row(obox, lane, reinterpret_cast<const float*>(d));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          if (colb < p.v_tma) tma_store_2d(&tmC, obox, static_cast<int32_t>(colb), row0);
-          bulk_commit_group();  // an empty one too: the buffers' turns are counted in groups
-        }
-        if (p.v_tma < p.V && p.v_tma < colb + kXBox && row < p.T) {
-          // the vocabulary's last columns (at most seven): a chunk that TMA would fill
-          // with zeros past the row's end
-          const int j = (p.v_tma - static_cast<int>(colb)) >> 3;
-          const uint4 c = ld_shared_v4(obox + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4));
-          const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-          uint16_t* o = p.out + static_cast<int64_t>(row) * p.ld + p.v_tma;
-#pragma unroll
-          for (int e = 0; e < 7; ++e)
-            st_global_u16_if(o + e, static_cast<uint16_t>(w[e / 2] >> (16 * (e & 1))),
-                             p.v_tma + e < p.V);
-        }
-      };
       if (!warp_on) {  // no row of this warp's is stored
         release();
         continue;
       }
       // the shared columns first (the last boxes of the first accumulator, the first of
       // the second): the next tile's MMAs wait for no more than these reads
-      const int first = (tile & 1u) ? 0 : kXBoxes - kXShared;
-      uint32_t d0[32], d1[32];
-      tmem_ld32_issue(src + first * kXBox, d0);
-      tmem_ld32_issue(src + (first + 1) * kXBox, d1);
-      tmem_ld_wait(d0);
-      tmem_ld_wait(d1);
-      release();
-      store(first, d0);
-      store(first + 1, d1);
-#pragma unroll 1
-      for (int i = kXShared; i < kXBoxes; ++i) {
-        const int b = (first + i) & (kXBoxes - 1);
-        tmem_ld32_issue(src + b * kXBox, d0);
+      if (p.wide > 0) {
+        uint16_t* const o = p.out + static_cast<int64_t>(row) * p.ld + col0;
+        const int n_cols = row < p.T ? static_cast<int>(min(int64_t{kXN}, p.V - col0)) : 0;
+        const int first = (tile & 1u) ? 0 : kXBoxes - kXShared;
+        uint32_t d0[32], d1[32];
+        tmem_ld32_issue(src + first * kXBox, d0);
+        tmem_ld32_issue(src + (first + 1) * kXBox, d1);
         tmem_ld_wait(d0);
-        store(b, d0);
+        tmem_ld_wait(d1);
+        release();
+        store_box(o, first * kXBox, n_cols, d0, p.wide);
+        store_box(o, (first + 1) * kXBox, n_cols, d1, p.wide);
+#pragma unroll 1
+        for (int i = kXShared; i < kXBoxes; ++i) {
+          const int b = (first + i) & (kXBoxes - 1);
+          tmem_ld32_issue(src + b * kXBox, d0);
+          tmem_ld_wait(d0);
+          store_box(o, b * kXBox, n_cols, d0, p.wide);
+        }
+        continue;
+      }
+      // rows at any address leave through shared memory, half a tile's columns at a time
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int h = (tile & 1u) ? i : 1 - i;
+        const int64_t colb = col0 + h * (kXN / 2);
+        uint32_t words[kXN / 4];
+#pragma unroll
+        for (int b = 0; b < kXBoxes / 2; ++b) {
+          uint32_t d[32];
+          tmem_ld32_issue(src + h * (kXN / 2) + b * kXBox, d);
+          tmem_ld_wait(d);
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            words[16 * b + j] = bf16x2_of(__uint_as_float(d[2 * j]), __uint_as_float(d[2 * j + 1]));
+        }
+        if (i == 0) release();
+        if (colb < p.V)
+          store_rows(stg, lane, words, p.out + static_cast<int64_t>(row0) * p.ld + colb, p.ld,
+                     min(32, p.T - row0),
+                     static_cast<int>(min(int64_t{kXN / 2}, p.V - colb)));
       }
     }
-    if (lane == 0) bulk_wait_group<0>();  // every output box of this warp has been written
   }
 
   tc_fence_before();
@@ -597,8 +617,8 @@ __global__ void __launch_bounds__(kXLogitsThreads, 1)
                         const __grid_constant__ CUtensorMap tmB,
                         const __grid_constant__ CUtensorMap tmSA,
                         const __grid_constant__ CUtensorMap tmSB,
-                        const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
-  logits_mxfp4_body<false>(tmA, tmB, tmSA, tmSB, tmC, p);
+                        const Mxfp4Params p) {
+  logits_mxfp4_body<false>(tmA, tmB, tmSA, tmSB, p);
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXLogitsThreads, 1)
@@ -606,8 +626,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kXLogitsThreads, 1)
                              const __grid_constant__ CUtensorMap tmB,
                              const __grid_constant__ CUtensorMap tmSA,
                              const __grid_constant__ CUtensorMap tmSB,
-                             const __grid_constant__ CUtensorMap tmC, const Mxfp4Params p) {
-  logits_mxfp4_body<true>(tmA, tmB, tmSA, tmSB, tmC, p);
+                             const Mxfp4Params p) {
+  logits_mxfp4_body<true>(tmA, tmB, tmSA, tmSB, p);
 }
 
 // The kernels' shared-memory attribute belongs to the device: set by its first call. *pairs:
@@ -765,12 +785,11 @@ extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidde
   p.a_rows = T < kXM ? static_cast<int>((T + 7) / 8 * 8) : kXM;
   p.out = logits;
   p.ld = ld_logits;
-  p.v_tma = static_cast<int>(V / 8 * 8);
-  p.tma_out = (ld_logits % 8 == 0 && !misaligned(logits, 16) && p.v_tma > 0) ? 1 : 0;
+  // one row has no distance to the next
+  p.wide = (T == 1 || ld_logits % 16 == 0) && !misaligned(logits, 32) ? 2
+           : (T == 1 || ld_logits % 8 == 0) && !misaligned(logits, 16) ? 1 : 0;
   p.status = status;
-  CUtensorMap ta, tb, tsa, tsb, tc{};
-  if (p.tma_out && (rc = api_make_out_tmap_bf16(&tc, logits, p.v_tma, T, ld_logits * 2)) != LMH_OK)
-    return rc;
+  CUtensorMap ta, tb, tsa, tsb;
   if ((rc = api_make_tmap_u8(&ta, hidden_q, H / 2, T, H / 2, kXK / 2, p.a_rows)) != LMH_OK ||
       (rc = api_make_tmap_u8(&tb, weight_q, H / 2, V, H / 2, kXK / 2, pair ? kXN / 2 : kXN)) !=
           LMH_OK ||
@@ -784,10 +803,10 @@ extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidde
     KernelTimer timer(K_LOGITS_MXFP4, st);
     if (pair) {
       const int grid = 2 * (p.n_units < pairs ? p.n_units : pairs);
-      logits_mxfp4_pair_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, tc, p);
+      logits_mxfp4_pair_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, p);
     } else {
       const int grid = p.n_units < sms ? p.n_units : sms;
-      logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, tc, p);
+      logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, p);
     }
     e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
