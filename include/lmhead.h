@@ -561,7 +561,8 @@ int lmhead_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual, const uint16
  *   scale   [ceil(rows / 128), ceil(cols / 128), 32, 16] bytes, 16-byte aligned: the byte
  *           of (row, block) is at [row / 128][block / 4][row % 32][row / 32 % 4 * 4 +
  *           block % 4] (the order in which the tensor cores read scales). The quantiser
- *           writes 127 (the scale 1) in places past the rows and columns
+ *           writes 127 (the scale 1) in places past the rows and columns; scales from
+ *           elsewhere need something below 255 past the columns
  * rows == 0 is a no-op.
  */
 int lmhead_quantize_mxfp4(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, uint8_t* q,

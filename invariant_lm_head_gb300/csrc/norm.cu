@@ -161,9 +161,9 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
     float r;
     if (sum < INFINITY) {
       r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), p.eps));
-    } else {  // squares past fp32 (or an infinity or a NaN): the row in units of 2^64
-      const float scaled = row_sum(squares(0x1p-64f), part[2]);
-      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(scaled, n), p.eps * 0x1p-64f * 0x1p-64f)) * 0x1p-64f;
+    } else {  // squares past fp32 (or an infinity or a NaN): the row in units of 2^80
+      const float scaled = row_sum(squares(0x1p-80f), part[2]);
+      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(scaled, n), p.eps * 0x1p-80f * 0x1p-80f)) * 0x1p-80f;
       __syncthreads();  // part[2] is free for the next such row
     }
 #pragma unroll

@@ -80,7 +80,7 @@ struct TopShared {
   uint16_t key[kPSlices / kC][kPThreads];  // a thread's largest value in each slice
   uint16_t hit[kPThreads * kPSlices / kC];
   uint32_t count[kPWarps];
-  uint32_t bar;                      // the key that alternatives reach
+  float temperature;
 };
 
 // 16 bits in the order of the values: 0 for a masked logit, and equal zeros.
@@ -247,7 +247,9 @@ __device__ __noinline__ void list_by_bisection(Shared& sh, const uint16_t* row, 
     else
       hi = mid;
   }
-  const int above = static_cast<int>(count_from<kAligned>(row, V, v0, v1, lo + 1, sh.count));
+  // (at most n, also where a caller changes the row meanwhile)
+  const int above = static_cast<int>(
+      min(count_from<kAligned>(row, V, v0, v1, lo + 1, sh.count), static_cast<uint32_t>(n)));
   if (threadIdx.x == 0) sh.n_list = 0;
   __syncthreads();
   int taken = above;  // list places given to equal ones start here
@@ -429,12 +431,11 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   const int n_mine = static_cast<int>(min(static_cast<int64_t>(n_vec - first), static_cast<int64_t>(per) * kMine));
   const int slices = (n_mine + per - 1) / per;
 
-  float t = p.row_t ? p.row_t[row] : p.temperature;
-  if (t == 0.f) t = 1.f;
-  const bool valid_t = t > 0.f && t <= 3.402823466e38f;
-  if (!valid_t) t = 1.f;
-  const float c = __fdiv_rn(kLog2e, t);
-  if (threadIdx.x == 0) sh.n_hit = sh.n_list = 0;
+  if (threadIdx.x == 0) {
+    // one reading of the temperature decides every thread's way
+    sh.temperature = p.row_t ? p.row_t[row] : p.temperature;
+    sh.n_hit = sh.n_list = 0;
+  }
   if (kC > 1) row_arrive();  // this CTA has begun: see the wait below
 
   const Ring<kAligned> ring(x, p.V, smem_u32(ring_smem), first);
@@ -449,6 +450,12 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   };
 #pragma unroll
   for (int d = 0; d < kPDepth - 1; ++d) fetch(d);
+  __syncthreads();
+  float t = sh.temperature;
+  if (t == 0.f) t = 1.f;
+  const bool valid_t = t > 0.f && t <= 3.402823466e38f;
+  if (!valid_t) t = 1.f;
+  const float c = __fdiv_rn(kLog2e, t);
 
   // The slices' sums as a binary tree: pairs, then all four. What is missing at the end
   // is empty, and leaves the rest as it is.

@@ -118,6 +118,21 @@ def test_norm_magnitudes(scale):
         assert ((s.double() - a / 448).abs() <= 1e-5 * a / 448).all()
 
 
+def test_norm_of_the_largest_values():
+    # every square past fp32, and their sum past what one scaling by 2^-64 would hold
+    import torch
+
+    big = float(-LOWEST)
+    x = torch.full((3, 512), big, dtype=torch.bfloat16, device=dev())
+    x[1, 7:] = 0
+    x[2] *= (-1.0) ** torch.arange(512, device=dev())
+    w = torch.full((512,), 2.0, dtype=torch.bfloat16, device=dev())
+    q, s, _ = lmh.lmhead_rmsnorm_fp8(x, w)
+    y = q.float() * s.repeat_interleave(128, 1)
+    assert (y[0] / 2 - 1).abs().max() < 1e-5 and (y[2].abs() / 2 - 1).abs().max() < 1e-5
+    assert (y[1, :7] / (2 * (512 / 7) ** 0.5) - 1).abs().max() < 1e-5 and (y[1, 7:] == 0).all()
+
+
 def test_norm_zeros_floor_and_not_finite():
     import torch
 
@@ -606,6 +621,32 @@ def test_top_at_any_address_and_alone(V):
     for a, b in [(0, 1), (39, 40), (7, 20)]:
         same(lmh.lmhead_top_logprobs(buf[a:b, :V].clone(), to_dev(ids[a:b]), 0.9),
              [v[a:b] for v in want])
+
+
+@pytest.mark.parametrize("T", [3, 60, 200])
+def test_top_while_its_inputs_change(T):
+    # A caller that forgets to order two streams gets senseless alternatives, nothing worse:
+    # one reading of a temperature decides a CTA's way, and every index is bounded.
+    import torch
+
+    V = 40003
+    x, g = logit_rows(T, T, V)
+    good = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    wild = torch.randint(-32768, 32767, (T, V), device=dev(), dtype=torch.int16).view(torch.bfloat16)
+    flat = torch.zeros_like(good)
+    lg = good.clone()
+    t = torch.full((T,), 0.9, device=dev())
+    ts = [t.clone(), torch.full_like(t, 0.0), torch.full_like(t, float("nan")), torch.full_like(t, 1e-30)]
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for i in range(200):
+        with torch.cuda.stream(other):
+            lg.copy_((wild, good, flat)[i % 3])
+            t.copy_(ts[i % 4])
+        lmh.lmhead_top_logprobs(lg, None, t, top=100)
+    torch.cuda.synchronize()
+    t.fill_(0.9)
+    same(lmh.lmhead_top_logprobs(good, None, t, top=100), lmh.lmhead_top_logprobs(good, None, 0.9, top=100))
 
 
 def test_top_many_rows():
