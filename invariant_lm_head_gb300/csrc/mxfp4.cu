@@ -452,11 +452,6 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
         }
       };
       for (int u = first_unit; u < p.n_units && ok; u += unit_stride, ++tile) {
-        // the tile before has left the columns that both accumulators hold (and the one
-        // before that has left this one)
-        if (!__all_sync(0xffffffffu, mbar_wait<kPair>(tfree_bar, (tile & 1u) ^ 1u, abort_flag,
-                                                      p.status)))
-          break;
         const uint32_t acc = tmem + ((tile & 1u) ? kXAcc1 : 0u);
         for (int kb = 0; kb < p.KB; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait(full_bar(stage), phase, abort_flag, p.status))) {
@@ -477,6 +472,18 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
                 tc_copy_scales<kPair>(sfb + 8 * a + 4 * i,
                                       sd + ((1 + i) * kXSetBytes + a * kXAtomBytes) / 16);
             }
+          }
+          if (kb == 0) {
+            // the tile before has left the columns that both accumulators hold (and the
+            // one before that has left this one)
+            if (!__all_sync(0xffffffffu, mbar_wait<kPair>(tfree_bar, (tile & 1u) ^ 1u, abort_flag,
+                                                          p.status))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (one) {
 #pragma unroll
             for (int k = 0; k < kXSteps; ++k)  // 32 bytes on in each 128-byte row
               if (k == 0 || k < now)
@@ -663,6 +670,18 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) != 0; }
 
+// Whether n_m row blocks of 128 go to pairs of CTAs. A wave of CTAs alone takes 1.15 to
+// 1.4 times a wave of pairs (at one and two row blocks they are the same), so an odd
+// last block, which leaves half of a pair idle, can make the pairs slower. H=3584,
+// V=152064 / 32000 (us, alone / pairs): 384 rows 86 / 94 and 26.4 / 31.4, 640 rows 132 /
+// 136 and 37 / 35, 1152 rows 218 / 202, 2048 rows 438 / 314; 200 rows 65 / 63.
+bool mxfp4_pairs(int64_t n_m, int64_t n_n, int sms, int pairs) {
+  if (n_m < 2 || pairs < 1) return false;
+  const int64_t alone = (n_m * n_n + sms - 1) / sms;
+  const int64_t paired = ((n_m + 1) / 2 * n_n + pairs - 1) / pairs;
+  return alone * 6 >= paired * 5;
+}
+
 int launch_error(cudaError_t e, const char* what) {
   char msg[256];
   snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
@@ -769,9 +788,9 @@ extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidde
   int pairs = 0;
   cudaError_t e = mxfp4_setup(sms, &pairs);
   if (e != cudaSuccess) return launch_error(e, "4-bit logits");
-  // two row blocks or more go to pairs of CTAs
-  const bool pair = T > kXM && pairs > 0;
-  const int64_t n_m = ceil_div(T, pair ? 2 * kXM : kXM), n_n = ceil_div(V, kXN);
+  const int64_t n_n = ceil_div(V, kXN);
+  const bool pair = mxfp4_pairs(ceil_div(T, kXM), n_n, sms, pairs);
+  const int64_t n_m = ceil_div(T, pair ? 2 * kXM : kXM);
   const int64_t k_words = ceil_div(H, kXAtomCols) * (kXAtomBytes / 4);
   Mxfp4Params p{};
   p.T = static_cast<int>(T);
