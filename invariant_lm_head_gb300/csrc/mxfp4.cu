@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "lmhead.h"
 #include "out_rows.cuh"
 #include "ptx.cuh"
@@ -84,8 +85,10 @@ __global__ void __launch_bounds__(kXThreads, 3)
     quantize_mxfp4_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
                           int64_t kb, int64_t n_tiles, uint8_t* __restrict__ q,
                           uint8_t* __restrict__ scale) {
+  ahead_done();
   const int sub = threadIdx.x & 15, r32 = threadIdx.x >> 4;
   for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
+    if (b + gridDim.x >= n_tiles) nearly_done();
     const int64_t rb = b / kb;
     const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
     const int64_t row0 = rb * kXAtomRows + r32;
@@ -130,8 +133,10 @@ __global__ void __launch_bounds__(kXThreads, 3)
     dequantize_mxfp4_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ scale,
                             int64_t rows, int64_t cols, int64_t kb, int64_t n_tiles,
                             uint16_t* __restrict__ out, int64_t ld) {
+  ahead_done();
   const int sub = threadIdx.x & 15, r32 = threadIdx.x >> 4;
   for (int64_t b = blockIdx.x; b < n_tiles; b += gridDim.x) {
+    if (b + gridDim.x >= n_tiles) nearly_done();
     const int64_t rb = b / kb;
     const int64_t col = (b - rb * kb) * kXAtomCols + sub * 8;
     const int64_t row0 = rb * kXAtomRows + r32;
@@ -392,6 +397,7 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   long long issued = 0;  // stages loaded by this CTA
+  ahead_done();
 
   // Warps 0 and 1 run their loops as whole warps and act by one elected lane: with the
   // loops in one lane's branch the issue of a stage's 11 instructions took 1450 cycles
@@ -437,6 +443,7 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
         }
       }
     }
+    nearly_done();
     if constexpr (kPair) {
       if (rank != 0 && one)  // CTA 0 waits for this CTA's copies too, at the end
         st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_issued)), 0),
@@ -738,8 +745,8 @@ extern "C" int lmhead_quantize_mxfp4(const uint16_t* x, int64_t rows, int64_t co
   {
     KernelTimer timer(K_QUANTIZE_MXFP4, st);
     const int grid = static_cast<int>(tiles < kXGridPerSm * sms ? tiles : kXGridPerSm * sms);
-    quantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(x, rows, cols, ld, kb, tiles, q, scale);
-    e = cudaGetLastError();
+    e = launch_early(quantize_mxfp4_kernel, grid, kXThreads, 0, st, 1, x, rows, cols, ld, kb, tiles,
+                     q, scale);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) return launch_error(e, "4-bit quantisation");
@@ -768,9 +775,8 @@ extern "C" int lmhead_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, i
   {
     KernelTimer timer(K_DEQUANTIZE_MXFP4, st);
     const int grid = static_cast<int>(tiles < kXGridPerSm * sms ? tiles : kXGridPerSm * sms);
-    dequantize_mxfp4_kernel<<<grid, kXThreads, 0, st>>>(q, scale, rows, cols, kb, tiles, out,
-                                                        ld_out);
-    e = cudaGetLastError();
+    e = launch_early(dequantize_mxfp4_kernel, grid, kXThreads, 0, st, 1, q, scale, rows, cols, kb,
+                     tiles, out, ld_out);
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) return launch_error(e, "4-bit dequantisation");
@@ -837,12 +843,13 @@ extern "C" int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidde
     KernelTimer timer(K_LOGITS_MXFP4, st);
     if (pair) {
       const int grid = 2 * (p.n_units < pairs ? p.n_units : pairs);
-      logits_mxfp4_pair_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, p);
+      e = launch_early(logits_mxfp4_pair_kernel, grid, kXLogitsThreads, kXSmemBytes, st, 1, ta, tb,
+                       tsa, tsb, p);
     } else {
       const int grid = p.n_units < sms ? p.n_units : sms;
-      logits_mxfp4_kernel<<<grid, kXLogitsThreads, kXSmemBytes, st>>>(ta, tb, tsa, tsb, p);
+      e = launch_early(logits_mxfp4_kernel, grid, kXLogitsThreads, kXSmemBytes, st, 1, ta, tb, tsa,
+                       tsb, p);
     }
-    e = cudaGetLastError();
     if (e == cudaSuccess) note_launch();
   }
   if (e != cudaSuccess) return launch_error(e, "4-bit logits");

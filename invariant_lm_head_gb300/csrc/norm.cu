@@ -24,6 +24,7 @@
 
 #include "fp8_block.cuh"
 #include "internal.h"
+#include "launch.cuh"
 #include "lmhead.h"
 #include "out_rows.cuh"
 #include "ptx.cuh"
@@ -83,6 +84,7 @@ template <int kU, int kD>
 __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t ahead[];
   __shared__ float part[3][32];
+  ahead_done();
   const int sub = threadIdx.x & (kNLanes - 1);
   int col[kU];
   uint4 w[kU][2];
@@ -122,6 +124,7 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
   }
   int parity = 0, depth = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, parity ^= 1) {
+    if (row + gridDim.x >= p.rows) nearly_done();
     fetch(row + static_cast<int64_t>(kD - 1) * gridDim.x, depth == 0 ? kD - 1 : depth - 1);
     copies_wait<kD - 1>();
     uint4 v[kU][2];
@@ -264,8 +267,7 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   }
   const int64_t most = static_cast<int64_t>(sms) * n;  // a persistent grid
   const unsigned grid = static_cast<unsigned>(p.rows < most ? p.rows : most);
-  norm_fp8_kernel<kU, kD><<<grid, threads, bytes, st>>>(p);
-  return cudaGetLastError();
+  return launch_early(norm_fp8_kernel<kU, kD>, grid, threads, bytes, st, 1, p);
 }
 
 }  // namespace

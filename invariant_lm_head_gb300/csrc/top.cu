@@ -39,6 +39,7 @@
 #include <cuda_bf16.h>
 
 #include "internal.h"
+#include "launch.cuh"
 #include "lmhead.h"
 #include "online_softmax.cuh"
 #include "ptx.cuh"
@@ -441,12 +442,13 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   const int n_mine = static_cast<int>(min(static_cast<int64_t>(n_vec - first), static_cast<int64_t>(per) * kMine));
   const int slices = (n_mine + per - 1) / per;
 
+  if (kC > 1) row_arrive();  // this CTA runs: see the wait below
+  ahead_done();
   if (threadIdx.x == 0) {
     // one reading of the temperature decides every thread's way
     sh.temperature = p.row_t ? p.row_t[row] : p.temperature;
     sh.n_hit = sh.n_list = 0;
   }
-  if (kC > 1) row_arrive();  // this CTA has begun: see the wait below
 
   const Ring<kAligned> ring(x, p.V, smem_u32(ring_smem), first);
   int ahead = 0, ahead_end = min(per, n_mine);  // the next group to fetch, its slice's end
@@ -519,6 +521,7 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
         merge_slice(two, one);
     }
   }
+  nearly_done();
   mine = slices & 1 ? one : none;
   if (slices >= 2) {
     merge_slice(two, mine);
@@ -728,24 +731,8 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     done[dev].store(true, std::memory_order_release);
   }
-  if constexpr (kC == 1) {
-    top_logprobs_kernel<kC, kAligned>
-        <<<static_cast<unsigned>(p.T), kPThreads, kBytes, st>>>(p);
-    return cudaGetLastError();
-  }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.T * kC));
-  cfg.blockDim = dim3(kPThreads);
-  cfg.dynamicSmemBytes = kBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kC;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, top_logprobs_kernel<kC, kAligned>, p);
+  return launch_early(top_logprobs_kernel<kC, kAligned>, static_cast<unsigned>(p.T * kC), kPThreads,
+                      kBytes, st, kC, p);
 }
 
 // CTAs of a row: as many as leave each an SM's share of the batch, and no more than
