@@ -79,7 +79,7 @@ static_assert(kXRows == 4, "the four rows that share 16 bytes of scales");
 // A CTA takes 128 rows x 128 columns: 16 lanes a row (16 bytes each), four rows a thread,
 // all loaded before the first is used. A block is four lanes; a row's four scales meet
 // in one word, and the words of a thread's four rows are the 16 bytes that they share.
-// Bound by HBM: 212 us for a weight of 152064 x 3584, 6.5 TB/s, 0.97 of the copy rate
+// Bound by HBM: 209 us for a weight of 152064 x 3584, 6.6 TB/s, 0.99 of the copy rate
 // (with 256 threads of eight rows 250 us). 64 x 3584 takes 4 us, most of it one load.
 __global__ void __launch_bounds__(kXThreads, 3)
     quantize_mxfp4_kernel(const uint16_t* __restrict__ x, int64_t rows, int64_t cols, int64_t ld,
@@ -314,15 +314,15 @@ __device__ __forceinline__ void store_box(uint16_t* row, int col, int n, const u
 // both), the others turn finished tiles to bf16. Tokens are the MMA's rows, the
 // vocabulary its columns.
 //
-// What bounds it. A short batch reads the weight once: 48 us at T=1 H=3584 V=152064, 6.0
-// TB/s, 0.90 of the copy rate; 16.7 us at T=64 H=4096 V=32000, where launch, first loads
-// and the single wave's end take 6 us beside 10 of bytes. A long batch takes 317 us at
-// T=2048 H=3584 V=152064 (7.0 PFLOP/s; 330-345, 6.6, in a loop that runs into the power
-// cap): MMAs and scale copies alone 259, with the loads 272 (17.5 TB/s out of L2, near
-// what it gives), with the stores on top 317, which share L2 and HBM with the loads. Of
-// the 259 us 218 are MMAs at their rate (128 cycles for 256 x 256 x 64 of a pair) and the
-// rest the gap between two tiles, about 1000 cycles: the accumulators share columns, and
-// the next tile's MMAs wait until those are read.
+// What bounds it. A short batch reads the weight once: 45 us at T=1 H=3584 V=152064, 6.4
+// TB/s, 0.95 of the copy rate; 14.8 us at T=64 H=4096 V=32000, where first loads and the
+// single wave's end take 5 us beside 10 of bytes. A long batch takes 314 us at T=2048
+// H=3584 V=152064 (7.1 PFLOP/s; 330, 6.8, in a loop that runs into the power cap): MMAs
+// and scale copies alone take 259, with the loads 272 (17.5 TB/s out of L2, near what it
+// gives), and the stores, which share L2 and HBM with the loads, the rest. Of the 259 us
+// 218 are MMAs at their rate (128 cycles for 256 x 256 x 64 of a pair) and the others the
+// gap between two tiles, about 1000 cycles: the accumulators share columns, and the next
+// tile's MMAs wait until those are read.
 // Tried and slower at T=2048: eight warps for the finished tiles (349 us), groups of 4
 // and 2 row blocks in the raster (340, 365), boxes of shared memory and TMA stores for
 // the output (as fast there, 18.1 us at T=64).

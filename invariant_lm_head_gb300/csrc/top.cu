@@ -22,12 +22,12 @@
 // Batch invariance: the slices and the order of every sum depend on V alone.
 //
 // What bounds it. Many rows: the issue of instructions (47000 a row of 152064 in warps,
-// 65 % of the slots) beside HBM: 64 us for 1024 rows, 4.8 TB/s, 0.72 of the copy rate;
+// 65 % of the slots) beside HBM: 63 us for 1024 rows, 4.9 TB/s, 0.74 of the copy rate;
 // 1024 rows are 1.7 times what the SMs hold at four CTAs each, and the second wave does
-// not fill them. Few rows: a chain of short steps, 11.5 us at one row of 152064 on four
+// not fill them. Few rows: a chain of short steps, 9.0 us at one row of 152064 on four
 // CTAs (9000 cycles to read and fold, 1700 to bisect the keys, 3000 for the second look,
-// 1100 for the cluster, 3500 for sums and lists).
-// Tried and slower at 1024 rows of 152064 (64 us): 512 threads a CTA (119), 384 (78),
+// 1100 for the cluster, 3500 for sums and lists, the kernel behind under way meanwhile).
+// Tried and slower at 1024 rows of 152064 (64 us then): 512 threads a CTA (119), 384 (78),
 // five vectors a group (74: spills), two CTAs a row (77), three CTAs an SM and three
 // groups ahead (70), eight slices (68).
 #include <atomic>
@@ -521,7 +521,6 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
         merge_slice(two, one);
     }
   }
-  nearly_done();
   mine = slices & 1 ? one : none;
   if (slices >= 2) {
     merge_slice(two, mine);
@@ -610,6 +609,7 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
       for (int k = 0; k < kC; k += 2 * by) merge_slice(part[k], part[k + by]);
     mine = part[0];
   }
+  nearly_done();
   // then the threads, all scaled to the row's maximum: within each warp, and the warps in order
   float m = mine.m, most = mine.most;
 #pragma unroll
