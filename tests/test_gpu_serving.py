@@ -895,3 +895,65 @@ def test_example_runs(kind):
                         "--steps", "8"], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert "tokens/s" in r.stdout
+
+
+@pytest.mark.parametrize("where", ["stream", "graph"])
+def test_calls_that_depend_on_each_other_back_to_back(where):
+    # each call begins while the one ahead ends: it must see all that one wrote, and
+    # must not write what that one still reads
+    import torch
+
+    B, H, V = 300, 512, 9001
+    h, r0, w, g = step_inputs(B, H, V)
+    r, q, s = r0.clone(), *lmh.lmhead_quantize_mxfp4(h)
+    wq, ws = lmh.lmhead_quantize_mxfp4(w)
+    x = h.clone()
+    logits = torch.empty(B, 9008, dtype=torch.bfloat16, device=dev())[:, :V]
+    n = 40
+
+    def chain(sync):
+        # the residual in place, a 4-bit round trip of it as the next input, its logits
+        # into one buffer, and what is read there
+        wait = torch.cuda.synchronize if sync else lambda: None
+        out = []
+        for _ in range(n):
+            nq, ns, _ = lmh.lmhead_rmsnorm_fp8(x, g, r, out_residual=r)
+            wait()
+            lmh.lmhead_quantize_mxfp4(r, out=q, out_scale=s)
+            wait()
+            lmh.lmhead_dequantize_mxfp4(q, s, out=x)
+            wait()
+            x.mul_(-0.25)
+            wait()
+            lmh.lmhead_logits_mxfp4(q, s, wq, ws, out_logits=logits)
+            wait()
+            out += [nq, ns, *lmh.lmhead_top_logprobs(logits, None, 0.8, top=4)[1:]]
+            wait()
+        return out
+
+    def start():
+        r.copy_(r0)
+        x.copy_(h)
+
+    want = [t.clone() for t in chain(True)]
+    end = r.clone()
+    assert not torch.equal(end, r0)
+    if where == "stream":
+        for _ in range(3):
+            start()
+            got = chain(False)
+            torch.cuda.synchronize()
+            same(got, want)
+            assert torch.equal(r, end)
+        return
+    graph = torch.cuda.CUDAGraph()
+    start()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        got = chain(False)
+    for _ in range(3):
+        start()
+        graph.replay()
+        torch.cuda.synchronize()
+        same(got, want)
+        assert torch.equal(r, end)
