@@ -3,8 +3,11 @@
 //
 // For a row x with temperature t (0 counts as 1), z = x / t, m = max z,
 //   logprob[i] = z[i] - m - log sum exp(z - m),   entropy = log sum - sum e (z - m) / sum,
-// one pass with a running maximum (base 2: y = x * c, c = log2(e) / t rounded once, and
-// y - m one FMA). Masked logits (-inf, NaN) weigh nothing, in the entropy either.
+// one pass with a running maximum of x: e = 2^((x - max x) * c) with c = log2(e) / t
+// rounded once, so that the largest logit's weight is 1 exactly (with the maximum of x * c
+// in its place it is off by that product's rounding, and the log-prob of a likely token,
+// a number near 0, by several times as much). Masked logits (-inf, NaN) weigh nothing, in
+// the entropy either.
 //
 // The alternatives are the first n in descending order of x, equal ones by index. The
 // pass over the row only keeps each thread's largest value: the n-th largest of those is
@@ -34,7 +37,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
-#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -75,10 +77,12 @@ struct TopParams {
   float* top_logprob;
 };
 
-// A slice's sums and its largest logit (-inf: all masked); stored whole by 16 bytes.
+// A slice's largest logit m (-inf: all masked) and its sums s = sum e, u = sum e * (x - m);
+// stored whole by 16 bytes.
 struct alignas(16) SliceStat {
-  float m, s, u, most;
+  float m, s, u;
 };
+constexpr float kPFar = -1e28f;  // what differences are cut to where their weight is 0 (c >= 1e-25)
 
 template <int kC>
 struct TopShared {
@@ -87,7 +91,7 @@ struct TopShared {
   int n_merged[kC];                  // and how many they are
   int n_hit, n_list;
   SliceStat warp[kPWarps];
-  float2 top[kPWarps];               // the warps' largest y and logit
+  float top[kPWarps];                // the warps' largest logits
   uint16_t key[kPSlices / kC][kPThreads];  // a thread's largest value in each slice
   uint16_t hit[kPThreads * kPSlices / kC];
   uint32_t count[kPWarps];
@@ -153,11 +157,65 @@ __device__ __forceinline__ __nv_bfloat162 bf2(uint32_t w) {
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
 }
 
-// Folds kV vectors into the state; `most` keeps the largest value. A masked value, or one
-// so far below the maximum that its shift leaves fp32, makes the plain sum of e * d a
-// NaN; the shifts are then cut to kPFloor.
+// Scales sums to the maximum m (their own or a larger one); those of nothing stay zero.
+__device__ __forceinline__ void rescale(SliceStat& a, float m, float c) {
+  const float d = fmaxf(__fsub_rn(a.m, m), kPFar);
+  const float e = ex2(fmaxf(__fmul_rn(d, c), kPFloor));
+  a.u = __fmul_rn(e, __fmaf_rn(a.s, d, a.u));
+  a.s = __fmul_rn(a.s, e);
+  a.m = m;
+}
+
+// a <- a (+) b. An empty side leaves the other's bits.
+__device__ __forceinline__ void merge_slice(SliceStat& a, SliceStat b, float c) {
+  const float m = fmaxf(a.m, b.m);
+  rescale(a, m, c);
+  rescale(b, m, c);
+  a.s = __fadd_rn(a.s, b.s);
+  a.u = __fadd_rn(a.u, b.u);
+}
+
+// One pair of values into the packed sums.
+template <bool kCut>
+__device__ __forceinline__ void add_pair(uint32_t pair, f32x2 nm2, f32x2 c2, f32x2& s2, f32x2& u2) {
+  f32x2 d2 = f2_add(bf16x2_f2(pair), nm2);
+  float ya, yb;
+  f2_unpack(f2_mul(d2, c2), ya, yb);
+  if (kCut) {  // a masked value's weight is 0, and its difference finite
+    float da, db;
+    f2_unpack(d2, da, db);
+    d2 = f2_pack(fmaxf(da, kPFar), fmaxf(db, kPFar));  // a NaN too
+    ya = fmaxf(ya, kPFloor);
+    yb = fmaxf(yb, kPFloor);
+  }
+  const f32x2 e2 = f2_pack(ex2(ya), ex2(yb));
+  s2 = f2_add(s2, e2);
+  u2 = f2_fma(e2, d2, u2);
+}
+
+__device__ __forceinline__ float2 sum_pairs(f32x2 s2, f32x2 u2) {
+  float s0, s1, u0, u1;
+  f2_unpack(s2, s0, s1);
+  f2_unpack(u2, u0, u1);
+  return make_float2(__fadd_rn(s0, s1), __fadd_rn(u0, u1));
+}
+
+// A group's sums where some are masked. Out of line: in line its values, kept with those
+// of the usual sums, cost registers that every group would spill.
+__device__ __noinline__ float2 cut_sums(uint4 a, uint4 b, uint4 g, uint4 h, float m, float c) {
+  const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-m, -m);
+  f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
+  const uint32_t w[16] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w,
+                          g.x, g.y, g.z, g.w, h.x, h.y, h.z, h.w};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) add_pair<true>(w[i], nm2, c2, s2, u2);
+  return sum_pairs(s2, u2);
+}
+
+// Folds kV vectors (of w's four, the others masked) into the state. A masked value makes
+// the plain sum of e * (x - m) a NaN.
 template <int kV>
-__device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w, float c) {
+__device__ __forceinline__ void fold(SliceStat& st, const uint4 (&w)[kPGroup], float c) {
   __nv_bfloat162 hi = bf2(w[0].x);  // passes over a NaN
 #pragma unroll
   for (int k = 0; k < kV; ++k) {
@@ -165,64 +223,22 @@ __device__ __forceinline__ void fold(OnlineStat& st, float& most, const uint4* w
 #pragma unroll
     for (int q = 0; q < 4; ++q) hi = __hmax2(hi, bf2(ws[q]));
   }
-  // (the largest of two NaN is one: a masked value)
-  const float gmax = fmaxf(fmaxf(__low2float(hi), __high2float(hi)), -INFINITY);
-  most = fmaxf(most, gmax);
-  // never -inf, from which a finite x * c would be infinitely far
-  const float mn = fmaxf(fmaxf(st.m, __fmul_rn(gmax, c)), -3.402823466e38f);
-  const float d0 = fmaxf(__fsub_rn(st.m, mn), kPFloor);
-  const float a = ex2(d0);
-  const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-mn, -mn);
-  float s, u;
-  auto sums = [&](auto cut) {
-    f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
+  // (the larger of two NaN is one: a masked value)
+  const float m = fmaxf(st.m, fmaxf(__low2float(hi), __high2float(hi)));
+  rescale(st, m, c);
+  const f32x2 c2 = f2_pack(c, c), nm2 = f2_pack(-m, -m);
+  f32x2 s2 = f2_pack(0.f, 0.f), u2 = s2;
 #pragma unroll
-    for (int k = 0; k < kV; ++k) {
-      const uint32_t ws[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float da, db;
-        f2_unpack(f2_fma(bf16x2_f2(ws[q]), c2, nm2), da, db);
-        if (decltype(cut)::value) {
-          da = fmaxf(da, kPFloor);  // a NaN too
-          db = fmaxf(db, kPFloor);
-        }
-        const f32x2 e2 = f2_pack(ex2(da), ex2(db));
-        s2 = f2_add(s2, e2);
-        u2 = f2_fma(e2, f2_pack(da, db), u2);
-      }
-    }
-    float lo, up;
-    f2_unpack(s2, lo, up);
-    s = __fadd_rn(lo, up);
-    f2_unpack(u2, lo, up);
-    u = __fadd_rn(lo, up);
-  };
-  sums(std::false_type{});
-  if (!(fabsf(u) <= 3.402823466e38f)) sums(std::true_type{});
-  st.u = __fadd_rn(__fmul_rn(a, __fmaf_rn(st.s, d0, st.u)), u);
-  st.s = __fadd_rn(__fmul_rn(st.s, a), s);
-  st.m = mn;
-}
-
-// Scales a slice's sums to the maximum m (its own or a larger one); an empty slice's
-// stay zero.
-__device__ __forceinline__ void rescale(SliceStat& a, float m) {
-  const float d = fmaxf(__fsub_rn(a.m, m), kPFloor);
-  const float e = ex2(d);
-  a.u = __fmul_rn(e, __fmaf_rn(a.s, d, a.u));
-  a.s = __fmul_rn(a.s, e);
-  a.m = m;
-}
-
-// a <- a (+) b. An empty side leaves the other's bits.
-__device__ __forceinline__ void merge_slice(SliceStat& a, SliceStat b) {
-  const float m = fmaxf(a.m, b.m);
-  rescale(a, m);
-  rescale(b, m);
-  a.s = __fadd_rn(a.s, b.s);
-  a.u = __fadd_rn(a.u, b.u);
-  a.most = fmaxf(a.most, b.most);
+  for (int k = 0; k < kV; ++k) {
+    add_pair<false>(w[k].x, nm2, c2, s2, u2);
+    add_pair<false>(w[k].y, nm2, c2, s2, u2);
+    add_pair<false>(w[k].z, nm2, c2, s2, u2);
+    add_pair<false>(w[k].w, nm2, c2, s2, u2);
+  }
+  float2 sums = sum_pairs(s2, u2);
+  if (!(fabsf(sums.y) <= 3.402823466e38f)) sums = cut_sums(w[0], w[1], w[2], w[3], m, c);
+  st.s = __fadd_rn(st.s, sums.x);
+  st.u = __fadd_rn(st.u, sums.y);
 }
 
 // How many values of the slice have a key of at least k, in every thread.
@@ -315,32 +331,35 @@ __device__ __noinline__ void list_by_bisection(Shared& sh, const uint16_t* row, 
   __syncthreads();
 }
 
-// z - max z where y = x * c is too large to be subtracted from.
-__device__ __forceinline__ float far_shift(float x, float most, float t) {
-  return x == most ? 0.f : __fdiv_rn(__fsub_rn(x, most), t);
+// z - max z.
+__device__ __forceinline__ float shift(float x, float most, float t) {
+  const float d = __fsub_rn(x, most);
+  if (x == most) return 0.f;
+  return d == -INFINITY ? __fsub_rn(__fdiv_rn(x, t), __fdiv_rn(most, t)) : __fdiv_rn(d, t);
 }
 
-// The sums of such a row: logits equal to the largest weigh 1. One CTA, in an order
-// fixed by V.
+// The sums (u in units of z) of a row whose differences, or their products with c, leave
+// fp32: logits equal to the largest weigh 1. One CTA, in an order fixed by V.
 template <class Shared>
 __device__ __noinline__ SliceStat sums_of_extremes(Shared& sh, const uint16_t* row, int64_t V,
                                                    float t, float most) {
   float s = 0.f, u = 0.f;
   for (int64_t i = threadIdx.x; i < V; i += kPThreads) {
-    const float x = __uint_as_float(static_cast<uint32_t>(row[i]) << 16);
-    const float d = fmaxf(__fmul_rn(far_shift(x, most, t), kLog2e), kPFloor);
-    const float e = ex2(d);
+    const uint32_t b = row[i];
+    if (order_key(b) == 0u) continue;
+    const float d = shift(__uint_as_float(b << 16), most, t);
+    const float e = ex2(fmaxf(__fmul_rn(d, kLog2e), kPFloor));
     s += e;
-    u += e * d;
+    u += e > 0.f ? e * d : 0.f;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, off);
     u += __shfl_xor_sync(0xffffffffu, u, off);
   }
-  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = SliceStat{0.f, s, u, most};
+  if ((threadIdx.x & 31) == 0) sh.warp[threadIdx.x >> 5] = SliceStat{most, s, u};
   __syncthreads();
-  SliceStat r{0.f, 0.f, 0.f, most};
+  SliceStat r{most, 0.f, 0.f};
   for (int w = 0; w < kPWarps; ++w) {
     r.s += sh.warp[w].s;
     r.u += sh.warp[w].u;
@@ -471,15 +490,14 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
 
   // The slices' sums as a binary tree: pairs, then all four. What is missing at the end
   // is empty, and leaves the rest as it is.
-  const SliceStat none{-INFINITY, 0.f, 0.f, -INFINITY};
+  const SliceStat none{-INFINITY, 0.f, 0.f};
   SliceStat one = none, two = none, mine = none;
   uint32_t top_key = 0;  // of this thread's values
   int depth = 0, v0 = 0;
 #pragma unroll 1
   for (int i = 0; i < slices; ++i) {
     const int end = min((i + 1) * per, n_mine);
-    OnlineStat st = stat_empty();
-    float most = -INFINITY;
+    mine = none;
 #pragma unroll 1
     for (; v0 < end; v0 += kStep) {
       fetch(depth == 0 ? kPDepth - 1 : depth - 1);
@@ -497,33 +515,32 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
         }
       }
       if (end - v0 > 3 * kPThreads)
-        fold<4>(st, most, w, c);
+        fold<4>(mine, w, c);
       else if (end - v0 > 2 * kPThreads)
-        fold<3>(st, most, w, c);
+        fold<3>(mine, w, c);
       else if (end - v0 > kPThreads)
-        fold<2>(st, most, w, c);
+        fold<2>(mine, w, c);
       else
-        fold<1>(st, most, w, c);
+        fold<1>(mine, w, c);
       if (++depth == kPDepth) depth = 0;
     }
     v0 = end;
-    const uint32_t key = order_key(__float_as_uint(most) >> 16);
+    const uint32_t key = order_key(__float_as_uint(mine.m) >> 16);
     sh.key[i][threadIdx.x] = static_cast<uint16_t>(key);
     top_key = max(top_key, key);
-    mine = SliceStat{st.m, st.s, st.u, most};
     if (!(i & 1)) {
       one = mine;
     } else {
-      merge_slice(one, mine);
+      merge_slice(one, mine, c);
       if (i == 1)
         two = one;
       else
-        merge_slice(two, one);
+        merge_slice(two, one, c);
     }
   }
   mine = slices & 1 ? one : none;
   if (slices >= 2) {
-    merge_slice(two, mine);
+    merge_slice(two, mine, c);
     mine = two;
   }
   // The first CTA's shared memory may be written once it runs; a CTA without a slice of
@@ -532,7 +549,7 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   if (kC > 1 && rank > 0) {
     const uint32_t at = first_cta<kC>(peer + (rank - 1) * kPThreads + threadIdx.x);
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(mine.m),
-                 "f"(mine.s), "f"(mine.u), "f"(mine.most)
+                 "f"(mine.s), "f"(mine.u), "f"(0.f)
                  : "memory");
   }
   __syncthreads();
@@ -606,25 +623,20 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
 #pragma unroll
     for (int by = 1; by < kC; by *= 2)
 #pragma unroll
-      for (int k = 0; k < kC; k += 2 * by) merge_slice(part[k], part[k + by]);
+      for (int k = 0; k < kC; k += 2 * by) merge_slice(part[k], part[k + by], c);
     mine = part[0];
   }
   nearly_done();
   // then the threads, all scaled to the row's maximum: within each warp, and the warps in order
-  float m = mine.m, most = mine.most;
+  float most = mine.m;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  for (int off = 16; off > 0; off >>= 1)
     most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-  }
-  if (lane == 0) sh.top[warp] = make_float2(m, most);
+  if (lane == 0) sh.top[warp] = most;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kPWarps; ++w) {
-    m = fmaxf(m, sh.top[w].x);
-    most = fmaxf(most, sh.top[w].y);
-  }
-  rescale(mine, m);
+  for (int w = 0; w < kPWarps; ++w) most = fmaxf(most, sh.top[w]);
+  rescale(mine, most, c);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     mine.s = __fadd_rn(mine.s, __shfl_xor_sync(0xffffffffu, mine.s, off));
@@ -632,37 +644,33 @@ __global__ void __launch_bounds__(kPThreads, 4) top_logprobs_kernel(const TopPar
   }
   if (lane == 0) sh.warp[warp] = mine;
   __syncthreads();
-  SliceStat all{m, 0.f, 0.f, most};
+  SliceStat all{most, 0.f, 0.f};
 #pragma unroll
   for (int w = 0; w < kPWarps; ++w) {
     all.s = __fadd_rn(all.s, sh.warp[w].s);
     all.u = __fadd_rn(all.u, sh.warp[w].u);
   }
-
-  // The largest y itself is shifted by its product's rounding, up to 2^-4 at 2^20; past
-  // that (or where the largest logit is +inf) the row is summed again.
-  const bool extreme = all.most > -INFINITY && !(fabsf(__fmul_rn(all.most, c)) <= 0x1p20f);
-  if (extreme) {
+  all.u = __fdiv_rn(all.u, t);
+  // where differences or their products may leave fp32 (or the largest logit is +inf) the
+  // row is summed again
+  const bool nothing = !(most > -INFINITY);
+  if (!nothing && !(most <= 1e36f && c >= 1e-25f && c <= 3.402823466e38f)) {
     __syncthreads();
-    all = sums_of_extremes(sh, x, p.V, t, all.most);
+    all = sums_of_extremes(sh, x, p.V, t, most);
   }
-  const bool nothing = !(all.most > -INFINITY);
-  const float l2s = log2f(all.s);
+  const float lse = __fmul_rn(kLn2, log2f(all.s));  // of z - max z
   const float bad = __int_as_float(0x7fffffff);
   auto logprob = [&](float v) -> float {
     if (!valid_t) return bad;
     if (nothing || !(v > -INFINITY)) return -INFINITY;  // a masked one
-    const float d = __fmaf_rn(v, c, -all.m);
-    if (extreme || d == -INFINITY)  // in base e what base 2 may not hold
-      return __fsub_rn(far_shift(v, all.most, t), __fmul_rn(kLn2, l2s));
-    return __fmul_rn(kLn2, __fsub_rn(d, l2s));
+    return __fsub_rn(shift(v, most, t), lse);
   };
   // the last threads take the tokens, the first ones the lists
   const int back = kPThreads - 1 - static_cast<int>(threadIdx.x);
   if (back == 0 && p.out_entropy)
     p.out_entropy[row] = !valid_t ? bad
                          : nothing ? 0.f
-                                   : __fmul_rn(kLn2, __fsub_rn(l2s, __fdiv_rn(all.u, all.s)));
+                                   : __fsub_rn(lse, __fdiv_rn(all.u, all.s));
   for (int i = back; i < p.n_tokens; i += kPThreads) {
     const int32_t id = p.tokens[row * p.n_tokens + i];
     float lp = valid_t ? 0.f : bad;
