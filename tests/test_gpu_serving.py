@@ -957,3 +957,45 @@ def test_calls_that_depend_on_each_other_back_to_back(where):
         torch.cuda.synchronize()
         same(got, want)
         assert torch.equal(r, end)
+
+
+@pytest.mark.parametrize("where", ["streams", "graph"])
+def test_calls_behind_two_streams(where):
+    # a call that begins early on one stream also waits for what it was told to on another
+    import torch
+
+    x = [to_dev_bf16(W.random_bf16(60 + i, (300, 512), 1.0)) for i in range(2)]
+    w = [to_dev_bf16(W.random_bf16(70 + i, (40000, 512), 0.05)) for i in range(2)]
+    want = [lmh.lmhead_logits_mxfp4(*lmh.lmhead_quantize_mxfp4(a), *lmh.lmhead_quantize_mxfp4(b))
+            for a, b in zip(x, w)]
+    h, m = torch.empty_like(x[0]), torch.empty_like(w[0])
+    hq, wq = lmh.lmhead_quantize_mxfp4(x[0]), lmh.lmhead_quantize_mxfp4(w[0])
+    out = torch.empty_like(want[0])
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            lmh.lmhead_quantize_mxfp4(m, out=wq[0], out_scale=wq[1])
+        lmh.lmhead_quantize_mxfp4(h, out=hq[0], out_scale=hq[1])
+        torch.cuda.current_stream().wait_stream(side)
+        lmh.lmhead_logits_mxfp4(*hq, *wq, out_logits=out)
+        return lmh.lmhead_top_logprobs(out, None, 1.0, top=3)
+
+    tops = [lmh.lmhead_top_logprobs(v, None, 1.0, top=3) for v in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    if where == "graph":
+        with torch.cuda.graph(graph):
+            got = step()
+    for i in range(30):
+        with torch.cuda.stream(main):
+            h.copy_(x[i % 2])
+            m.copy_(w[i % 2])
+            if where == "graph":
+                graph.replay()
+            else:
+                got = step()
+        torch.cuda.synchronize()
+        same((out,), (want[i % 2],))
+        same(got, tops[i % 2])
