@@ -25,14 +25,15 @@
 // Batch invariance: the slices and the order of every sum depend on V alone.
 //
 // What bounds it. Many rows: the issue of instructions (47000 a row of 152064 in warps,
-// 65 % of the slots) beside HBM: 63 us for 1024 rows, 4.9 TB/s, 0.74 of the copy rate;
+// 65 % of the slots) beside HBM: 64 us for 1024 rows, 4.8 TB/s, 0.72 of the copy rate;
 // 1024 rows are 1.7 times what the SMs hold at four CTAs each, and the second wave does
 // not fill them. Few rows: a chain of short steps, 9.0 us at one row of 152064 on four
 // CTAs (9000 cycles to read and fold, 1700 to bisect the keys, 3000 for the second look,
 // 1100 for the cluster, 3500 for sums and lists, the kernel behind under way meanwhile).
 // Tried and slower at 1024 rows of 152064 (64 us then): 512 threads a CTA (119), 384 (78),
 // five vectors a group (74: spills), two CTAs a row (77), three CTAs an SM and three
-// groups ahead (70), eight slices (68).
+// groups ahead (70), eight slices (68), each thread's largest value kept for 32 values at
+// a time, for a shorter second look (70), the keys bisected two bits at a time (65).
 #include <atomic>
 #include <cmath>
 #include <cstdint>
