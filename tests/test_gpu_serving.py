@@ -544,6 +544,32 @@ def test_top_ties_go_by_index(V, kind):
     check_top(x, 128, 0.5)
 
 
+@pytest.mark.parametrize("n", [1, 20, 128])
+@pytest.mark.parametrize("V", [9001, 152064])
+def test_top_of_crowded_levels(V, n):
+    # more equal logits than a list holds, and the few above them where a search that
+    # stops early would miss them; the n-th on the crowded level, and on one above it
+    x = np.full((7, V), -3.0, np.float32)
+    x[0, -5:] = 2.0, 1.0, 5.0, 1.0, 4.0
+    x[1] = LOWEST
+    x[1, -3:] = LOWEST / 2, 0.0, LOWEST / 4
+    x[2, V // 2:] = -2.5  # a level of its own above the first
+    x[2, -n // 2 - 1:] = 7.0
+    x[3, ::7] = -2.984375  # the next number of the type
+    x[4, ::7] = -2.984375
+    x[4, -n:] = 8.0
+    x[5] = -np.inf
+    x[5, V // 3:V // 3 + 2000] = -1e30  # the only ones not masked
+    x[6, np.random.default_rng(V).permutation(V)[:V // 2]] = -np.inf
+    ids = np.array([[0, V - 1]] * 7, np.int32)
+    check_top(x, n, 1.0, ids)
+    logits = to_dev_bf16(W.f32_to_bf16_bits(x))
+    many = lmh.lmhead_top_logprobs(logits.repeat(160, 1), to_dev(ids).repeat(160, 1), top=n)
+    one = lmh.lmhead_top_logprobs(logits, to_dev(ids), top=n)
+    for a, b in zip(many, one):
+        assert all((a[i:i + 7] == b).all() for i in (0, 7 * 80, 7 * 159))
+
+
 @pytest.mark.parametrize("V", [200, 9000, 70000])
 def test_top_masks(V):
     g = np.random.default_rng(V)
