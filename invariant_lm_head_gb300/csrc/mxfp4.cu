@@ -574,10 +574,14 @@ __device__ __forceinline__ void logits_mxfp4_body(const CUtensorMap& tmA, const 
 #pragma unroll 1
         for (int i = kXShared; i < kXBoxes; ++i) {
           const int b = (first + i) & (kXBoxes - 1);
+          // the stores part the lanes (rows past T, the vocabulary's end), and TMEM is read
+          // by whole warps only
+          __syncwarp();
           tmem_ld32_issue(src + b * kXBox, d0);
           tmem_ld_wait(d0);
           store_box(o, b * kXBox, n_cols, d0, p.wide);
         }
+        __syncwarp();  // and so is the next tile
         continue;
       }
       // rows at any address leave through shared memory, half a tile's columns at a time
