@@ -7,8 +7,10 @@ import numpy as np
 import pytest
 
 import invariant_lm_head_gb300 as lmh
-from helpers import dev
-from test_gpu_serving import check_logits, operands
+import workloads as W
+from helpers import dev, to_dev
+from oracle import serving as o
+from test_gpu_serving import LOWEST, check_logits, logit_rows, near, operands, same
 
 pytestmark = pytest.mark.gpu
 
@@ -34,3 +36,94 @@ def test_logits_where_the_lanes_of_a_warp_part(T, V, step):
     check_logits(out, *ops)
     assert (buf[:, V:] == 7.0).all()
     lmh.lmhead_device_status()
+
+
+# ------------------------------------------------------------------ alternatives
+
+def rows_of_every_kind(T, V):
+    """(logits as bf16 values in fp32, temperatures, tokens): plain rows, and at the start
+    ties past the list, masks, infinities and temperatures far from 1."""
+    x, g = logit_rows(T + V, T, V)
+    x[0] = 0.25  # all equal
+    x[1] = LOWEST
+    x[1, V - 3:] = 2.0, 1.0, 1.0
+    x[2] = -np.inf
+    x[2, V - 1] = -4.0
+    x[3] = -np.inf
+    x[4, ::2] = np.nan
+    x[5, V - 6000:V - 2000] = 30.0  # the largest in one run, behind the middle
+    x[6, V - 9] = np.inf
+    x[7, [3, V // 2, V - 2]] = np.inf
+    x[8] *= np.float32(1e37)
+    x[12, g.random(V) < 0.98] = -np.inf
+    x[13, V // 4:] = -np.inf  # nothing behind the first quarter
+    x[14, :3 * V // 4] = np.nan  # nothing before the last
+    x[15, ::3] = -2.984375  # more on one level than a list holds, a few above
+    x[16] = np.round(x[16])
+    t = (0.5 + g.random(T)).astype(np.float32)
+    t[9], t[10], t[11], t[17] = 1e-30, 1e30, 0.0, 2e-39
+    ids = g.integers(0, V, (T, 3)).astype(np.int32)
+    ids[:20, 0] = V - 1
+    ids[3:6, 1] = -1, V, 2 ** 31 - 1
+    return W.bf16_bits_to_f32(W.f32_to_bf16_bits(x)), t, ids
+
+
+def batch_of_two_ctas(which):
+    """77, 100 and 152 rows where the device has 152 SMs: rows that two CTAs share."""
+    import torch
+
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return {"first": sms // 2 + 1, "middle": 2 * sms // 3, "last": sms}[which]
+
+
+@pytest.mark.parametrize("n", [1, 20, 128])
+@pytest.mark.parametrize("V", [32003, 70000, 152064])
+@pytest.mark.parametrize("which", ["first", "middle", "last"])
+def test_top_of_rows_that_two_ctas_share(which, V, n):
+    # against the formula; and the bits of the rows alone, in a batch of one CTA a row, and
+    # at addresses that are not on 16 bytes
+    import torch
+
+    T = batch_of_two_ctas(which)
+    x, t, ids = rows_of_every_kind(T, V)
+    lg = torch.from_numpy(x).to(dev()).to(torch.bfloat16)
+    ts, tokens = to_dev(t), to_dev(ids)
+    got = lmh.lmhead_top_logprobs(lg, tokens, ts, top=n)
+    lp, ent, tok, tlp = [v.cpu().numpy() for v in got]
+    for i in [*range(20), T // 2, T - 1]:
+        rlp, rent, rtok, rtlp = o.top_row(x[i], t[i], n, ids[i])
+        assert np.array_equal(tok[i], rtok), (i, tok[i], rtok)
+        near(tlp[i], rtlp)
+        near(lp[i], rlp)
+        assert abs(ent[i] - rent) <= 3e-6 * (2 + 2 * abs(rent)), i
+    for a, b in [(0, 12), (12, 40), (T - 1, T)]:
+        alone = lmh.lmhead_top_logprobs(lg[a:b], tokens[a:b], ts[a:b], top=n)
+        same(alone, [v[a:b] for v in got])
+    many = [v.repeat(6, *[1] * (v.dim() - 1)) for v in (lg, tokens, ts)]
+    whole = lmh.lmhead_top_logprobs(many[0], many[1], many[2], top=n)
+    for i in (0, 5):
+        same([v[i * T:(i + 1) * T] for v in whole], got)
+    for stride, off in [(V + 1, 1), (V + 5, 4)]:
+        flat = torch.full((off + T * stride,), 60.0, dtype=torch.bfloat16, device=dev())
+        odd = flat[off:].view(T, stride)[:, :V]
+        odd.copy_(lg)
+        same(lmh.lmhead_top_logprobs(odd, tokens, ts, top=n), got)
+    lmh.lmhead_device_status()
+
+
+@pytest.mark.parametrize("V", [32003, 152064])
+@pytest.mark.parametrize("T", [3, 100])
+def test_top_bad_temperatures_of_rows_that_ctas_share(T, V):
+    import torch
+
+    x, g = logit_rows(T, T, V)
+    lg = torch.from_numpy(x).to(torch.bfloat16).to(dev())
+    ids = to_dev(np.stack([g.integers(0, V, T), np.full(T, -1)], 1).astype(np.int32))
+    t = torch.ones(T, device=dev())
+    for bad in (-1.0, float("nan"), float("inf"), -float("inf")):
+        t[1::2] = bad
+        lp, ent, tok, tlp = lmh.lmhead_top_logprobs(lg, ids, t, top=30)
+        assert lp[1::2].isnan().all() and ent[1::2].isnan().all()
+        assert (tok[1::2] == -1).all() and tlp[1::2].isnan().all()
+        good = lmh.lmhead_top_logprobs(lg, ids, 1.0, top=30)
+        same([v[::2] for v in (lp, ent, tok, tlp)], [v[::2] for v in good])
