@@ -766,13 +766,25 @@ cudaError_t launch_top(const TopParams& p, cudaStream_t st) {
                       kBytes, st, kC, p);
 }
 
-// CTAs of a row: as many as leave each an SM's share of the batch, and no more than
-// there are slices with something in them.
+// CTAs of a row: 4 while the batch then needs no more than two an SM, else 2 likewise,
+// else 1; and of them more than half get a part of the row, whose slices are dealt out
+// whole, 4 / CTAs to each (so a row of two slices, V up to 16384, takes one). us at 1 / 2 /
+// 4 CTAs a row:
+//   rows      V=16000             V=32000             V=152064
+//     1    6.6   7.0   6.2     7.7   6.8   6.0    16.2  11.6   8.9
+//    48    6.7   7.3   7.0     8.2   7.3   7.1    17.5  12.7  11.4
+//    76    6.9   7.5   8.0     8.2   7.6   8.3    17.7  14.0  13.9
+//   100    7.0   8.6   8.8     8.3   8.7   9.0    18.8  15.5  15.5
+//   152    7.1   8.2  12.1     8.5   9.1  12.9    20.6  18.7  22.4
+//   256    9.1  11.3  16.0    11.5  11.1  16.7    25.7  24.2  30.8
+//   608   10.9  21.7  33.5    14.3  21.3  35.1    40.3  47.9  62.9
+// The bounds lose up to 0.8 us to the best of the three, but for 153 to 304 rows of the
+// largest vocabulary, where two CTAs would save 0.8 to 2.7.
 template <bool kAligned>
 cudaError_t launch_by_rows(const TopParams& p, int sms, cudaStream_t st) {
   int most = p.T * 4 <= 2 * sms ? 4 : p.T * 2 <= 2 * sms ? 2 : 1;
   const int64_t used = ((p.V + 7) / 8 + p.per - 1) / p.per;  // slices
-  while (most > 1 && most / 2 >= used) most /= 2;
+  while (most > 1 && (used * most + kPSlices - 1) / kPSlices <= most / 2) most /= 2;
   switch (most) {
     case 4: return launch_top<4, kAligned>(p, st);
     case 2: return launch_top<2, kAligned>(p, st);

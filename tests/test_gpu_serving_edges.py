@@ -3,6 +3,8 @@
 Tolerances are those of test_gpu_serving.py, where they are derived.
 """
 
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -127,3 +129,57 @@ def test_top_bad_temperatures_of_rows_that_ctas_share(T, V):
         assert (tok[1::2] == -1).all() and tlp[1::2].isnan().all()
         good = lmh.lmhead_top_logprobs(lg, ids, 1.0, top=30)
         same([v[::2] for v in (lp, ent, tok, tlp)], [v[::2] for v in good])
+
+
+class KernelNode(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_void_p), ("grid", ctypes.c_uint * 3), ("block", ctypes.c_uint * 3),
+                ("shared", ctypes.c_uint), ("params", ctypes.c_void_p), ("extra", ctypes.c_void_p),
+                ("kern", ctypes.c_void_p), ("ctx", ctypes.c_void_p)]
+
+
+def launched_grids(call):
+    """The grids of the kernels that a call launches, from a graph that it is captured into."""
+    import torch
+
+    cuda = ctypes.CDLL("libcuda.so.1")
+    stream, graph, n = torch.cuda.Stream(), ctypes.c_void_p(), ctypes.c_size_t(0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        handle = ctypes.c_void_p(stream.cuda_stream)
+        assert cuda.cuStreamBeginCapture_v2(handle, 2) == 0
+        try:
+            call()
+        finally:
+            assert cuda.cuStreamEndCapture(handle, ctypes.byref(graph)) == 0
+    assert cuda.cuGraphGetNodes(graph, None, ctypes.byref(n)) == 0
+    nodes, grids = (ctypes.c_void_p * n.value)(), []
+    assert cuda.cuGraphGetNodes(graph, nodes, ctypes.byref(n)) == 0
+    for node in nodes:
+        p = KernelNode()
+        assert cuda.cuGraphKernelNodeGetParams_v2(ctypes.c_void_p(node), ctypes.byref(p)) == 0
+        grids.append(tuple(p.grid))
+    assert cuda.cuGraphDestroy(graph) == 0
+    return grids
+
+
+@pytest.mark.parametrize("V", [5, 8192, 8193, 9001, 16000, 16384, 16385, 24576, 24577, 32003, 152064])
+@pytest.mark.parametrize("T", [1, 48, 100, 400])
+def test_top_launches_no_idle_half(T, V):
+    # of the CTAs that share a row, more than half have a part of it; the row's bits are
+    # those of any other batch
+    import torch
+
+    lg = torch.randn(T, V, device=dev(), generator=torch.Generator(device=dev()).manual_seed(V)).to(torch.bfloat16)
+    outs = dict(out_entropy=torch.empty(T, device=dev()),
+                out_top_token=torch.empty(T, 5, dtype=torch.int32, device=dev()),
+                out_top_logprob=torch.empty(T, 5, device=dev()))
+    lmh.lmhead_top_logprobs(lg, top=5, **outs)
+    got = [v.clone() for v in outs.values()]
+    grids = launched_grids(lambda: lmh.lmhead_top_logprobs(lg, top=5, **outs))
+    assert len(grids) == 1 and grids[0][0] % T == 0
+    ctas = grids[0][0] // T
+    assert ctas in (1, 2, 4)
+    vectors = -(-V // 8)  # a slice: a quarter of the row in whole runs of 32, 1024 at least
+    slices = -(-vectors // max(1024, -(-(-(-vectors // 4)) // 32) * 32))
+    assert ctas == 1 or 2 * -(-slices * ctas // 4) > ctas
+    same(lmh.lmhead_top_logprobs(lg[T - 1:], top=5)[1:], [v[T - 1:] for v in got])
