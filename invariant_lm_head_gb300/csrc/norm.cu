@@ -43,6 +43,7 @@ struct NormParams {
   int64_t rows, ld_x, ld_res, ld_out;
   int cols, kb;
   float eps;
+  float low;  // smaller sums of squares are taken again in smaller units
   uint16_t* out_residual;
   uint8_t* q;
   float* scale;
@@ -169,11 +170,14 @@ __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const Nor
     const float n = static_cast<float>(p.cols);
     const float sum = row_sum(squares(1.f), part[parity]);
     float r;
-    if (sum < INFINITY) {
+    if (sum >= p.low && sum < INFINITY) {
       r = __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), p.eps));
-    } else {  // squares past fp32 (or an infinity or a NaN): the row in units of 2^80
-      const float scaled = row_sum(squares(0x1p-80f), part[2]);
-      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(scaled, n), p.eps * 0x1p-80f * 0x1p-80f)) * 0x1p-80f;
+    } else {
+      // squares past fp32 (or an infinity or a NaN): the row in units of 2^80; squares that
+      // underflow beside an eps that is no normal number: in units of 2^-64
+      const float unit = sum < p.low ? 0x1p64f : 0x1p-80f;
+      const float scaled = row_sum(squares(unit), part[2]);
+      r = __frsqrt_rn(__fadd_rn(__fdiv_rn(scaled, n), p.eps * unit * unit)) * unit;
       __syncthreads();  // part[2] is free for the next such row
     }
 #pragma unroll
@@ -313,6 +317,8 @@ extern "C" int lmhead_rmsnorm_fp8(const uint16_t* x, const uint16_t* residual,
   p.cols = static_cast<int>(cols);
   p.kb = static_cast<int>((cols + kNBlock - 1) / kNBlock);
   p.eps = eps;
+  // a square's underflow is off by 2^-150: next to nothing beside any normal eps
+  p.low = eps < 0x1p-126f ? 0x1p-60f : 0.f;
   p.out_residual = out_residual;
   p.q = q;
   p.scale = scale;

@@ -10,9 +10,9 @@ import pytest
 
 import invariant_lm_head_gb300 as lmh
 import workloads as W
-from helpers import dev, to_dev
+from helpers import dev, to_dev, to_dev_bf16
 from oracle import serving as o
-from test_gpu_serving import LOWEST, check_logits, logit_rows, near, operands, same
+from test_gpu_serving import LOWEST, check_logits, f64, logit_rows, near, operands, same
 
 pytestmark = pytest.mark.gpu
 
@@ -20,6 +20,25 @@ pytestmark = pytest.mark.gpu
 @pytest.fixture(scope="module", autouse=True)
 def built():
     lmh.build()
+
+
+# ------------------------------------------------------------------ norm
+
+@pytest.mark.parametrize("eps", [1e-37, 1e-39, 1e-42, 2.0 ** -149])
+@pytest.mark.parametrize("cols", [272, 8000, 20000])
+def test_norm_with_an_eps_near_the_squares(cols, eps):
+    # squares at and below the smallest fp32 numbers, beside an eps that is no larger
+    x = W.random_bf16(3, (12, cols), 1.0)
+    size = np.float32([1e-19, 1e-20, 1e-21, 3e-22, 1e-22, 3e-23, 1e-23, 1e-24, 1e-26, 1.0, 1e-35, 0.0])
+    x = W.f32_to_bf16_bits(W.bf16_bits_to_f32(x) * size[:, None])
+    w = W.random_bf16(4, (1, cols), 1.0)[0]
+    q, s, _ = lmh.lmhead_rmsnorm_fp8(to_dev_bf16(x), to_dev_bf16(w), eps=eps)
+    eps = float(np.float32(eps))
+    rq, rs, _ = o.rmsnorm_fp8(W.bf16_bits_to_f32(x).astype(np.float64),
+                              W.bf16_bits_to_f32(w).astype(np.float64), None, eps)
+    assert (np.abs(f64(s) - rs) <= 32 * 2.0 ** -24 * rs).all()
+    usual = np.arange(12) != 10  # its products are below 2^-100 and take the rounded y
+    assert np.array_equal(f64(q)[usual], rq[usual])
 
 
 # ------------------------------------------------------------------ 4-bit logits
