@@ -12,7 +12,7 @@ import invariant_lm_head_gb300 as lmh
 import workloads as W
 from helpers import dev, to_dev, to_dev_bf16
 from oracle import serving as o
-from test_gpu_serving import LOWEST, check_logits, f64, logit_rows, near, operands, same
+from test_gpu_serving import LOWEST, check_logits, f64, logit_rows, near, norm_inputs, operands, same
 
 pytestmark = pytest.mark.gpu
 
@@ -39,6 +39,59 @@ def test_norm_with_an_eps_near_the_squares(cols, eps):
     assert (np.abs(f64(s) - rs) <= 32 * 2.0 ** -24 * rs).all()
     usual = np.arange(12) != 10  # its products are below 2^-100 and take the rounded y
     assert np.array_equal(f64(q)[usual], rq[usual])
+
+
+def check_rounded(q, quotient):
+    """q is the e4m3 value next to the quotient that the kernel has: off by half a step, by the
+    row's factor's 2^-19 and by the four roundings of y and of the block's largest y."""
+    _, e = np.frexp(np.abs(quotient))
+    half = np.ldexp(0.5, np.maximum(e - 1, -6) - 3)
+    assert (np.abs(q - quotient) <= half + (2.0 ** -19 + 2.0 ** -22) * np.abs(quotient)).all()
+
+
+@pytest.mark.parametrize("cols", [400, 4096, 8192, 16400])
+@pytest.mark.parametrize("scale", [1e-36, 5e-32, 1e-25, 1e-12])
+def test_norm_values_of_small_rows(scale, cols):
+    # rows of which every block is below the floor (1e-36), or above it with products too
+    # small to be exact (5e-32), or exact
+    eps = float(np.float32(1e-30))
+    x = W.random_bf16(11, (9, cols), 1.0)
+    x = W.f32_to_bf16_bits(W.bf16_bits_to_f32(x) * np.float32(scale))
+    w = norm_inputs(1, cols)[2]
+    q, s, _ = lmh.lmhead_rmsnorm_fp8(to_dev_bf16(x), to_dev_bf16(w), eps=eps)
+    xv, wv = (W.bf16_bits_to_f32(v).astype(np.float64) for v in (x, w))
+    rq, rs, _ = o.rmsnorm_fp8(xv, wv, None, eps)
+    assert (np.abs(f64(s) - rs) <= 32 * 2.0 ** -24 * rs).all()
+    if scale > 1e-30:
+        assert np.array_equal(f64(q), rq)
+    else:
+        y = xv * wv / np.sqrt((xv * xv).mean(1, keepdims=True) + eps)
+        check_rounded(f64(q), y / np.repeat(rs, 128, 1)[:, :cols])
+    assert (np.abs(f64(q)).max(1) >= 0.25).all()  # 1e-36: 1e-21 * 448 / 2^-60 is about a half
+
+
+@pytest.mark.parametrize("cols", [640, 4096, 8192, 20000])
+def test_norm_blocks_below_the_floor_beside_others(cols):
+    # blocks of ordinary size, below the floor with values that do not vanish there, and
+    # all zero, in the same warps
+    x = W.bf16_bits_to_f32(W.random_bf16(12, (20, cols), 1.0))
+    block = np.arange(cols) // 128
+    size = np.float32([1.0, 2.0 ** -62, 2.0 ** -66, 1.0, 0.0])
+    rows = np.arange(20)[:, None]
+    x = W.f32_to_bf16_bits(x * size[(block[None] + rows) % 5])
+    w = norm_inputs(1, cols)[2]
+    q, s, _ = lmh.lmhead_rmsnorm_fp8(to_dev_bf16(x), to_dev_bf16(w))
+    xv, wv = (W.bf16_bits_to_f32(v).astype(np.float64) for v in (x, w))
+    rq, rs, _ = o.rmsnorm_fp8(xv, wv, None, float(np.float32(1e-6)))
+    assert (np.abs(f64(s) - rs) <= 32 * 2.0 ** -24 * rs).all()
+    q, kind = f64(q), (block[None] + rows) % 5
+    ordinary = (kind == 0) | (kind == 3)
+    assert np.array_equal(q[ordinary], rq[ordinary])
+    y = xv * wv / np.sqrt((xv * xv).mean(1, keepdims=True) + float(np.float32(1e-6)))
+    check_rounded(q, y / np.repeat(rs, 128, 1)[:, :cols])
+    for k in (1, 2):
+        assert (q[kind == k] != 0).any()
+    assert (q[kind == 4] == 0).all()
 
 
 # ------------------------------------------------------------------ 4-bit logits
