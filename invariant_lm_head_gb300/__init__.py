@@ -727,13 +727,14 @@ def lmhead_rmsnorm_fp8(x, weight, residual=None, *, eps: float = 1e-6, out=None,
     out_residual may be residual or x itself; want_residual=False leaves the sum out.
     """
     torch = _torch()
-    bf16, dev, size, index = torch.bfloat16, x.device, x.shape, x.get_device()
+    tensor, bf16, dev, size, index = torch.Tensor, torch.bfloat16, x.device, x.shape, x.get_device()
     if (stream is None and out is None and out_scale is None and out_residual is None
             and index >= 0 and x.dtype is bf16 and len(size) == 2 and x.is_contiguous()
-            and weight.dtype is bf16 and weight.shape == size[1:] and weight.is_contiguous()
-            and weight.get_device() == index
-            and (residual is None or residual.dtype is bf16 and residual.shape == size
-                 and residual.is_contiguous() and residual.get_device() == index)
+            and isinstance(weight, tensor) and weight.dtype is bf16 and weight.shape == size[1:]
+            and weight.is_contiguous() and weight.get_device() == index
+            and (residual is None or isinstance(residual, tensor) and residual.dtype is bf16
+                 and residual.shape == size and residual.is_contiguous()
+                 and residual.get_device() == index)
             and torch.cuda.current_device() == index):
         rows, ld = size
         cols = ld_res = ld_out = ld
@@ -812,7 +813,8 @@ def lmhead_dequantize_mxfp4(q, scale, *, out=None, stream=None):
     torch = _torch()
     u8, dev, size, index = torch.uint8, q.device, q.shape, q.get_device()
     if (stream is None and out is None and index >= 0 and q.dtype is u8 and len(size) == 2
-            and q.is_contiguous() and scale.dtype is u8 and scale.get_device() == index
+            and q.is_contiguous() and isinstance(scale, torch.Tensor) and scale.dtype is u8
+            and scale.get_device() == index
             and scale.shape == _mxfp4_scale_shape(size[0], 2 * size[1]) and scale.is_contiguous()
             and torch.cuda.current_device() == index):
         rows, cols = size[0], 2 * size[1]
@@ -843,26 +845,27 @@ def lmhead_logits_mxfp4(hidden_q, hidden_scale, weight_q, weight_scale, *, out_l
     as lmhead_quantize_mxfp4 returns them. out_logits may have strided rows.
     """
     torch = _torch()
-    u8, dev, index = torch.uint8, hidden_q.device, hidden_q.get_device()
-    size, weight_size = hidden_q.shape, weight_q.shape
+    tensor, u8, dev, index = torch.Tensor, torch.uint8, hidden_q.device, hidden_q.get_device()
+    size = hidden_q.shape
     if (stream is None and out_logits is None and index >= 0 and hidden_q.dtype is u8
-            and len(size) == 2 and hidden_q.is_contiguous() and weight_q.dtype is u8
-            and len(weight_size) == 2 and weight_size[1] == size[1] and weight_q.is_contiguous()
-            and weight_q.get_device() == index and hidden_scale.dtype is u8
+            and len(size) == 2 and hidden_q.is_contiguous() and isinstance(weight_q, tensor)
+            and weight_q.dtype is u8 and weight_q.dim() == 2 and weight_q.shape[1] == size[1]
+            and weight_q.is_contiguous() and weight_q.get_device() == index
+            and isinstance(hidden_scale, tensor) and hidden_scale.dtype is u8
             and hidden_scale.shape == _mxfp4_scale_shape(size[0], 2 * size[1])
             and hidden_scale.is_contiguous() and hidden_scale.get_device() == index
-            and weight_scale.dtype is u8
-            and weight_scale.shape == _mxfp4_scale_shape(weight_size[0], 2 * size[1])
+            and isinstance(weight_scale, tensor) and weight_scale.dtype is u8
+            and weight_scale.shape == _mxfp4_scale_shape(weight_q.shape[0], 2 * size[1])
             and weight_scale.is_contiguous() and weight_scale.get_device() == index
             and torch.cuda.current_device() == index):
-        T, V, H = size[0], weight_size[0], 2 * size[1]
+        T, V, H = size[0], weight_q.shape[0], 2 * size[1]
         ld = V
         st, empty = torch._C._cuda_getCurrentRawStream(index), torch.empty
     else:
         _need(hidden_q, "hidden_q", u8, dev, 2)
         _need(weight_q, "weight_q", u8, dev, 2)
-        T, V, H = size[0], weight_size[0], 2 * size[1]
-        if weight_size[1] != size[1]:
+        T, V, H = size[0], weight_q.shape[0], 2 * size[1]
+        if weight_q.shape[1] != size[1]:
             raise ValueError("shape mismatch between hidden_q and weight_q")
         _need_out(hidden_scale, "hidden_scale", u8, dev, _mxfp4_scale_shape(T, H))
         _need_out(weight_scale, "weight_scale", u8, dev, _mxfp4_scale_shape(V, H))
@@ -899,9 +902,9 @@ def lmhead_top_logprobs(logits, tokens=None, temperature=1.0, *, top: int = 20, 
     if (stream is None and out_logprob is None and out_entropy is None and out_top_token is None
             and out_top_logprob is None and index >= 0 and logits.dtype is torch.bfloat16
             and len(size) == 2 and logits.is_contiguous()
-            and (tokens is None or tokens.dtype is i32 and 1 <= tokens.dim() <= 2
-                 and tokens.shape[0] == size[0] and tokens.is_contiguous()
-                 and tokens.get_device() == index)
+            and (tokens is None or isinstance(tokens, torch.Tensor) and tokens.dtype is i32
+                 and 1 <= tokens.dim() <= 2 and tokens.shape[0] == size[0]
+                 and tokens.is_contiguous() and tokens.get_device() == index)
             and (not per_row or temperature.dtype is f32 and temperature.shape == size[:1]
                  and temperature.is_contiguous() and temperature.get_device() == index)
             and torch.cuda.current_device() == index):
@@ -913,7 +916,9 @@ def lmhead_top_logprobs(logits, tokens=None, temperature=1.0, *, top: int = 20, 
         ld = _need_rows(logits, "logits", torch.bfloat16, dev)
         T, V = size
         if tokens is not None:
-            if not isinstance(tokens, torch.Tensor) or tokens.dim() not in (1, 2):
+            if not isinstance(tokens, torch.Tensor):
+                raise TypeError("tokens must be a torch.Tensor")
+            if tokens.dim() not in (1, 2):
                 raise ValueError("tokens must be a 1-D or 2-D tensor")
             _need(tokens, "tokens", i32, dev, tokens.dim())
             if tokens.shape[0] != T:
