@@ -13,6 +13,10 @@ head takes the last layer's output and the residual stream:
 
     head = FP8Head(weight, norm_weight, norm_eps=1e-6)
     token, logprob = head.sample(hidden, uniform, residual=residual)
+    head.refresh(weight, norm_weight)           # after a training step
+
+The norm's weight is not quantised, and so not copied: the head reads the tensor that it
+was given, and writes a refresh's norm_weight into it.
 
 Every call runs on the current stream and can be captured into a CUDA graph
 (after a first call outside of one). The head holds one byte per weight
@@ -41,9 +45,20 @@ class FP8Head(QuantizedHead):
     def hidden_size(self) -> int:
         return self.weight_q.shape[1]
 
-    def refresh(self, weight) -> None:
-        """Quantise a new weight of the same shape in place (graphs stay valid)."""
+    def refresh(self, weight, norm_weight=None) -> None:
+        """Quantise a new weight of the same shape in place (graphs stay valid).
+
+        norm_weight: the norm's new weight, written into the tensor that the head holds;
+        without one that tensor stays as it is.
+        """
+        held = self.norm_weight
+        if norm_weight is not None:
+            if held is None:
+                raise ValueError("norm_weight needs a head with a norm")
+            lmh._need_out(norm_weight, "norm_weight", held.dtype, held.device, tuple(held.shape))
         lmh.lmhead_quantize_fp8(weight, 128, out=self.weight_q, out_scale=self.weight_scale)
+        if norm_weight is not None:
+            held.detach().copy_(norm_weight.detach())
 
     def logits(self, hidden, *, residual=None, out_logits=None):
         """bf16 logits [T, V] of hidden bf16 [T, H] (rows may be strided).

@@ -12,7 +12,8 @@ import invariant_lm_head_gb300 as lmh
 import workloads as W
 from helpers import dev, to_dev, to_dev_bf16
 from oracle import serving as o
-from test_gpu_serving import LOWEST, check_logits, f64, logit_rows, near, norm_inputs, operands, same
+from test_gpu_serving import (LOWEST, check_logits, f64, logit_rows, near, norm_inputs, operands,
+                              same, step_inputs)
 
 pytestmark = pytest.mark.gpu
 
@@ -255,3 +256,39 @@ def test_top_launches_no_idle_half(T, V):
     slices = -(-vectors // max(1024, -(-(-(-vectors // 4)) // 32) * 32))
     assert ctas == 1 or 2 * -(-slices * ctas // 4) > ctas
     same(lmh.lmhead_top_logprobs(lg[T - 1:], top=5)[1:], [v[T - 1:] for v in got])
+
+
+# ------------------------------------------------------------------ heads
+
+def test_fp8_head_takes_over_a_new_norm():
+    # in a captured graph too; a trainer's parameter as the norm's weight, and updates in place
+    import torch
+
+    from invariant_lm_head_gb300.fp8_head import FP8Head
+
+    h, r, w, g = step_inputs()
+    w2, g2 = w.flip(0).contiguous(), (g.float() * 1.5 + 0.25).to(torch.bfloat16)
+    norm = torch.nn.Parameter(g.clone())
+    head = FP8Head(w, norm, 1e-5)
+    at = norm.data_ptr()
+    head.logits(h, residual=r)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = head.logits(h, residual=r)
+
+    def expect(weight, norm_weight):
+        want = FP8Head(weight, norm_weight, 1e-5).logits(h, residual=r)
+        graph.replay()
+        assert torch.equal(head.logits(h, residual=r), want) and torch.equal(out, want)
+
+    expect(w, g)
+    head.refresh(w2, torch.nn.Parameter(g2))
+    assert head.norm_weight.data_ptr() == at
+    expect(w2, g2)
+    head.refresh(w)  # the norm's stays
+    expect(w, g2)
+    with torch.no_grad():
+        norm.copy_(g)  # the tensor that the head holds
+    expect(w, g)
+    head.refresh(w2, norm)
+    expect(w2, g)

@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import invariant_lm_head_gb300 as lmh
+from invariant_lm_head_gb300.fp8_head import FP8Head
 from test_serving_host import Here, lib  # noqa: F401  (a fixture)
 
 
@@ -33,3 +34,17 @@ def test_what_is_no_tensor_is_a_type_error(kind, lib, monkeypatch):  # noqa: F81
     with pytest.raises(TypeError, match="must be a torch.Tensor"):
         lmh.lmhead_rmsnorm_fp8(x, None)
     assert lib.lmhead_kernel_launches() == before
+
+
+def test_refresh_refuses_another_norm_before_it_writes():
+    w, g = torch.zeros(1000, 256, dtype=torch.bfloat16), torch.ones(256, dtype=torch.bfloat16)
+    head = FP8Head.__new__(FP8Head)
+    head.norm_weight = None
+    with pytest.raises(ValueError, match="needs a head with a norm"):
+        head.refresh(w, g)
+    head.norm_weight = g.clone()
+    for bad, error in ((g[:128], ValueError), (g[:1], ValueError), (g.float(), TypeError),
+                       ([1.0] * 256, TypeError), (g.view(1, 256), ValueError)):
+        with pytest.raises(error, match="norm_weight"):
+            head.refresh(w, bad)
+    assert torch.equal(head.norm_weight, g)
