@@ -526,7 +526,8 @@ int lmhead_sample(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logit
  * a = max(max |y|, 2^-60):
  *   scale = a / 448,   q = y * 448 / a, rounded to e4m3 once (nearest, ties to even)
  * h is not rounded again and y not at all: a block of ordinary size has the q that exact
- * arithmetic gives, and its scale 24 bits. A row that holds an infinity or a NaN has
+ * arithmetic gives, and its scale is within 2^-19 (2^-22 in practice: the rounding of the
+ * row's sum, in fp32). A row that holds an infinity or a NaN has
  * the values that the formula gives in fp32 (a block with a NaN gets it as its scale and
  * NaN in every q).
  *   x             bf16 [rows, cols], 16-byte aligned, rows ld_x apart (>= cols, a
@@ -607,7 +608,7 @@ int lmhead_logits_mxfp4(const uint8_t* hidden_q, const uint8_t* hidden_scale,
  *                row whose temperature is negative or not finite gets token -1 and NaN
  *   tokens       int32 [T, n_tokens], n_tokens >= 0
  *   n_top        0 to 128; it may exceed V
- *   out_entropy  f32 [T] or NULL
+ *   out_entropy  f32 [T] or NULL (which leaves out the write, not the sum)
  * T == 0 is a no-op.
  */
 int lmhead_top_logprobs(const uint16_t* logits, int64_t T, int64_t V, int64_t ld_logits,

@@ -892,6 +892,7 @@ def lmhead_top_logprobs(logits, tokens=None, temperature=1.0, *, top: int = 20, 
     temperature a number or f32 [T] (0 counts as 1), top the number of alternatives (0
     to 128). Returns (logprob f32, shaped as tokens, or None; entropy f32 [T] or None;
     top_token int32 [T, top]; top_logprob f32 [T, top]); see include/lmhead.h for masks.
+    want_entropy=False saves the output, not the time.
     """
     torch = _torch()
     f32, i32, dev = torch.float32, torch.int32, logits.device

@@ -7,7 +7,7 @@
 // before it. Behind any other kind of work in the stream, and behind a kernel that says
 // nothing, such a launch is an ordinary one. A CTA says it late: said at its start, the
 // CTAs behind crowd onto the SMs that have room first (256 rows of V=152064 in
-// lmhead_top_logprobs, back to back: 33 us for 24).
+// lmhead_top_logprobs, back to back: 33 us for 25.5).
 // (4-bit logits back to back: T=64 H=4096 V=32000 17.0 -> 15.3 us, T=200 H=3616 V=32003
 // 26.7 -> 23.9, T=1 H=3584 V=152064 48.4 -> 46.7.)
 #pragma once

@@ -314,15 +314,19 @@ __device__ __forceinline__ void store_box(uint16_t* row, int col, int n, const u
 // both), the others turn finished tiles to bf16. Tokens are the MMA's rows, the
 // vocabulary its columns.
 //
-// What bounds it. A short batch reads the weight once: 45 us at T=1 H=3584 V=152064, 6.4
-// TB/s, 0.95 of the copy rate; 14.8 us at T=64 H=4096 V=32000, where first loads and the
+// What bounds it. A short batch reads the weight once: 46 us at T=1 H=3584 V=152064, 6.3
+// TB/s, 0.94 of the copy rate; 14.8 us at T=64 H=4096 V=32000, where first loads and the
 // single wave's end take 5 us beside 10 of bytes. A long batch takes 314 us at T=2048
-// H=3584 V=152064 (7.1 PFLOP/s; 330, 6.8, in a loop that runs into the power cap): MMAs
+// H=3584 V=152064 (7.1 PFLOP/s; 360, 6.2, in a loop that runs into the power cap): MMAs
 // and scale copies alone take 259, with the loads 272 (17.5 TB/s out of L2, near what it
 // gives), and the stores, which share L2 and HBM with the loads, the rest. Of the 259 us
 // 218 are MMAs at their rate (128 cycles for 256 x 256 x 64 of a pair) and the others the
 // gap between two tiles, about 1000 cycles: the accumulators share columns, and the next
 // tile's MMAs wait until those are read.
+// In between: T=200 V=32000 takes 19.0 us at H=3584 (two waves of pairs, the second of 50 of
+// 76), 22.1 at H=3616: where H / 32 is odd, rows of q start between two 32-byte sectors of
+// L2 (T=300 24.2 us at H=3840, 33.8 at 3616). Rows of V=32003 one behind the other take
+// 1.3 us more than on 16 bytes.
 // Tried and slower at T=2048: eight warps for the finished tiles (349 us), groups of 4
 // and 2 row blocks in the raster (340, 365), boxes of shared memory and TMA stores for
 // the output (as fast there, 18.1 us at T=64).
@@ -698,9 +702,12 @@ bool misaligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t
 
 // Whether n_m row blocks of 128 go to pairs of CTAs. A wave of CTAs alone takes 1.15 to
 // 1.4 times a wave of pairs (at one and two row blocks they are the same), so an odd
-// last block, which leaves half of a pair idle, can make the pairs slower. H=3584,
-// V=152064 / 32000 (us, alone / pairs): 384 rows 86 / 94 and 26.4 / 31.4, 640 rows 132 /
-// 136 and 37 / 35, 1152 rows 218 / 202, 2048 rows 438 / 314; 200 rows 65 / 63.
+// last block, which leaves half of a pair idle, can make the pairs slower. H=3584 (us for a
+// few calls, alone / pairs): V=152064 200 rows 64 / 60, 384 rows 85 / 90, 512 rows 108 / 96,
+// 640 rows 129 / 125, 768 rows 152 / 131, 896 rows 175 / 165, 1152 rows 219 / 198, 2048
+// rows 438 / 314; V=32000 384 rows 25.2 / 27.5, 640 rows 36.7 / 32.2. At the power cap
+// pairs are the hotter: 640 rows of V=152064, a tie of the rule's, 136 / 141 in a loop, 896
+// rows 185 / 184.
 bool mxfp4_pairs(int64_t n_m, int64_t n_n, int sms, int pairs) {
   if (n_m < 2 || pairs < 1) return false;
   const int64_t alone = (n_m * n_n + sms - 1) / sms;

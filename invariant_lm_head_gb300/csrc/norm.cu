@@ -76,11 +76,13 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 // the CTA's next kD - 1 rows to shared memory while it works on one (no barrier: no
 // other thread reads it), since the barrier of the row's sum would leave the memory idle.
 //
-// What bounds it: HBM. 92 us at 16384 x 5120 with a residual (7 bytes an element), 6.4
-// TB/s, 0.95 of the copy rate (97 where nothing is launched behind it); loads into
+// What bounds it: HBM. 90 us at 16384 x 5120 with a residual (7 bytes an element), 6.5
+// TB/s, 0.97 of the copy rate (94 to 97 where nothing is launched behind it); loads into
 // registers at each row's start 104 us, the same with 16 elements a thread and 320
 // threads 119. The grid is what the SMs hold at once: one CTA an SM more 117 us. One row
-// of 4096 takes 4.3 us, a load, a sum and a store one after the other.
+// of 4096 takes 4.3 us, a load, a sum and a store one after the other. Past 16384 columns
+// a row fills the shared memory (kD = 1: none ahead) and 64 elements a thread spill: 4096 x
+// 20000 158 us, 3.6 TB/s, 2048 x 32768 100 us, 4.7 TB/s; 4096 x 16384 70 us, 6.7.
 template <int kU, int kD>
 __global__ void __launch_bounds__(kU == 1 ? 256 : 512) norm_fp8_kernel(const NormParams p) {
   extern __shared__ __align__(16) uint8_t ahead[];

@@ -16,8 +16,10 @@
 // at again. The tokens found there, n and a few more, are ranked by counting. Where
 // more tokens reach it than the list holds (equal logits, a mask of the type's lowest
 // value), the n-th largest value is found by bisection over the 16-bit keys, counting over
-// the row; first it is tried itself, which it mostly is (1024 such rows of 152064 take
-// 114 us, and 2560 without that trial and four vectors at a time).
+// the row; first it is tried itself, which it mostly is (1024 rows of 152064 equal logits
+// take 116 us, and 2560 without that trial and four vectors at a time). The row is then
+// listed from its start until the n are found: a lowest-value mask that leaves fewer than n
+// tokens, spread over the row, takes 600 us.
 //
 // A row is four slices, and every thread of a CTA has its share of each. A cluster of 1
 // to 4 CTAs takes the row, as many as a short batch leaves SMs for; a thread's sums are
@@ -26,10 +28,14 @@
 //
 // Batch invariance: the slices and the order of every sum depend on V alone.
 //
-// What bounds it. Many rows: the issue of instructions (47000 a row of 152064 in warps,
-// 65 % of the slots) beside HBM: 64 us for 1024 rows, 4.8 TB/s, 0.72 of the copy rate;
-// 1024 rows are 1.7 times what the SMs hold at four CTAs each, and the second wave does
-// not fill them. Few rows: a chain of short steps, 9.0 us at one row of 152064 on four
+// What bounds it. Many rows: the issue of instructions (49000 a row of 152064 in warps,
+// 64 % of the slots) beside HBM: 64 to 67 us for 1024 rows, 4.6 to 4.9 TB/s, 0.69 to 0.73
+// of the copy rate; 1024 rows are 1.7 times what the SMs hold at four CTAs each, and the
+// second wave does not fill them. With 90 % of the logits -inf, which sends every group's
+// sums to cut_sums, 91 us. Rows off 16 bytes: a ring of twice the size, three CTAs an SM,
+// 92 us at V=152061. Middle batches and vocabularies: some 6 us a wave of rows for the
+// n-th key, the second look, the ranking and the sums, while nothing is being read (1024
+// rows of 8000 15 us, of 32000 23.5; 256 rows of 32000 11.4, of 152064 25.5). Few rows: a chain of short steps, 9.0 us at one row of 152064 on four
 // CTAs (9000 cycles to read and fold, 1700 to bisect the keys, 3000 for the second look,
 // 1100 for the cluster, 3500 for sums and lists, the kernel behind under way meanwhile).
 // Tried and slower at 1024 rows of 152064 (64 us then): 512 threads a CTA (119), 384 (78),
